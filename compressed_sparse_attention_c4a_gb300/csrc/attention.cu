@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "rows.cuh"
 #include "topk_cluster.cuh"
 
 namespace dsa {
@@ -254,10 +255,13 @@ __device__ __forceinline__ uint32_t sw128_offset(int r, int e, int chunk_stride)
 // Keys of a row for the tensor-core kernel: [0, n_comp) compressed slots, [n_comp, ncp) padding up to a
 // multiple of 4, [ncp, ncp + window count) window positions.
 
-template <int NH, bool FP8, bool FUSED>
+template <int NH, int DT, bool FUSED>
 __global__ void __launch_bounds__(kClThreads, 1)
     attn_cl_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap, AttnArgs a) {
     using L = ClSmem<NH>;
+    constexpr bool FP8 = DT != DSA_BF16;     // rows of codes, widened to bf16 on the way, with a scale per row
+    constexpr bool FP4 = DT == DSA_FP4_BLOCK;
+    constexpr int kRawRow = FP4 ? kFp4BlockRow : kD;  // bytes of a stored row of codes
     using Ro = ClRoles<FP8 ? 4 : 2>;
     // bf16 key stages: four for bf16 rows; three for e4m3 rows, whose codes land in a ring of two raw slots
     // (16 KB each, the fourth stage's space) and are widened into a stage once its previous product is done
@@ -504,9 +508,22 @@ __global__ void __launch_bounds__(kClThreads, 1)
             for (int u = 0; u < kRowsPerWarp; ++u) {
                 const int kk = gw + u * Ro::kGatherWarps;
                 if (ok && kk < kClKeys) {
+                    uint32_t bf[8];
+                    if constexpr (FP4) {
+                        const uint8_t* rw = raw + kk * kRawRow;
+                        const uint2 code = *reinterpret_cast<const uint2*>(rw + lane * 8);
+                        const __half_raw sh = __nv_cvt_fp8_to_halfraw(rw[kD / 2 + lane], __NV_E4M3);
+                        const __half2 s2 = __half2half2(*reinterpret_cast<const __half*>(&sh));
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const __half2_raw h2 =
+                                __nv_cvt_fp4x2_to_halfraw2((uint8_t)((q < 4 ? code.x : code.y) >> (8 * (q & 3))), __NV_E2M1);
+                            const float2 f2 = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h2), s2));
+                            bf[q] = pack_bf16(f2.x, f2.y);
+                        }
+                    } else {
                     const uint4 code = *reinterpret_cast<const uint4*>(raw + kk * kD + lane * 16);
                     const uint32_t w4[4] = {code.x, code.y, code.z, code.w};
-                    uint32_t bf[8];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
 #pragma unroll
@@ -516,6 +533,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
                             const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&h2));
                             bf[2 * q + hlf] = pack_bf16(f2.x, f2.y);
                         }
+                    }
                     }
                     const int d0 = 16 * lane;
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + sw128_offset(kk, d0, kClKeys * 128)),
@@ -627,8 +645,11 @@ __global__ void __launch_bounds__(kClThreads, 1)
                         if (kk < kClKeys) {
                             const int rr = rows[kk];
                             const dsa_pool_t& pl = pools[kk] == 2 ? a.swa : a.main;
-                            const uint8_t* src = static_cast<const uint8_t*>(pl.data) + (rr >= 0 ? (long long)rr * kD : 0);
-                            cp_async16_hint(raw + kk * kD + lane * 16, src + lane * 16, rr >= 0 ? 16u : 0u, row_policy);
+                            const uint8_t* src =
+                                static_cast<const uint8_t*>(pl.data) + (rr >= 0 ? (long long)rr * kRawRow : 0);
+                            if (lane < kRawRow / 16)
+                                cp_async16_hint(raw + kk * kRawRow + lane * 16, src + lane * 16, rr >= 0 ? 16u : 0u,
+                                                row_policy);
                             if (lane == 0)
                                 cp_async4(smem_u32(ksc + kk), rr >= 0 ? pl.scale + rr : pl.scale, rr >= 0 ? 4u : 0u);
                         }
@@ -1225,7 +1246,7 @@ static bool make_out_map(CUtensorMap* map, void* base, uint64_t rows, int box_ro
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NH, bool FP8, bool FUSED = false>
+template <int NH, int DT, bool FUSED = false>
 static dsa_status_t launch_attn_cl(const AttnArgs& a, int cl, cudaStream_t st) {
     using L = ClSmem<NH>;
     CUtensorMap qmap, omap;
@@ -1233,16 +1254,25 @@ static dsa_status_t launch_attn_cl(const AttnArgs& a, int cl, cudaStream_t st) {
     if (!make_out_map(&omap, a.out8 ? static_cast<void*>(a.out8) : static_cast<void*>(a.out), (uint64_t)a.rows * a.heads,
                       NH, a.out8 != nullptr))
         return DSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(attn_cl_kernel<NH, FP8, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) !=
+    if (cudaFuncSetAttribute(attn_cl_kernel<NH, DT, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) !=
         cudaSuccess)
         return DSA_ERR_CUDA;
     const long long grid = (long long)a.rows * a.hg_count * a.nsplit * cl;
-    cudaError_t e = launch_pdl_cluster(attn_cl_kernel<NH, FP8, FUSED>, dim3((unsigned)grid), dim3(kClThreads), L::kAlloc, st, cl,
+    cudaError_t e = launch_pdl_cluster(attn_cl_kernel<NH, DT, FUSED>, dim3((unsigned)grid), dim3(kClThreads), L::kAlloc, st, cl,
                                        qmap, omap, a);
     if (e == cudaSuccess && a.nsplit > 1)
         e = launch_pdl(attn_combine_kernel, dim3(a.rows * a.heads), dim3(128), 0, st, a);
     if (e != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();
+}
+
+template <int DT>
+static dsa_status_t launch_attn_heads(const AttnArgs& a, const SplitPlan& p, cudaStream_t st) {
+    switch (p.hg) {
+        case 16: return launch_attn_cl<16, DT>(a, p.cl, st);
+        case 32: return launch_attn_cl<32, DT>(a, p.cl, st);
+        default: return launch_attn_cl<64, DT>(a, p.cl, st);
+    }
 }
 
 // The indexer scores a fused call selects from (the kernel's top-k phase), and whether a plan allows it: one
@@ -1322,7 +1352,6 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
 
     a.status = dev_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool fp8 = main->dtype == DSA_FP8_E4M3;
     if (fz) {  // topk is the output of the kernel's own top-k phase
         if (!fusable(p, heads, fz->ld, k)) return DSA_ERR_UNSUPPORTED;
         a.topk = nullptr;
@@ -1330,19 +1359,16 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
         a.scores = fz->scores;
         a.score_ld = fz->ld;
         a.n_valid = fz->n_valid;
-        return fp8 ? launch_attn_cl<64, true, true>(a, p.cl, st) : launch_attn_cl<64, false, true>(a, p.cl, st);
-    }
-    if (!fp8) {
-        switch (p.hg) {
-            case 16: return launch_attn_cl<16, false>(a, p.cl, st);
-            case 32: return launch_attn_cl<32, false>(a, p.cl, st);
-            default: return launch_attn_cl<64, false>(a, p.cl, st);
+        switch (main->dtype) {
+            case DSA_BF16: return launch_attn_cl<64, DSA_BF16, true>(a, p.cl, st);
+            case DSA_FP8_E4M3: return launch_attn_cl<64, DSA_FP8_E4M3, true>(a, p.cl, st);
+            default: return launch_attn_cl<64, DSA_FP4_BLOCK, true>(a, p.cl, st);
         }
     }
-    switch (p.hg) {
-        case 16: return launch_attn_cl<16, true>(a, p.cl, st);
-        case 32: return launch_attn_cl<32, true>(a, p.cl, st);
-        default: return launch_attn_cl<64, true>(a, p.cl, st);
+    switch (main->dtype) {
+        case DSA_BF16: return launch_attn_heads<DSA_BF16>(a, p, st);
+        case DSA_FP8_E4M3: return launch_attn_heads<DSA_FP8_E4M3>(a, p, st);
+        default: return launch_attn_heads<DSA_FP4_BLOCK>(a, p, st);
     }
 }
 
@@ -1361,7 +1387,7 @@ extern "C" size_t dsa_attn_workspace_size(int32_t nq, int32_t heads, int32_t max
 extern "C" dsa_status_t dsa_attn_plan(int32_t nq, int32_t heads, int32_t max_keys, int32_t dtype, int32_t* plan) {
     if (!plan || nq <= 0 || max_keys <= 0) return DSA_ERR_INVALID_ARG;
     if (dtype == DSA_FP4_E2M1) return DSA_ERR_UNSUPPORTED;  // e2m1 holds indexer keys only
-    if (dtype != DSA_BF16 && dtype != DSA_FP8_E4M3) return DSA_ERR_INVALID_ARG;
+    if (dtype != DSA_BF16 && dtype != DSA_FP8_E4M3 && dtype != DSA_FP4_BLOCK) return DSA_ERR_INVALID_ARG;
     if (heads != 16 && heads != 32 && heads != 64 && heads != 128) return DSA_ERR_UNSUPPORTED;
     const SplitPlan p = plan_for(nq, heads, max_keys, dtype);
     plan[0] = p.hg;

@@ -17,6 +17,7 @@
 namespace dsa {
 
 constexpr int kBlockPositions = 256;  // raw positions per logical block, every cache kind
+constexpr int kFp4Block = 16;         // elements that share a scale in a DSA_FP4_BLOCK row
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 // -------------------------------------------------------------------------------------
@@ -99,7 +100,8 @@ inline int sm_count() {
 
 inline bool pool_ok(const dsa_pool_t* p) {
     if (!p || !p->data || p->num_blocks <= 0 || p->rows_per_block <= 0 || p->dim <= 0) return false;
-    if (p->dtype != DSA_BF16 && p->dtype != DSA_FP8_E4M3 && p->dtype != DSA_FP4_E2M1) return false;
+    if (p->dtype != DSA_BF16 && p->dtype != DSA_FP8_E4M3 && p->dtype != DSA_FP4_E2M1 && p->dtype != DSA_FP4_BLOCK)
+        return false;
     if (p->dtype != DSA_BF16 && (!p->scale || !aligned(p->scale, 16))) return false;
     if (p->dtype == DSA_FP4_E2M1 && (p->dim % 64 || !aligned(p->data, 32))) return false;
     return aligned(p->data, 16);
@@ -107,7 +109,12 @@ inline bool pool_ok(const dsa_pool_t* p) {
 
 // Bytes of one pool row.
 inline long long row_bytes_of(const dsa_pool_t* p) {
-    return p->dtype == DSA_BF16 ? 2ll * p->dim : (p->dtype == DSA_FP8_E4M3 ? p->dim : p->dim / 2);
+    switch (p->dtype) {
+        case DSA_BF16: return 2ll * p->dim;
+        case DSA_FP8_E4M3: return p->dim;
+        case DSA_FP4_BLOCK: return p->dim / 2 + p->dim / kFp4Block;  // codes, then one e4m3 scale per block
+        default: return p->dim / 2;
+    }
 }
 
 inline bool table_ok(const dsa_block_table_t* t, int batch) {

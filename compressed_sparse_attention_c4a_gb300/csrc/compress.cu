@@ -11,9 +11,9 @@
 // DIM/32 consecutive elements, so every row load and store is one coalesced transaction set.
 // Raw tokens of an entry that are shared with its neighbour (c4a overlap) are re-read from L2.
 #include "common.cuh"
+#include "rows.cuh"
 
 namespace dsa {
-
 
 struct CompressArgs {
     int w, s, batch, dim;
@@ -41,32 +41,6 @@ struct CompressArgs {
     int req_items;    // warps per request: entry_items * nsub + token_items, rounded up to whole CTAs
     int32_t* status;
 };
-
-template <int E>
-__device__ __forceinline__ void load_bf16(const uint16_t* row, int lane, float (&v)[E]) {
-    const uint16_t* p = row + lane * E;
-    if constexpr (E == 16) {
-        uint4 a = *reinterpret_cast<const uint4*>(p);
-        uint4 b = *reinterpret_cast<const uint4*>(p + 8);
-        uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[2 * k] = __uint_as_float(u[k] << 16);
-            v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-        }
-    } else if constexpr (E == 4) {
-        uint2 a = *reinterpret_cast<const uint2*>(p);
-        v[0] = __uint_as_float(a.x << 16);
-        v[1] = __uint_as_float(a.x & 0xffff0000u);
-        v[2] = __uint_as_float(a.y << 16);
-        v[3] = __uint_as_float(a.y & 0xffff0000u);
-    } else {
-        static_assert(E == 2, "row width");
-        uint32_t a = *reinterpret_cast<const uint32_t*>(p);
-        v[0] = __uint_as_float(a << 16);
-        v[1] = __uint_as_float(a & 0xffff0000u);
-    }
-}
 
 template <int E>
 __device__ __forceinline__ void copy_bf16(uint16_t* dst, const uint16_t* src, int lane) {
@@ -106,63 +80,6 @@ __device__ __forceinline__ void copy_f32(float* dst, const float* src, int lane)
             *reinterpret_cast<float4*>(dst + lane * E + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
     } else {
         *reinterpret_cast<float2*>(dst + lane * E) = make_float2(v[0], v[1]);
-    }
-}
-
-// Store one row (the warp's E values per lane) into a pool row: bf16, e4m3 + amax/448 scale, or e2m1 + amax/6.
-template <int E>
-__device__ __forceinline__ void store_row(const dsa_pool_t& pool, long long prow, int lane, const float (&v)[E]) {
-    if (pool.dtype == DSA_BF16) {
-        uint16_t* dst = reinterpret_cast<uint16_t*>(pool.data) + prow * (E * 32) + lane * E;
-        uint32_t u[E / 2];
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k)
-            u[k] = (uint32_t)float_to_bf16(v[2 * k]) | ((uint32_t)float_to_bf16(v[2 * k + 1]) << 16);
-        if constexpr (E == 16) {
-            reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-            reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-        } else if constexpr (E == 4) {
-            *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
-        } else {
-            *reinterpret_cast<uint32_t*>(dst) = u[0];
-        }
-    } else if (pool.dtype == DSA_FP4_E2M1) {  // e2m1 codes, two per byte, scale amax / 6
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < E; ++k) amax = fmaxf(amax, fabsf(v[k]));
-        amax = warp_max(amax);
-        const float scale = amax > 0.f ? amax / 6.f : 1.f;
-        uint8_t* dst = reinterpret_cast<uint8_t*>(pool.data) + prow * (E * 16) + lane * (E / 2);
-        uint32_t c[(E / 2 + 3) / 4] = {};  // the lane's E/2 code bytes, little-endian in words
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k)
-            c[k / 4] |= (uint32_t)float2_to_e2m1x2(v[2 * k] / scale, v[2 * k + 1] / scale) << (8 * (k % 4));
-        if constexpr (E == 16) {
-            *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
-        } else if constexpr (E == 4) {
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)c[0];
-        } else {
-            *dst = (uint8_t)c[0];
-        }
-        if (lane == 0) pool.scale[prow] = scale;
-    } else {
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < E; ++k) amax = fmaxf(amax, fabsf(v[k]));
-        amax = warp_max(amax);
-        const float scale = amax > 0.f ? amax / 448.f : 1.f;
-        uint8_t* dst = reinterpret_cast<uint8_t*>(pool.data) + prow * (E * 32) + lane * E;
-        uint32_t c[(E + 3) / 4] = {};  // the lane's E codes, little-endian in words
-#pragma unroll
-        for (int k = 0; k < E; ++k) c[k / 4] |= (uint32_t)float_to_e4m3(v[k] / scale) << (8 * (k % 4));
-        if constexpr (E == 16) {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(c[0], c[1], c[2], c[3]);
-        } else if constexpr (E == 4) {
-            *reinterpret_cast<uint32_t*>(dst) = c[0];
-        } else {
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)c[0];
-        }
-        if (lane == 0) pool.scale[prow] = scale;
     }
 }
 
@@ -577,10 +494,11 @@ static dsa_status_t make_job(int batch, int max_new, int w, int s, const void* x
     if (rope->rope_dim < 0 || rope->rope_dim > dim || (rope->rope_dim & 1) || !(rope->theta > 0.0))
         return DSA_ERR_INVALID_ARG;
     if (rope->rope_dim > 64) return DSA_ERR_UNSUPPORTED;  // the frequency table holds 32 pairs
+    if (!block_rows_ok(out)) return DSA_ERR_UNSUPPORTED;
     if (swa) {
         if (!pool_ok(swa) || !table_ok(swa_bt, batch)) return DSA_ERR_INVALID_ARG;
         if (swa->rows_per_block != kBlockPositions || swa->dim != dim) return DSA_ERR_INVALID_ARG;
-        if (swa->dtype == DSA_FP4_E2M1) return DSA_ERR_UNSUPPORTED;
+        if (swa->dtype == DSA_FP4_E2M1 || !block_rows_ok(swa)) return DSA_ERR_UNSUPPORTED;
     }
     if (!aligned(x_new, 16) || !aligned(state_x, 16)) return DSA_ERR_INVALID_ARG;
     if (gate_pc != 0 && gate_pc != 1) return DSA_ERR_INVALID_ARG;

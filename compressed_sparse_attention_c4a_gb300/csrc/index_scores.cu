@@ -967,7 +967,8 @@ static dsa_status_t index_scores(int32_t nq, int32_t heads, int32_t dim, const u
     if (!q8 || !q_scale || !w || !q_pos || !q_req || !scores || !keys || !bt || !bt->table || bt->max_blocks <= 0)
         return DSA_ERR_INVALID_ARG;
     if (!pool_ok(keys) || keys->dim != dim || keys->rows_per_block != kPage) return DSA_ERR_INVALID_ARG;
-    if (keys->dtype == DSA_BF16 || (keys->dtype == DSA_FP4_E2M1 && dim != 128)) return DSA_ERR_UNSUPPORTED;
+    if (keys->dtype == DSA_BF16 || keys->dtype == DSA_FP4_BLOCK || (keys->dtype == DSA_FP4_E2M1 && dim != 128))
+        return DSA_ERR_UNSUPPORTED;
     if (!aligned(q8, 16) || !aligned(q_scale, 16) || !aligned(w, 16) || !aligned(work, 8)) return DSA_ERR_INVALID_ARG;
     if (q_group > 64) return DSA_ERR_INVALID_ARG;
     if ((nq + q_group - 1) / q_group > 4096) return DSA_ERR_UNSUPPORTED;  // per-group tables live in smem

@@ -18,15 +18,16 @@ if not os.path.exists(_PATH):
 _lib = ctypes.CDLL(_PATH)
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE_FAULT, DSA_ERR_TIMEOUT = range(6)
-DSA_BF16, DSA_FP8_E4M3, DSA_FP4_E2M1 = 0, 1, 2
+DSA_BF16, DSA_FP8_E4M3, DSA_FP4_E2M1, DSA_FP4_BLOCK = 0, 1, 2, 3
 DSA_C4A, DSA_C128A = 0, 1
 KIND = {"c4a": DSA_C4A, "c128a": DSA_C128A}
+ATTN_DTYPE = {"bf16": DSA_BF16, "fp8": DSA_FP8_E4M3, "fp4_block": DSA_FP4_BLOCK}
 
 EXPORTS = ["dsa_status_string", "dsa_compress", "dsa_index_scores", "dsa_topk", "dsa_topk_plan", "dsa_attn_workspace_size",
            "dsa_sparse_attn_decode", "dsa_sparse_attn_prefill", "dsa_gather_rows", "dsa_sparse_attn_decode_static",
            "dsa_attn_static_scratch_bytes", "dsa_attn_plan", "dsa_debug_index_scores_stalled", "dsa_index_topk",
            "dsa_index_topk_workspace_size", "dsa_index_scores_counted", "dsa_topk_counted", "dsa_sparse_attn_q8",
-           "dsa_compress_jobs", "dsa_topk_sparse_attn_decode"]
+           "dsa_compress_jobs", "dsa_topk_sparse_attn_decode", "dsa_cache_write", "dsa_cache_read"]
 
 
 class DsaPool(ctypes.Structure):
@@ -93,6 +94,8 @@ for _name, _args in {
                                 _P, ctypes.c_size_t, _P, _P],
     "dsa_topk_sparse_attn_decode": [_I, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _I, ctypes.c_float, _P,
                                     _P, _P, _P, ctypes.c_size_t, _P, _P],
+    "dsa_cache_write": [_I, _P, _P, _I, _P, _P, _P, _P, _P],
+    "dsa_cache_read": [_P, _P, _I, _P, _P, _P, _P, _P],
     "dsa_gather_rows": [_P, _P, _I, _P, _P, _P, _P, _P, _P],
     "dsa_sparse_attn_q8": [_I, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, ctypes.c_float, _P, _P, _P, _P, _P,
                            ctypes.c_size_t, _P, _P],
@@ -124,12 +127,16 @@ def dsa_status_string(code):
 
 def pool(data, rows_per_block, scale=None, fmt=None):
     """A DsaPool over a tensor viewed as [num_blocks * rows_per_block, row] (bf16, uint8 e4m3, or with
-    fmt="fp4" uint8 bytes of two e2m1 codes each, so that dim = 2 * row)."""
+    fmt="fp4" uint8 bytes of two e2m1 codes each, so that dim = 2 * row; with fmt="fp4_block" uint8 rows of dim / 2
+    code bytes and dim / 16 block scales, 288 bytes for dim 512)."""
     rows = data.numel() // data.shape[-1]
     assert rows % rows_per_block == 0
     if fmt == "fp4":
         assert data.dtype == torch.uint8
         dtype, dim = DSA_FP4_E2M1, 2 * data.shape[-1]
+    elif fmt == "fp4_block":
+        assert data.dtype == torch.uint8 and data.shape[-1] % 9 == 0
+        dtype, dim = DSA_FP4_BLOCK, data.shape[-1] // 9 * 16
     else:
         dtype = DSA_BF16 if data.dtype == torch.bfloat16 else DSA_FP8_E4M3
         dim = data.shape[-1]
@@ -259,8 +266,7 @@ def dsa_topk_plan(nq, ld, k):
 def dsa_attn_plan(nq, heads, max_keys, dtype="bf16"):
     """(heads per CTA, CTAs per cluster, key splits per row, kernels per call) of the attention call."""
     plan = (ctypes.c_int32 * 4)()
-    code = _lib.dsa_attn_plan(int(nq), int(heads), int(max_keys), {"bf16": DSA_BF16, "fp8": DSA_FP8_E4M3}.get(dtype, dtype),
-                              plan)
+    code = _lib.dsa_attn_plan(int(nq), int(heads), int(max_keys), ATTN_DTYPE.get(dtype, dtype), plan)
     _check("dsa_attn_plan", code)
     return tuple(int(x) for x in plan)
 
@@ -315,6 +321,21 @@ def dsa_sparse_attn_q8(q, q_pos, q_req, kind, topk, k, main, main_bt, swa, swa_b
                                    int(window), float(sm_scale), ctypes.byref(rope_cfg), _ptr(out), _ptr(out_scale),
                                    _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
     _check("dsa_sparse_attn_q8", code)
+
+
+def dsa_cache_write(cu_new, start_row, x, pool_, bt, dev_status=None, stream=None):
+    """Rows of x (bf16 [n][dim], request r's at cu_new[r] .. cu_new[r + 1]) stored from logical row start_row[r] on, in
+    the pool's format (see include/dsa.h)."""
+    code = _lib.dsa_cache_write(start_row.numel(), _ptr(cu_new), _ptr(start_row), x.shape[0], _ptr(x),
+                                ctypes.byref(pool_), ctypes.byref(bt), _ptr(dev_status), _stream(stream))
+    _check("dsa_cache_write", code)
+
+
+def dsa_cache_read(pool_, bt, req, ids, out, dev_status=None, stream=None):
+    """out[j] (bf16 [n][dim]) = the value of logical row ids[j] of request req[j]; id -1: zeros."""
+    code = _lib.dsa_cache_read(ctypes.byref(pool_), ctypes.byref(bt), ids.numel(), _ptr(req), _ptr(ids), _ptr(out),
+                               _ptr(dev_status), _stream(stream))
+    _check("dsa_cache_read", code)
 
 
 def dsa_gather_rows(pool_, bt, req, ids, out, out_scale=None, dev_status=None, stream=None):

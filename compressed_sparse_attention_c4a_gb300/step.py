@@ -33,9 +33,9 @@ class LayerStep:
         dev = case["q"].device
         self.kind = spec.kind
         epb = case["epb"]
-        self.main = dsa.pool(case["main_data"], epb, case["main_scale"])
+        self.main = dsa.pool(case["main_data"], epb, case["main_scale"], fmt=spec.main_dtype)
         self.main_bt = dsa.block_table(case["bt_main"])
-        self.swa = dsa.pool(case["swa_data"], 256, case["swa_scale"])
+        self.swa = dsa.pool(case["swa_data"], 256, case["swa_scale"], fmt=spec.swa_dtype)
         self.swa_bt = dsa.block_table(case["bt_swa"])
         self.rope_main = dsa.rope(spec.rope_dim, ROPE_THETA)
         self.has_index = spec.idx_heads > 0

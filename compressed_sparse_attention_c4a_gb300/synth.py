@@ -11,7 +11,8 @@ new token (chunked prefill).  All value draws are N(0, 1) (indexer head weights
 U(0, 1)); bf16 values are torch's round-to-nearest of fp32 draws; fp8 codes are
 torch's e4m3 conversion of 64 * N(0, 1) draws with a per-row scale drawn
 U(0.5, 1.5) / 64; fp4 indexer keys are uniformly random bytes (two e2m1 codes each, every code
-equally likely) with a per-row scale drawn U(0.5, 1.5) / 6.  Physical blocks are a seeded permutation of a pool that is about
+equally likely) with a per-row scale drawn U(0.5, 1.5) / 6; fp4_block rows are uniformly random code bytes,
+block scales that are torch's e4m3 conversion of 16 * U(0.5, 1.5), and row scales 2^-7, 2^-6 or 2^-5.  Physical blocks are a seeded permutation of a pool that is about
 12% larger than what the requests need, so tables are shuffled and fragmented.  With the per-channel gate
 the logits are N(0, 1) per raw token and channel.
 """
@@ -39,10 +40,10 @@ class CaseSpec:
     idx_dim: int = 128
     topk: int = 512
     window: int = 128
-    main_dtype: str = "bf16"                            # "bf16" or "fp8"
+    main_dtype: str = "bf16"                            # "bf16", "fp8" or "fp4_block" (e2m1, a scale per 16 elements)
     idx_dtype: str = "fp8"                              # indexer keys: "fp8" (e4m3) or "fp4" (e2m1, packed)
     gate: str = "scalar"                                # compressor logits: "scalar" (per raw token) or "channel"
-    swa_dtype: str = "bf16"
+    swa_dtype: str = "bf16"                             # as main_dtype (attention takes both pools in one format)
     index_compress: bool = True                         # run the indexer compressor on the new tokens
     seed: int = 0
 
@@ -78,6 +79,21 @@ def _fp4_codes_and_scale(rows, dim, gen, device):
     return packed, scale
 
 
+def _fp4_block_rows_and_scale(rows, dim, gen, device):
+    codes = torch.randint(0, 256, (rows, dim // 2), generator=gen, device=device, dtype=torch.int32).to(torch.uint8)
+    bs = ((torch.rand((rows, dim // 16), generator=gen, device=device) + 0.5) * 16.0).to(torch.float8_e4m3fn)
+    e = torch.randint(-7, -4, (rows,), generator=gen, device=device, dtype=torch.int32)
+    return torch.cat([codes, bs.view(torch.uint8)], dim=1), ((e + 127) << 23).view(torch.float32)
+
+
+def _pool_rows(dtype, rows, dim, gen, device):
+    """Rows of a main or window pool in its format, and their scales (None for bf16)."""
+    if dtype == "bf16":
+        return _randn((rows, dim), gen, device).to(torch.bfloat16), None
+    draw = _fp4_block_rows_and_scale if dtype == "fp4_block" else _fp8_codes_and_scale
+    return draw(rows, dim, gen, device)
+
+
 def _tables(blocks_needed, cpu_gen, spare=0.125):
     """Block tables [B][max_blocks] (int32, -1 = unmapped) over a shuffled shared pool."""
     total = sum(len(b) for b in blocks_needed)
@@ -109,11 +125,7 @@ def make_case(spec: CaseSpec, device="cpu"):
     main_blocks = [list(range((t + BLOCK_POSITIONS - 1) // BLOCK_POSITIONS)) for t in tot]
     bt_main, nb_main = _tables(main_blocks, cpu)
     out["bt_main"], out["nb_main"] = bt_main.to(dev), nb_main
-    if spec.main_dtype == "bf16":
-        out["main_data"] = _randn((nb_main * epb, D), gen, dev).to(torch.bfloat16)
-        out["main_scale"] = None
-    else:
-        out["main_data"], out["main_scale"] = _fp8_codes_and_scale(nb_main * epb, D, gen, dev)
+    out["main_data"], out["main_scale"] = _pool_rows(spec.main_dtype, nb_main * epb, D, gen, dev)
 
     # indexer key pool (c4a only)
     if spec.idx_heads:
@@ -134,11 +146,7 @@ def make_case(spec: CaseSpec, device="cpu"):
         swa_blocks.append(list(range(lo // BLOCK_POSITIONS, hi // BLOCK_POSITIONS + 1)))
     bt_swa, nb_swa = _tables(swa_blocks, cpu)
     out["bt_swa"], out["nb_swa"] = bt_swa.to(dev), nb_swa
-    if spec.swa_dtype == "bf16":
-        out["swa_data"] = _randn((nb_swa * BLOCK_POSITIONS, D), gen, dev).to(torch.bfloat16)
-        out["swa_scale"] = None
-    else:
-        out["swa_data"], out["swa_scale"] = _fp8_codes_and_scale(nb_swa * BLOCK_POSITIONS, D, gen, dev)
+    out["swa_data"], out["swa_scale"] = _pool_rows(spec.swa_dtype, nb_swa * BLOCK_POSITIONS, D, gen, dev)
 
     # compressor rolling state: slot r holds request r's last w raw tokens (slot = pos mod w)
     out["state_slot"] = torch.arange(B, dtype=torch.int32, device=dev)

@@ -60,14 +60,21 @@ typedef int32_t dsa_status_t;
 #define DSA_FP8_E4M3 1 /* e4m3 bytes + one fp32 scale per row: value = scale * e4m3(code) */
 #define DSA_FP4_E2M1 2 /* e2m1 codes packed two per byte (element 2j in the low nibble) + one fp32 scale per
                           row: value = scale * e2m1(code); [P2] 第三层 (the fp4 indexer cache); indexer keys only */
+#define DSA_FP4_BLOCK 3 /* a 4-bit main / window cache ([P2] 第三层), dim 512: a row is 256 bytes of e2m1 codes (element
+                          2j in the low nibble of byte j), then 32 e4m3 bytes, the scale of each 16 elements; beside it one
+                          fp32 scale per row: value_d = scale * e4m3(block d / 16) * e2m1(code_d).  Rows are quantised
+                          with scale = the least power of two with amax <= 2688 * scale (at least 2^-126; 1 for a row of
+                          zeros), block scale = e4m3(block amax / (6 * scale)), code = e2m1(x / (scale * block scale)),
+                          each to nearest even and saturating; a row with an infinity or a NaN is stored with scale NaN
+                          and zero codes, and reads back as NaN */
 
 /* compressor kinds ([P1] §5.2, [P2] 机制二) */
 #define DSA_C4A 0   /* window 8 raw tokens, stride 4: 64 entries per block */
 #define DSA_C128A 1 /* window 128, stride 128: 2 entries per block */
 
 /* A paged pool.  data: [num_blocks][rows_per_block][dim] elements (bf16 or e4m3 bytes; e2m1: dim / 2 bytes
- * per row), row-major and contiguous, 16-byte aligned (e2m1: 32-byte).  scale: [num_blocks][rows_per_block]
- * fp32, required for DSA_FP8_E4M3 and DSA_FP4_E2M1, ignored for DSA_BF16. */
+ * per row; DSA_FP4_BLOCK: 288 bytes per row of 512), row-major and contiguous, 16-byte aligned (e2m1: 32-byte).
+ * scale: [num_blocks][rows_per_block] fp32, 16-byte aligned, required for every format but DSA_BF16, which ignores it. */
 typedef struct dsa_pool {
     void* data;
     float* scale;
@@ -119,8 +126,8 @@ const char* dsa_status_string(dsa_status_t status);
  * x_new      [cu_new[batch]][dim] bf16;  logit_new [cu_new[batch]] fp32
  * state_*    rolling state; num_slots host int = number of slots; state_slot [batch]
  * rms_gamma  [dim] fp32 or NULL (= all ones);  rms_eps > 0
- * out        bf16, e4m3 or e2m1 pool (e2m1: scale = amax/6), rows_per_block = 256/s;  swa: rows_per_block = 256
- *            (bf16 or e4m3), or NULL
+ * out        bf16, e4m3, e2m1 (scale = amax/6) or, with dim 512, DSA_FP4_BLOCK pool, rows_per_block = 256/s;
+ *            swa: rows_per_block = 256 (bf16, e4m3 or DSA_FP4_BLOCK), or NULL
  * Supported: dim in {64, 128, 512}, rope_dim even and <= min(dim, 64).
  * Launched with programmatic dependent launch: cu_new, start_pos, state_slot, the block tables and rms_gamma
  * are read before waiting for the preceding kernel in the stream; the raw tokens, logits and rolling state
@@ -308,14 +315,14 @@ dsa_status_t dsa_topk_plan(int32_t nq, int32_t ld, int32_t k, int32_t* plan);
 /*
  * Workspace (bytes) that dsa_sparse_attn_decode / _prefill need for nq query rows of
  * `heads` heads and at most `max_keys` keys per row (compressed + window) on the current
- * device, for either pool format: the fp32 partial outputs and (max, sums) of rows whose keys
+ * device, for every pool format: the fp32 partial outputs and (max, sums) of rows whose keys
  * are split over several groups of CTAs.  0 means the call needs none.
  */
 size_t dsa_attn_workspace_size(int32_t nq, int32_t heads, int32_t max_keys);
 
 /*
  * dsa_attn_plan - how dsa_sparse_attn_decode / _prefill split the work for these sizes on
- * the current device and pool format (dtype DSA_BF16 or DSA_FP8_E4M3); host only, launches
+ * the current device and pool format (dtype DSA_BF16, DSA_FP8_E4M3 or DSA_FP4_BLOCK); host only, launches
  * nothing.  plan[0] = heads per CTA, plan[1] = CTAs per cluster (one query row's keys shared
  * among them), plan[2] = key splits per row, plan[3] = kernels one call launches (1, or 2 with
  * the split merge).  Returns DSA_ERR_INVALID_ARG / DSA_ERR_UNSUPPORTED as the attention call
@@ -339,7 +346,7 @@ dsa_status_t dsa_attn_plan(int32_t nq, int32_t heads, int32_t max_keys, int32_t 
  * q          [batch][heads][512] bf16, already rotated at m;  q_pos [batch] int32
  * kind       DSA_C4A or DSA_C128A (visibility and rows_per_block of `main`)
  * topk       [batch][k] int32 logical entry ids (-1 = none) or NULL;  k host int <= 2048
- * main, swa  pools with dim 512, bf16 or fp8 (per-row scale);  window: host int, 1..1024
+ * main, swa  pools with dim 512, both bf16, both e4m3 or both DSA_FP4_BLOCK;  window: host int, 1..1024
  * sm_scale   host float (1/sqrt(512) in the layer)
  * out        [batch][heads][512] bf16;  lse [batch][heads] fp32 (natural log of the softmax
  *            denominator) or NULL
@@ -443,10 +450,44 @@ dsa_status_t dsa_sparse_attn_decode_static(int32_t batch, int32_t heads, const v
 size_t dsa_attn_static_scratch_bytes(void);
 
 /*
+ * dsa_cache_write - store rows in a paged cache, in the pool's format.  [P1] §2.2 (logical rows through a request's
+ * block table), [P2] 第三层 (a prefill keeps its caches in bf16, decode reads them quantised row by row): for rows that
+ * are formed already, such as the caches a prefill hands over or another cache's rows read back.  Row j of x, of the
+ * request r with cu_new[r] <= j < cu_new[r+1], becomes logical row start_row[r] + j - cu_new[r] of request r.
+ *
+ * batch      requests (host int, >= 0);  cu_new [batch + 1] int32, cu_new[0] = 0, non-decreasing
+ * start_row  [batch] int32 >= 0
+ * n          host int: rows that x holds; rows of x from cu_new[batch] on are ignored.  batch or n 0 is a no-op
+ * x          [n][dim] bf16, 16-byte aligned
+ * pool, bt   any format (bf16: a copy; e4m3: scale amax/448; e2m1: amax/6; DSA_FP4_BLOCK as described there), dim 64, 128
+ *            or 512 (DSA_FP4_BLOCK: 512);  bt->batch >= batch
+ * The rows a call writes must be distinct: two requests that map to one physical row race on it.
+ * A row whose logical row is unmapped or beyond the table is not written and raises DSA_ERR_DEVICE_FAULT; the others
+ * are written.  Pool rows that no row of x maps to are left as they were.
+ * Launched with programmatic dependent launch: cu_new, start_row and the block table are read before waiting for the
+ * preceding kernel in the stream; x is read, and the pool written, only after it.
+ */
+dsa_status_t dsa_cache_write(int32_t batch, const int32_t* cu_new, const int32_t* start_row, int32_t n, const void* x,
+                             const dsa_pool_t* pool, const dsa_block_table_t* bt, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_cache_read - rows of a paged cache as bf16 values (the values the attention computes with): out[j] = the value
+ * of logical row ids[j] of request req[j], rounded to nearest even (DSA_FP4_BLOCK and bf16 rows are exact).  The same row may be
+ * read any number of times.
+ * n          host int, >= 0 (0 is a no-op);  req, ids [n] int32;  id -1 (as dsa_topk pads): a row of zeros
+ * out        [n][dim] bf16, 16-byte aligned
+ * pool, bt   any format, dim 64, 128 or 512 (DSA_FP4_BLOCK: 512)
+ * A request outside the table, or a row that is unmapped or beyond it, is written as zeros and raises
+ * DSA_ERR_DEVICE_FAULT.  Launched with programmatic dependent launch: everything is read after the wait.
+ */
+dsa_status_t dsa_cache_read(const dsa_pool_t* pool, const dsa_block_table_t* bt, int32_t n, const int32_t* req,
+                            const int32_t* ids, void* out, int32_t* dev_status, void* stream);
+
+/*
  * dsa_gather_rows - copy the stored bytes of n logical rows, exactly as the attention
  * reads them, into a dense array (a checking hook for the block-table translation of
  * [P1] §2.2 / [P2] 设计 1).  Row j is logical row ids[j] of request req[j].
- * out: [n][dim * element_size] bytes;  out_scale: [n] fp32 (fp8 pools) or NULL.
+ * out: [n][bytes of a row];  out_scale: [n] fp32 (the row scales of every format but bf16) or NULL.
  * An unmapped or out-of-range row is written as zeros and raises DSA_ERR_DEVICE_FAULT.
  */
 dsa_status_t dsa_gather_rows(const dsa_pool_t* pool, const dsa_block_table_t* bt, int32_t n, const int32_t* req,

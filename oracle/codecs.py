@@ -191,3 +191,41 @@ def fp4_quantize_rows(v):
 def fp4_dequantize_rows(packed, scale):
     """Row value = scale * e2m1(code)."""
     return e2m1_decode(fp4_unpack(packed)) * np.asarray(scale, dtype=np.float64)[..., None]
+
+
+# ---- fp4 e2m1 with an e4m3 scale per 16 elements and a power-of-two scale per row ----------------------------------
+FP4_BLOCK = 16
+
+
+def fp4_block_row_scale(v):
+    """The least power of two s with amax <= 448 * 6 * s (at least 2^-126); 1 for a row of zeros."""
+    amax = np.max(np.abs(np.asarray(v, dtype=np.float64)), axis=-1)
+    e = np.full(amax.shape, -126, dtype=np.int64)
+    while True:
+        short = amax > np.ldexp(E4M3_MAX * E2M1_MAX, e)
+        if not np.any(short):
+            break
+        e = np.where(short, e + 1, e)
+    return np.where(amax > 0, np.ldexp(1.0, e), 1.0)
+
+
+def fp4_block_quantize_rows(v):
+    """Rows [..., d] of finite float64 values -> (bytes [..., d / 2 + d / 16], scale [...]): packed e2m1 codes, then the
+    e4m3 block scales, value = scale * e4m3(block) * e2m1(code)."""
+    v = np.asarray(v, dtype=np.float64)
+    s = fp4_block_row_scale(v)
+    blocks = v.reshape(v.shape[:-1] + (-1, FP4_BLOCK)) / s[..., None, None]
+    bs_codes = e4m3_encode(np.max(np.abs(blocks), axis=-1) / E2M1_MAX)
+    bs = e4m3_decode(bs_codes)[..., None]
+    q = np.divide(blocks, bs, out=np.zeros_like(blocks), where=bs > 0)
+    packed = fp4_pack(e2m1_encode(q).reshape(v.shape))
+    return np.concatenate([packed, bs_codes.astype(np.uint8)], axis=-1), s
+
+
+def fp4_block_dequantize_rows(data, scale):
+    """Row value = scale * e4m3(block scale) * e2m1(code)."""
+    data = np.asarray(data, dtype=np.uint8)
+    half = data.shape[-1] // 9 * 8
+    el = e2m1_decode(fp4_unpack(data[..., :half]))
+    bs = np.repeat(e4m3_decode(data[..., half:]), FP4_BLOCK, axis=-1)
+    return el * bs * np.asarray(scale, dtype=np.float64)[..., None]

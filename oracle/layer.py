@@ -21,13 +21,15 @@ from .topk import topk as _topk
 BF16 = "bf16"
 FP8 = "fp8_e4m3"
 FP4 = "fp4_e2m1"
+FP4_BLOCK = "fp4_block"
 
 
 class Pool:
     """A paged cache pool: ``data`` [num_blocks * epb, dim], ``scale`` [num_blocks * epb] for fp8.
 
     bf16 pools hold either float64 values or the raw uint16 bit patterns (decoded on read); fp4 pools hold
-    packed e2m1 bytes [num_blocks * epb, dim / 2] and a scale per row.
+    packed e2m1 bytes [num_blocks * epb, dim / 2] and a scale per row; fp4_block pools the codes and block scales
+    [num_blocks * epb, dim / 2 + dim / 16] and a scale per row.
     """
 
     def __init__(self, epb, dtype, data, scale=None):
@@ -50,6 +52,8 @@ class Pool:
             return np.asarray(self.data[rows], dtype=np.float64)
         if self.dtype == FP4:
             return codecs.fp4_dequantize_rows(self.data[rows], self.scale[rows])
+        if self.dtype == FP4_BLOCK:
+            return codecs.fp4_block_dequantize_rows(self.data[rows], self.scale[rows])
         return codecs.fp8_dequantize_rows(self.data[rows], self.scale[rows])
 
     def read_codes(self, table_row, ids):
@@ -67,6 +71,8 @@ class Pool:
             codes, scale = codecs.fp4_quantize_rows(values)
             self.data[rows] = codes
             self.scale[rows] = scale
+        elif self.dtype == FP4_BLOCK:
+            self.data[rows], self.scale[rows] = codecs.fp4_block_quantize_rows(values)
         else:
             codes, scale = codecs.fp8_quantize_rows(values)
             self.data[rows] = codes
@@ -166,5 +172,5 @@ def ring_contents(states):
     return np.stack([s.x for s in states]), np.stack([s.z for s in states])
 
 
-__all__ = ["Pool", "BF16", "FP8", "FP4", "compress", "index_scores", "topk", "sparse_attn", "sparse_attn_q8",
+__all__ = ["Pool", "BF16", "FP8", "FP4", "FP4_BLOCK", "compress", "index_scores", "topk", "sparse_attn", "sparse_attn_q8",
            "ring_contents", "WINDOW"]
