@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
 LIB_CHECKED = os.path.join(PKG, "libdsa_checked.so")
-SOURCES = ["api.cu", "compress.cu", "index_scores.cu", "topk.cu", "attention.cu", "cache.cu"]
+SOURCES = ["api.cu", "compress.cu", "index_scores.cu", "topk.cu", "attention.cu", "attention_fp4.cu", "cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -10,6 +10,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "dsa.h"
@@ -82,12 +83,16 @@ inline cudaError_t launch_pdl(void (*kernel)(Exp...), dim3 grid, dim3 block, siz
 }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link dependency).
+// Looked up once per process (a failed lookup is tried again).
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    void* fn = nullptr;
+    static std::atomic<void*> found{nullptr};
+    void* fn = found.load(std::memory_order_relaxed);
+    if (fn) return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
         q != cudaDriverEntryPointSuccess)
         return nullptr;
+    found.store(fn, std::memory_order_relaxed);
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
 }
 

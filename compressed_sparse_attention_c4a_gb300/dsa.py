@@ -107,13 +107,13 @@ for _name, _args in {
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # the current stream's handle alone: a Stream object costs as much as the launch (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(fn, code):
@@ -129,24 +129,25 @@ def pool(data, rows_per_block, scale=None, fmt=None):
     """A DsaPool over a tensor viewed as [num_blocks * rows_per_block, row] (bf16, uint8 e4m3, or with
     fmt="fp4" uint8 bytes of two e2m1 codes each, so that dim = 2 * row; with fmt="fp4_block" uint8 rows of dim / 2
     code bytes and dim / 16 block scales, 288 bytes for dim 512)."""
-    rows = data.numel() // data.shape[-1]
+    cols = data.shape[-1]
+    rows = data.numel() // cols
     assert rows % rows_per_block == 0
     if fmt == "fp4":
         assert data.dtype == torch.uint8
-        dtype, dim = DSA_FP4_E2M1, 2 * data.shape[-1]
+        dtype, dim = DSA_FP4_E2M1, 2 * cols
     elif fmt == "fp4_block":
-        assert data.dtype == torch.uint8 and data.shape[-1] % 9 == 0
-        dtype, dim = DSA_FP4_BLOCK, data.shape[-1] // 9 * 16
+        assert data.dtype == torch.uint8 and cols % 9 == 0
+        dtype, dim = DSA_FP4_BLOCK, cols // 9 * 16
     else:
         dtype = DSA_BF16 if data.dtype == torch.bfloat16 else DSA_FP8_E4M3
-        dim = data.shape[-1]
+        dim = cols
     return DsaPool(data.data_ptr(), None if scale is None else scale.data_ptr(), rows // rows_per_block,
                    rows_per_block, dim, dtype)
 
 
 def block_table(table):
     """A DsaBlockTable over an int32 [batch][max_blocks] tensor."""
-    return DsaBlockTable(table.data_ptr(), table.shape[0], table.shape[1])
+    return DsaBlockTable(table.data_ptr(), *table.shape)
 
 
 def rope(rope_dim=64, theta=10000.0):
