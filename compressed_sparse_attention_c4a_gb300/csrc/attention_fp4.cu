@@ -17,8 +17,8 @@ namespace dsa {
 //               two tiles ahead, every lane loads 8 code bytes and one block scale of each row straight into registers
 //               (two tiles in flight, nothing staged), and once the key stage is free (its P V is done) the codes become
 //               bf16 and are stored 128B-swizzled as [64-dim chunk][64 keys][128 B];
-//   warps 4-5   S = Q K^T (M = 64 heads, N = 64 keys), 256 dims each into accumulators of their own;
-//   warps 6-7   O^T += V^T P^T (M = 128 dims, N = NH heads, K = 64 keys), two of the four 128-dim tiles each;
+//   warp 4      S = Q K^T (M = 64 heads, N = 64 keys);
+//   warp 5      O^T += V^T P^T (four tiles of M = 128 dims, N = NH heads, K = 64 keys);
 //   warps 0-3   softmax: 16 heads a warp, a head's 64 logits over the 4 lanes of a quad (the 16-lane TMEM load spreads a
 //               row over a quad, so every lane works although M = 64 fills 16 of the 32 TMEM lanes).
 // Two key stages, two S and two P buffers: S of tile i + 1 and the widening of tile i + 2 overlap the softmax and P V of i.
@@ -40,8 +40,8 @@ struct Fp4Smem {
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + kQ;                        // key stages; received tiles
     static constexpr int kOffP = kOffK + 2 * kFp4Stage;             // two P^T buffers; output staging at the end
-    static constexpr int kOffKsc = kOffP + 2 * kP;                  // float [2][64]: row scales of a stage
-    static constexpr int kOffMask = kOffKsc + 2 * kFp4Keys * 4;     // uint64 [2]: valid keys of a stage
+    static constexpr int kOffKsc = kOffP + 2 * kP;                  // float [2][32][4]: see s_ksc
+    static constexpr int kOffMask = kOffKsc + 2 * kFp4Keys * 8;     // uint64 [2]: valid keys of a stage
     static constexpr int kOffAlpha = kOffMask + 16;                 // float [2][NH]
     static constexpr int kOffVote = kOffAlpha + 2 * NH * 4;         // int [2][4]
     static constexpr int kOffOwn = kOffVote + 32;                   // float m[NH], l[NH], e[NH] of this CTA
@@ -51,9 +51,9 @@ struct Fp4Smem {
     static constexpr int kOffSwb = kOffBt + kBtCache * 4;           // int [8]: window-pool blocks from that of wlo
     static constexpr int kOffFault = kOffSwb + 32;                  // int: a key of this CTA hit a device fault
     static constexpr int kOffRope = kOffFault + 16;                 // float [32][2]: cos, sin of each pair's angle at m
-    static constexpr int kOffBar = kOffRope + 256;                  // 12 mbarriers, TMEM address
-    static constexpr int kOffXfull = kOffBar + 9 * 8;               // the last three: received tile slots
-    static constexpr int kOffTopk = kOffBar + 12 * 8 + 16;          // int [kFusedK]: the row's top-k (fused)
+    static constexpr int kOffBar = kOffRope + 256;                  // 14 mbarriers, TMEM address
+    static constexpr int kOffXfull = kOffBar + 11 * 8;              // the last three: received tile slots
+    static constexpr int kOffTopk = kOffBar + 14 * 8 + 16;          // int [kFusedK]: the row's top-k (fused)
     static constexpr int kBytes = kOffTopk + kFusedK * 4;
     static constexpr int kAlloc = kBytes + 1024;                    // + alignment slack
     static constexpr int kOffOut1 = kOffK + kFp4Stage;              // second output staging buffer (the second stage)
@@ -68,7 +68,7 @@ struct Fp4Smem {
     static_assert(6 * kTile <= kQ + kFp4Stage, "the received tiles fit before the second output buffer");
     static_assert(NH * 128 * 2 <= 2 * kP, "an output tile must fit in the P^T buffers");
     static_assert(sizeof(TopkRowScratch<kClThreads, kFusedVpt, 4>) <= 2 * kFp4Stage, "the fused top-k's scratch");
-    static constexpr int kTmemCols = 512;  // S: [2 buffers][2 parts][64 keys]; O^T: [4 tiles][NH heads]
+    static constexpr int kTmemCols = 512;  // S: [2 buffers][64 keys]; O^T: [4 tiles][NH heads]
 };
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -138,6 +138,31 @@ __device__ __forceinline__ void tmem_ld_16x64_nowait(uint32_t taddr, float (&v)[
         : "memory");
 }
 
+// Two fp32 values in one register pair (packed arithmetic halves the instructions of the softmax).
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float* lo, float* hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ float quad_max(float v) {
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
@@ -154,6 +179,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sP = smem_u32(smem + L::kOffP);
+    // the row scales of keys 2 p and 2 p + 1 of a stage, then the same times sm_scale log2(e)
     float* s_ksc = reinterpret_cast<float*>(smem + L::kOffKsc);
     uint8_t* s_mask8 = smem + L::kOffMask;
     float* s_alpha = reinterpret_cast<float*>(smem + L::kOffAlpha);
@@ -161,10 +187,11 @@ __global__ void __launch_bounds__(kClThreads, 1)
     float* s_own = reinterpret_cast<float*>(smem + L::kOffOwn);
     // tile i: key stage, S columns and P^T buffer i & 1
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // [2] stage widened (widening warps)
-    uint64_t* sfull = full + 2;                                         // [2] S in TMEM (both S warps' commits)
+    uint64_t* sfull = full + 2;                                         // [2] S in TMEM
     uint64_t* pfull = sfull + 2;                                        // [2] P^T written (4 softmax warps)
-    uint64_t* pvdone = pfull + 2;                                       // [2] O^T += V^T P^T done (2 commits)
+    uint64_t* pvdone = pfull + 2;                                       // [2] O^T += V^T P^T done
     uint64_t* qfull = pvdone + 2;                                       // query rows loaded
+    uint64_t* rdone = qfull + 1;                                        // O^T rescaled (4 softmax warps)
     uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + L::kOffXfull);  // [3] each received tile slot loaded
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(xfull + 3);
     volatile int* s_fault = reinterpret_cast<volatile int*>(smem + L::kOffFault);
@@ -179,11 +206,12 @@ __global__ void __launch_bounds__(kClThreads, 1)
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(&full[b], kFp4Widen);
-            mbar_init(&sfull[b], 2);
+            mbar_init(&sfull[b], 1);
             mbar_init(&pfull[b], 4);
-            mbar_init(&pvdone[b], 2);
+            mbar_init(&pvdone[b], 1);
         }
         mbar_init(qfull, 1);
+        mbar_init(rdone, 4);
         for (int b = 0; b < 3; ++b) mbar_init(&xfull[b], 1);
         *s_fault = 0;
         fence_barrier_init();
@@ -199,7 +227,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const uint32_t tS = tmem, tO = tmem + 4 * kFp4Keys;
+    const uint32_t tS = tmem, tO = tmem + 2 * kFp4Keys;
     if (csize > 1) cluster_arrive_relaxed();  // phase 0: this CTA has started (waited on before DSMEM use)
 
     // Position, request, block tables and query rows: inputs that no kernel of the layer step writes, read while the
@@ -356,8 +384,13 @@ __global__ void __launch_bounds__(kClThreads, 1)
         auto widen = [&](int b, int i) {
             const int st = i & 1;
             if (i >= 2) ok = ok && mbar_wait_bounded(&pvdone[st], ((i >> 1) - 1) & 1, kWaitLimitNs);  // stage free
+            if (gt == 0) DSA_TRACE(i, 0);
             if (ok) {
-                if (lane < kFp4PerWarp) s_ksc[st * kFp4Keys + ww * kFp4PerWarp + lane] = ksc[b];
+                if (lane < kFp4PerWarp) {
+                    float* k = s_ksc + st * 2 * kFp4Keys + (ww * kFp4PerWarp + lane) / 2 * 4 + (lane & 1);
+                    k[0] = ksc[b];
+                    k[2] = ksc[b] * a.scale_log2;
+                }
                 if (lane == 0) s_mask8[st * 8 + ww] = (uint8_t)valid[b];
 #pragma unroll
                 for (int u = 0; u < kFp4PerWarp; ++u) {
@@ -376,6 +409,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
             fence_proxy_async_smem();  // the bf16 rows -> visible to the tensor core (async proxy)
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);
+            if (gt == 0) DSA_TRACE(i, 1);
         };
         if (n_mine > 0) {
             int id0, id1, id2;
@@ -399,161 +433,204 @@ __global__ void __launch_bounds__(kClThreads, 1)
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
-    } else if (warp >= 6) {
-        // ---- O^T += V^T P^T: two 128-dim tiles each, issued by one elected lane ----------------------------
-        const int part = warp - 6;
+    } else if (warp == 5) {
+        // ---- O^T += V^T P^T, issued by one elected lane ------------------------------------------------------
         const uint32_t idesc_o = idesc_bf16(NH, 1, 128);
-        for (int i = 0; i < n_mine && ok; ++i) {
+        uint32_t rescales = 0;
+        for (int i = 0; i < n_mine; ++i) {
             const int b = i & 1;
             ok = mbar_wait_bounded(&pfull[b], (i >> 1) & 1, kWaitLimitNs);  // P^T written (so S done, the stage full)
+            if (ok && (s_vote[b * 4] | s_vote[b * 4 + 1] | s_vote[b * 4 + 2] | s_vote[b * 4 + 3]))
+                ok = mbar_wait_bounded(rdone, rescales++ & 1, kWaitLimitNs);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
+            if (tid == 160) DSA_TRACE(i, 6);
             const uint64_t dv = sw128_desc(sK + b * kFp4Stage, kFp4Keys * 128, 1024);
             const uint64_t dp = sw128_desc(sP + b * L::kP, 16, 1024);
 #pragma unroll
-            for (int mt = 2 * part; mt < 2 * part + 2; ++mt)
+            for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                 for (int ks = 0; ks < kFp4Keys / 16; ++ks)
                     mma_bf16_ss_elect(tO + mt * NH,
                                       dv + (uint64_t)(((2 * mt) * (kFp4Keys * 128) + (2 * ks) * 1024) >> 4),
                                       dp + (uint64_t)((ks * 32) >> 4), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
             mma_commit_elect(&pvdone[b]);
+            if (tid == 160) DSA_TRACE(i, 7);
         }
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
-    } else if (warp >= 4) {
-        // ---- S = Q K^T: 256 dims each, issued by one elected lane ------------------------------------------
-        const int part = warp - 4;
+    } else if (warp == 4) {
+        // ---- S = Q K^T, issued by one elected lane -----------------------------------------------------------
         const uint32_t idesc_s = idesc_bf16(kFp4Keys, 0, 64);
         const uint64_t dq = sw128_desc(sQ, 16, 1024);
         if (n_mine > 0) ok = mbar_wait_bounded(qfull, 0, kWaitLimitNs);
-        for (int i = 0; i < n_mine && ok; ++i) {
+        for (int i = 0; i < n_mine; ++i) {
             const int b = i & 1;
-            if (i >= 2) ok = mbar_wait_bounded(&pfull[b], ((i >> 1) - 1) & 1, kWaitLimitNs);  // S buffer read
+            if (i >= 2) ok = ok && mbar_wait_bounded(&pfull[b], ((i >> 1) - 1) & 1, kWaitLimitNs);  // S buffer read
             ok = ok && mbar_wait_bounded(&full[b], (i >> 1) & 1, kWaitLimitNs);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
+            if (tid == 128) DSA_TRACE(i, 2);
             const uint64_t dk = sw128_desc(sK + b * kFp4Stage, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < kD / 32; ++k) {
-                const int ks = part * (kD / 32) + k;
+            for (int ks = 0; ks < kD / 16; ++ks) {
                 const uint64_t off = (uint64_t)((((ks >> 2) * (64 * 128)) + (ks & 3) * 32) >> 4);  // 64-row chunks, both
-                mma_bf16_ss_elect(tS + (b * 2 + part) * kFp4Keys, dq + off, dk + off, idesc_s, k > 0 ? 1u : 0u);
+                mma_bf16_ss_elect(tS + b * kFp4Keys, dq + off, dk + off, idesc_s, ks > 0 ? 1u : 0u);
             }
             mma_commit_elect(&sfull[b]);
+            if (tid == 128) DSA_TRACE(i, 3);
         }
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
-    } else {
+    } else if (warp < 4) {
         // ---- softmax warps: heads 16 warp + lane / 4 and + 8, keys 8 i + 2 (lane % 4), + 1 ------------------
         const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
         const int hr = lane >> 2, c = lane & 3;
-        // l_run, e_run: the lane's share of the sum of the probabilities (both fp32: the row scale makes the rounded
-        // ones multiples of other units), m_run: the head's running maximum, lazy: it moves only by more than 2^8
-        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        // m_run: the head's running maximum, lazy: it moves only when exceeded by more than 2^8, so O^T is rarely
+        // rescaled and exp2(s - m) <= 2^8.  l_run: the lane's share of the sum of the fp32 probabilities, two halves
+        float m_run[2] = {-INFINITY, -INFINITY};
+        uint64_t l_run[2] = {0ull, 0ull};
+        // O^T times alpha per head, when a head's maximum moved in tile i: after the other warps' votes for the tile are
+        // in (their P^T is written) and the product of tile i - 1 is done; the product of tile i waits for it
+        auto rescale = [&](int i) {
+            const int b = i & 1;
+            ok = ok && mbar_wait_bounded(&pfull[b], (i >> 1) & 1, kWaitLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !(s_vote[b * 4] | s_vote[b * 4 + 1] | s_vote[b * 4 + 2] | s_vote[b * 4 + 3])) return;
+            ok = mbar_wait_bounded(&pvdone[b ^ 1], ((i - 1) >> 1) & 1, kWaitLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+                    for (int c0 = 0; c0 < NH; c0 += 16) {
+                        float v[16];
+                        tmem_ld16(tO + mt * NH + lane_off + c0, v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] *= s_alpha[b * NH + c0 + e];
+                        tmem_st16(tO + mt * NH + lane_off + c0, v);
+                    }
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rdone);
+        };
         for (int i = 0; i < n_mine; ++i) {
             const int b = i & 1;
+            if (i > 0) rescale(i - 1);
             ok = ok && mbar_wait_bounded(&full[b], (i >> 1) & 1, kWaitLimitNs);  // the stage's scales and mask
             ok = ok && mbar_wait_bounded(&sfull[b], (i >> 1) & 1, kWaitLimitNs);
             if (i >= 2) ok = ok && mbar_wait_bounded(&pvdone[b], ((i >> 1) - 1) & 1, kWaitLimitNs);  // P^T buffer free
             ok = __all_sync(0xffffffffu, ok);
+            if (tid == 0) DSA_TRACE(i, 4);
             float alpha[2] = {1.f, 1.f};
             bool resc = false;
             if (ok) {
                 tc_fence_after();
-                float sv[32], sh[32];
-                tmem_ld_16x64_nowait(tS + (b * 2) * kFp4Keys + lane_off, sv);
-                tmem_ld_16x64_nowait(tS + (b * 2 + 1) * kFp4Keys + lane_off, sh);
-                tmem_wait_ld();
-                tmem_regs_after_wait<32>(sv);
-                tmem_regs_after_wait<32>(sh);
+                float sv[32];  // logits of head h in 4 e + 2 h, 4 e + 2 h + 1: keys 8 e + 2 c, + 1
+                tmem_ld_16x64_nowait(tS + b * kFp4Keys + lane_off, sv);
+                const float4* k4 = reinterpret_cast<const float4*>(s_ksc + b * 2 * kFp4Keys) + c;
                 const uint64_t vm = *reinterpret_cast<const uint64_t*>(s_mask8 + b * 8);
-                const float2* k2 = reinterpret_cast<const float2*>(s_ksc + b * kFp4Keys) + c;
-                float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 ks = k2[4 * e];
-                    const uint32_t bits = (uint32_t)(vm >> (8 * e)) >> (2 * c);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float& x = sv[4 * e + 2 * h];
-                        float& y = sv[4 * e + 2 * h + 1];
-                        x = bits & 1 ? (x + sh[4 * e + 2 * h]) * (ks.x * a.scale_log2) : -INFINITY;
-                        y = bits & 2 ? (y + sh[4 * e + 2 * h + 1]) * (ks.y * a.scale_log2) : -INFINITY;
-                        mx[h] = fmaxf(mx[h], fmaxf(x, y));
-                    }
-                }
-                float mr[2];
+                float m0[2];  // the logits are taken relative to m0: the running maximum, 0 before the first key
+                uint64_t neg[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    mx[h] = quad_max(mx[h]);
-                    if (mx[h] > m_run[h] + kLazyLog2) {  // also the first finite maximum (m_run = -inf)
-                        alpha[h] = exp2f(m_run[h] - mx[h]);
-                        resc = i > 0;
-                        m_run[h] = mx[h];
-                    }
-                    mr[h] = m_run[h] == -INFINITY ? 0.f : m_run[h];  // all keys so far masked: p = 0
+                    m0[h] = m_run[h] == -INFINITY ? 0.f : m_run[h];
+                    neg[h] = pack_f32x2(-m0[h], -m0[h]);
                 }
-                float sum[2] = {0.f, 0.f};
+                tmem_wait_ld();
+                tmem_regs_after_wait<32>(sv);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float2 ks = k2[4 * e];
+                    const float4 k = k4[4 * e];
+                    const uint64_t kl = pack_f32x2(k.z, k.w);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        unpack_f32x2(fma_f32x2(pack_f32x2(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]), kl, neg[h]),
+                                     &sv[4 * e + 2 * h], &sv[4 * e + 2 * h + 1]);
+                }
+                if (vm != ~0ull) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t bits = (uint32_t)(vm >> (8 * e)) >> (2 * c);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!(bits & 1)) sv[4 * e + 2 * h] = -INFINITY;
+                            if (!(bits & 2)) sv[4 * e + 2 * h + 1] = -INFINITY;
+                        }
+                    }
+                }
+                float mx[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mx[h] = fmaxf(sv[2 * h], sv[2 * h + 1]);
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) mx[h] = fmaxf(mx[h], fmaxf(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]));
+                    mx[h] = quad_max(mx[h]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (mx[h] > (m_run[h] == -INFINITY ? -INFINITY : kLazyLog2)) {  // also the first finite maximum
+                        const float m_new = m0[h] + mx[h];
+                        alpha[h] = exp2f(m_run[h] - m_new);
+                        resc = i > 0;
+                        m_run[h] = m_new;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            sv[4 * e + 2 * h] -= mx[h];
+                            sv[4 * e + 2 * h + 1] -= mx[h];
+                        }
+                    }
+                }
+                uint64_t sum[2] = {0ull, 0ull};
+                const int head0 = warp * 16 + hr;
+                const uint32_t prow = sP + b * L::kP + head0 * 128 + 4 * c;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 k = k4[4 * e];
+                    const uint64_t ks = pack_f32x2(k.x, k.y);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float p = ex2_sfu(sv[4 * e + 2 * h] - mr[h]), q = ex2_sfu(sv[4 * e + 2 * h + 1] - mr[h]);
-                        sum[h] += p + q;
-                        const int head = warp * 16 + hr + 8 * h;
-                        if (head < NH)  // the probability that multiplies the codes carries the row scale
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sP + b * L::kP + head * 128 +
-                                                                           ((e ^ (head & 7)) << 4) + 4 * c),
-                                         "r"(bf16x2_rn(p * ks.x, q * ks.y))
+                        const uint64_t p = pack_f32x2(ex2_sfu(sv[4 * e + 2 * h]), ex2_sfu(sv[4 * e + 2 * h + 1]));
+                        sum[h] = add_f32x2(sum[h], p);
+                        float p0, p1;  // the probability that multiplies the codes carries the row scale
+                        unpack_f32x2(mul_f32x2(p, ks), &p0, &p1);
+                        if (NH == 64 || head0 + 8 * h < NH)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + h * 1024 + ((e ^ (hr & 7)) << 4)),
+                                         "r"(bf16x2_rn(p0, p1))
                                          : "memory");
                     }
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) l_run[h] = l_run[h] * alpha[h] + sum[h];
+                for (int h = 0; h < 2; ++h) l_run[h] = fma_f32x2(l_run[h], pack_f32x2(alpha[h], alpha[h]), sum[h]);
             }
             if (c == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (warp * 16 + hr + 8 * h < NH) s_alpha[b * NH + warp * 16 + hr + 8 * h] = alpha[h];
+                    if (NH == 64 || warp * 16 + hr + 8 * h < NH) s_alpha[b * NH + warp * 16 + hr + 8 * h] = alpha[h];
             }
             const bool any = __any_sync(0xffffffffu, resc);
             if (lane == 0) s_vote[b * 4 + warp] = any ? 1 : 0;
-            named_bar_sync(2, 128);
-            if (s_vote[b * 4] | s_vote[b * 4 + 1] | s_vote[b * 4 + 2] | s_vote[b * 4 + 3]) {
-                // a head's maximum moved: O^T (after the previous tile's product) times alpha per head
-                ok = ok && mbar_wait_bounded(&pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1, kWaitLimitNs);
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-                        for (int c0 = 0; c0 < NH; c0 += 16) {
-                            float v[16];
-                            tmem_ld16(tO + mt * NH + lane_off + c0, v);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] *= s_alpha[b * NH + c0 + e];
-                            tmem_st16(tO + mt * NH + lane_off + c0, v);
-                        }
-                    }
-                    tmem_wait_st();
-                }
-            }
             fence_proxy_async_smem();  // P^T stores -> async proxy
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&pfull[b]);
+            if (tid == 0) DSA_TRACE(i, 5);
         }
         if (n_mine > 0) {  // the last product must be complete before O^T is read
+            rescale(n_mine - 1);
             ok = ok && mbar_wait_bounded(&pvdone[(n_mine - 1) & 1], ((n_mine - 1) >> 1) & 1, kWaitLimitNs);
             tc_fence_after();
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int head = warp * 16 + hr + 8 * h;
-            const float l = quad_sum(l_run[h]);
+            float l0, l1;
+            unpack_f32x2(l_run[h], &l0, &l1);
+            const float l = quad_sum(l0 + l1);
             if (c == 0 && head < NH) {
                 // a NaN among masked or absent maxima only: give the partial a weight, so that the NaN reaches the row
                 s_own[head] = m_run[h] == -INFINITY && l != l ? 0.f : m_run[h];
@@ -599,3 +676,5 @@ dsa_status_t launch_attn_fp4(const AttnArgs& a, int hg, int cl, bool fused, cuda
 }
 
 }  // namespace dsa
+
+DSA_TIMELINE_SETTER(dsa_timeline_attention_fp4)

@@ -490,3 +490,19 @@ def test_attention_over_block_rows(name):
     assert int(status) == 0
     rows = None if case["nq"] <= 60 else list(range(0, case["nq"], 7)) + [case["nq"] - 1]
     _check(out, lse, _expected(case, rows))
+
+
+@gpu
+@pytest.mark.parametrize("name", ["ragged", "dense", "prefill_few", "heads128"])
+def test_attention_when_the_running_maximum_moves(name):
+    """Queries 12 times as long: the maxima of later tiles exceed the earlier ones by more than the lazy margin, for some
+    heads and not for others (every fourth head keeps its length), so accumulated outputs are rescaled."""
+    spec = ATTN[name]
+    case = _attn_case(spec, "random" if spec.topk else None, seed=spec.seed)
+    long = torch.full((spec.heads, 1), 12.0)
+    long[::4] = 1.0
+    case["q"] = (case["q"].float() * long).to(torch.bfloat16)
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    _check(out, lse, _expected(case))
