@@ -175,6 +175,7 @@ struct ClSmem {
     static_assert(3 * kTile <= kQ, "the sent tiles fit in the query rows");
     static_assert(6 * kTile <= kQ + kClStages * kClStage, "the received tiles fit after them");
     static_assert(NH * 128 * 2 <= 2 * kP, "an output tile must fit in the P^T buffers");
+    static __host__ __device__ constexpr int stat(int rank, int h) { return kOffStat + (rank * NH + h) * 16; }
     static constexpr int kTmemCols = 512;  // S: [2 buffers][4 parts][32 keys]; O^T: [4 tiles][NH heads]
 };
 
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
 }
 
 // Split plans, shared by the workspace query and the launch: one cluster of `cl` CTAs per (row, head group, split)
-// over sub-tiles of 32 keys (4-bit rows: tiles of 64): clusters of 4
+// over sub-tiles of 32 keys (4-bit rows: tiles of 48): clusters of 4
 // while four CTAs per row still fit on the GPU at once, then 2, then 1; a row splits further only when
 // its clusters leave SMs idle, and never below two sub-tiles per CTA.
 struct SplitPlan {
@@ -960,10 +961,9 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
         a.scores = fz->scores;
         a.score_ld = fz->ld;
         a.n_valid = fz->n_valid;
-        if (fp4) return launch_attn_fp4(a, p.hg, p.cl, true, st);
         return fp8 ? launch_attn_cl<64, true, true>(a, p.cl, st) : launch_attn_cl<64, false, true>(a, p.cl, st);
     }
-    if (fp4) return launch_attn_fp4(a, p.hg, p.cl, false, st);
+    if (fp4) return launch_attn_fp4(a, p.hg, p.cl, st);
     if (!fp8) {
         switch (p.hg) {
             case 16: return launch_attn_cl<16, false>(a, p.cl, st);
@@ -1026,7 +1026,7 @@ extern "C" dsa_status_t dsa_topk_sparse_attn_decode(
     if (heads != 16 && heads != 32 && heads != 64 && heads != 128) return DSA_ERR_UNSUPPORTED;
     if (window < 1 || window > 1024) return DSA_ERR_INVALID_ARG;
     const SplitPlan p = plan_for(batch, heads, k + window, main->dtype);
-    if (!fusable(p, heads, ld, k)) {  // two launches: the top-k, then the attention over its output
+    if (main->dtype == DSA_FP4_BLOCK || !fusable(p, heads, ld, k)) {  // two launches: the top-k, then the attention over its output
         const dsa_status_t e = dsa_topk(batch, scores, ld, n_visible, k, topk_out, dev_status, stream);
         if (e != DSA_OK) return e;
         return sparse_attn(batch, heads, q, q_pos, nullptr, kind, topk_out, k, main, main_bt, swa, swa_bt, window,

@@ -99,7 +99,6 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int* s_vote = reinterpret_cast<int*>(smem + L::kOffVote);
     float* s_own = reinterpret_cast<float*>(smem + L::kOffOwn);
-    float* s_stat = reinterpret_cast<float*>(smem + L::kOffStat);
     float* s_fac = reinterpret_cast<float*>(smem + L::kOffFac);  // [4][NH]: weight of each CTA's partial
     float* s_inv = s_fac + 4 * NH;
     float* s_M = s_inv + NH;
@@ -165,11 +164,11 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
         for (int b = 0; b < (csize - 1) * tiles_per; ++b) mbar_arrive_expect_tx(&xfull[b], (uint32_t)L::kTile);
     const float fo = *s_fault ? 1.f : 0.f;  // this CTA met a device fault: the whole row is written as zeros
     for (int h = tid; h < NH; h += kClThreads) {
-        const uint32_t dst = smem_u32(s_stat + (crank * NH + h) * 4);
+        const uint32_t dst = smem_u32(smem + L::stat(crank, h));
         const float mo = have ? s_own[h] : -INFINITY, lo = have ? s_own[NH + h] : 0.f,
                     eo = have ? s_own[2 * NH + h] : 0.f;
         if (csize == 1)
-            *reinterpret_cast<float4*>(s_stat + h * 4) = make_float4(mo, lo, eo, fo);
+            *reinterpret_cast<float4*>(smem + L::stat(0, h)) = make_float4(mo, lo, eo, fo);
         else
             for (int q = 0; q < csize; ++q)
                 st_cluster_v4(mapa_shared(dst, (uint32_t)q), mo, lo, eo, fo);
@@ -207,7 +206,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
     if (tid < NH * 4) {
         const int h = tid >> 2, qq = tid & 3;
         const bool in = qq < csize;
-        const float4 st = in ? *reinterpret_cast<const float4*>(s_stat + (qq * NH + h) * 4)
+        const float4 st = in ? *reinterpret_cast<const float4*>(smem + L::stat(qq, h))
                              : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         float M = fmaxf(st.x, __shfl_xor_sync(0xffffffffu, st.x, 1));
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
@@ -259,10 +258,11 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
         inv[e] = b4.x, inv[e + 1] = b4.y, inv[e + 2] = b4.z, inv[e + 3] = b4.w;
         fown[e] = a4.x, fown[e + 1] = a4.y, fown[e + 2] = a4.z, fown[e + 3] = a4.w;
     }
-    // output staging: two buffers of [NH][128] bf16 (the P^T buffers, and key stages that no received tile uses,
-    // idle by now), each stored by one TMA box
+    // output staging: a buffer of [NH][128] bf16 for each owned tile (the P^T buffers, and key stages that no received
+    // tile uses, idle by now), each stored by one TMA box
     uint8_t* const ob0 = smem + L::kOffP;
     uint8_t* const ob1 = smem + L::kOffOut1;
+    static_assert(L::kOffOut1 + 3 * NH * 256 <= L::kOffP, "the other tiles' buffers end before the P^T buffers");
     const int firstd = kD - a.rope.rope_dim;
     const bool odd = lane & 1;
     float v_next[G];  // the next owned tile's columns, loaded from TMEM while this one is finished and stored
@@ -316,11 +316,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
             }
         }
         if (a.nsplit == 1) {
-            if (j >= 2) {  // this buffer's previous box has been read out
-                if (tid == 0) bulk_wait_read<1>();
-                __syncthreads();
-            }
-            uint8_t* const obuf = (j & 1) ? ob1 : ob0;
+            uint8_t* const obuf = j == 0 ? ob0 : ob1 + (j - 1) * (NH * 256);
             uint32_t* o32 = reinterpret_cast<uint32_t*>(obuf);
             const int De = D & ~1;  // the pair's even dim
             float rc = 1.f, rs = 0.f;
@@ -413,11 +409,11 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
 }
 
 // The kernel over DSA_FP4_BLOCK rows (attention_fp4.cu) for a plan of cl CTAs per cluster, heads per CTA hg.
-dsa_status_t launch_attn_fp4(const AttnArgs& a, int hg, int cl, bool fused, cudaStream_t st);
+dsa_status_t launch_attn_fp4(const AttnArgs& a, int hg, int cl, cudaStream_t st);
 // Tensor maps of the query rows and of the output (attention.cu).
 bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, int box_rows);
 bool make_out_map(CUtensorMap* map, void* base, uint64_t rows, int box_rows, bool e4m3);
 cudaError_t launch_attn_combine(const AttnArgs& a, cudaStream_t st);
-constexpr int kFp4Keys = 64;  // keys per tile of that kernel
+constexpr int kFp4Keys = 48;  // keys per tile of that kernel
 
 }  // namespace dsa

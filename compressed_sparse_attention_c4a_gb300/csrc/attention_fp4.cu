@@ -12,63 +12,97 @@
 namespace dsa {
 
 // Work split as the bf16 kernel (attention.cu): a cluster of CL CTAs per (query row, group of NH <= 64 heads, key split),
-// tile i of a CTA being the split's tile crank + CL i of 64 keys.  Inside a CTA, 16 warps:
-//   warps 8-15  widen: each owns 8 keys of every tile.  Lanes 0-7 resolve the keys (top-k index -> block table -> row)
-//               two tiles ahead, every lane loads 8 code bytes and one block scale of each row straight into registers
-//               (two tiles in flight, nothing staged), and once the key stage is free (its P V is done) the codes become
-//               bf16 and are stored 128B-swizzled as [64-dim chunk][64 keys][128 B];
-//   warp 4      S = Q K^T (M = 64 heads, N = 64 keys);
-//   warp 5      O^T += V^T P^T (four tiles of M = 128 dims, N = NH heads, K = 64 keys);
-//   warps 0-3   softmax: 16 heads a warp, a head's 64 logits over the 4 lanes of a quad (the 16-lane TMEM load spreads a
+// tile i of a CTA being the split's tile crank + CL i of 48 keys.  Inside a CTA, 16 warps:
+//   warps 8-15  widen: each owns 6 keys of every tile.  Lanes 0-5 resolve the keys (top-k index -> block table -> row)
+//               ahead; the rows' bytes are copied into shared memory with cp.async, each quarter of the warp's share
+//               again as soon as it is converted, so a tile's copies have a whole tile's time; the codes become bf16
+//               and are stored 128B-swizzled as [64-dim chunk][48 keys][128 B], the first 256 dims, then the others;
+//   warps 4, 6  S = Q K^T (M = 64 heads, N = 48 keys) of even and odd tiles;
+//   warp 5      O^T += V^T P^T (four tiles of M = 128 dims, N = NH heads, K = 48 keys);
+//   warps 0-3   softmax: 16 heads a warp, a head's 48 logits over the 4 lanes of a quad (the 16-lane TMEM load spreads a
 //               row over a quad, so every lane works although M = 64 fills 16 of the 32 TMEM lanes).
-// Two key stages, two S and two P buffers: S of tile i + 1 and the widening of tile i + 2 overlap the softmax and P V of i.
-// A 64-key tile reads Q (64 KB) half as often per key as a 32-key one and issues N = 64 products, whose rate is the tensor
-// pipe's and not the issuing warp's.
-constexpr int kFp4Stage = kFp4Keys * kD * 2;
-constexpr int kFp4Widen = 8;                           // widening warps
+// The widened keys are a ring of five half-tiles (48 keys x 256 dims): S starts on the first half, P V frees it first.  Two
+// S and two P buffers.  A tile passes through four hands (widen, S, softmax, P V), each hand-over costing 250 to 400
+// cycles: with two stages of 64 keys that chain, and not any unit, set the pace.  The rows go through shared memory and
+// not straight into registers: 227 KB of shared memory leave the L1 cache about 220 lines, which the rows of one tile fill,
+// and further loads wait for lines when they are issued.
+constexpr int kFp4Ring = 5;                            // half-tiles
+constexpr int kFp4Half = kFp4Keys * (kD / 2) * 2;
+constexpr int kFp4Chunk = kFp4Keys * 128;              // bytes of a 64-dim chunk
+constexpr int kFp4Tiles = 3;                           // tiles whose scales and masks are kept
+constexpr int kFp4Widen = 8;                           // widening warps, two on each of the SM's four schedulers
 constexpr int kFp4PerWarp = kFp4Keys / kFp4Widen;      // keys of a tile per widening warp
-constexpr int kFp4WidenThreads = 32 * kFp4Widen;
-static_assert(kFp4PerWarp == 8, "lanes 0-7 resolve a warp's keys, its bits are one byte of the tile's mask");
+constexpr int kFp4Pairs = kFp4PerWarp / 2;             // a warp converts two rows at a time
+constexpr int kFp4Groups = kFp4Keys / 8;               // groups of 8 keys (the softmax's columns)
+constexpr uint64_t kFp4AllValid = 0x3F3F3F3F3F3F3F3Full;  // a mask byte per widening warp, a bit per key
+static_assert(kFp4PerWarp == 6, "six mask bits a warp");
 // Widened values carry 2^-8: e2m1 bits placed in a bf16 are 2^-126 of the value, and the factor that undoes it times a
 // block scale of up to 448 must stay below 2^128, so it is 2^118.
 constexpr int kFp4Shift = 8;
 
+// Bounded wait (2 s of %globaltimer).  The try suspends the warp in hardware for up to kSuspendNs at a time: measured,
+// spinning on the default, short suspension, the waiting warps took a quarter of all issue slots from the softmax and the
+// widening.
+constexpr uint32_t kSuspendNs = 100000;
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+    const uint32_t addr = smem_u32(bar);
+    auto attempt = [&]() {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        return done != 0;
+    };
+    if (attempt()) return true;
+    const uint64_t t0 = global_ns();
+    while (!attempt())
+        if (global_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
+
 template <int NH>
 struct Fp4Smem {
     static constexpr int kQ = 64 * kD * 2;                          // [8][64 rows][128 B]
-    static constexpr int kP = NH * 128;                             // [NH rows][64 keys] bf16
+    static constexpr int kP = NH * 128;                             // [NH rows][64 keys] bf16, keys 0 .. 47 used
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kOffQ + kQ;                        // key stages; received tiles
-    static constexpr int kOffP = kOffK + 2 * kFp4Stage;             // two P^T buffers; output staging at the end
-    static constexpr int kOffKsc = kOffP + 2 * kP;                  // float [2][32][4]: see s_ksc
-    static constexpr int kOffMask = kOffKsc + 2 * kFp4Keys * 8;     // uint64 [2]: valid keys of a stage
-    static constexpr int kOffAlpha = kOffMask + 16;                 // float [2][NH]
+    static constexpr int kOffK = kOffQ + kQ;                        // ring of widened half-tiles; received tiles
+    static constexpr int kOffP = kOffK + kFp4Ring * kFp4Half;       // two P^T buffers; output staging at the end
+    static constexpr int kOffRaw = kOffP + 2 * kP;                  // [48 keys][288 B]: a tile's rows as stored
+    static constexpr int kOffKsc = kOffRaw + kFp4Keys * kFp4BlockRow;  // float [3][24][4]: see s_ksc
+    static constexpr int kOffMask = kOffKsc + kFp4Tiles * kFp4Keys * 8;  // uint8 [3][8]: valid keys of each widening warp
+    static constexpr int kOffAlpha = kOffMask + 32;                 // float [2][NH]
     static constexpr int kOffVote = kOffAlpha + 2 * NH * 4;         // int [2][4]
-    static constexpr int kOffOwn = kOffVote + 32;                   // float m[NH], l[NH], e[NH] of this CTA
-    static constexpr int kOffStat = kOffOwn + 3 * NH * 4;           // float [4 ranks][NH][4]: (m, l, e, fault)
-    static constexpr int kOffFac = kOffStat + 4 * NH * 16;          // float f[4 ranks][NH], 1/L, M, L, E [NH]
-    static constexpr int kOffBt = kOffFac + 8 * NH * 4;             // int [kBtCache]: the request's main block table
-    static constexpr int kOffSwb = kOffBt + kBtCache * 4;           // int [8]: window-pool blocks from that of wlo
-    static constexpr int kOffFault = kOffSwb + 32;                  // int: a key of this CTA hit a device fault
+    static constexpr int kOffFault = kOffVote + 32;                 // int: a key of this CTA hit a device fault
     static constexpr int kOffRope = kOffFault + 16;                 // float [32][2]: cos, sin of each pair's angle at m
-    static constexpr int kOffBar = kOffRope + 256;                  // 14 mbarriers, TMEM address
-    static constexpr int kOffXfull = kOffBar + 11 * 8;              // the last three: received tile slots
-    static constexpr int kOffTopk = kOffBar + 14 * 8 + 16;          // int [kFusedK]: the row's top-k (fused)
-    static constexpr int kBytes = kOffTopk + kFusedK * 4;
-    static constexpr int kAlloc = kBytes + 1024;                    // + alignment slack
-    static constexpr int kOffOut1 = kOffK + kFp4Stage;              // second output staging buffer (the second stage)
+    static constexpr int kBars = 2 * kFp4Ring + 10;
+    static constexpr int kOffBar = kOffRope + 256;                  // kBars mbarriers, TMEM address
+    static constexpr int kOffXfull = kOffBar + (kBars - 3) * 8;     // the last three: received tile slots
+    static constexpr int kBytes = kOffBar + kBars * 8 + 16;
+    static constexpr int kAlloc = kBytes;                           // the base is declared 1024-byte aligned
     static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
-    static_assert(kOffKsc % 16 == 0 && kOffMask % 16 == 0 && kOffAlpha % 16 == 0 && kOffVote % 16 == 0 &&
-                      kOffOwn % 16 == 0 && kOffStat % 16 == 0 && kOffFac % 16 == 0 && kOffBt % 16 == 0 &&
-                      kOffSwb % 16 == 0 && kOffFault % 16 == 0 && kOffRope % 16 == 0 && kOffBar % 16 == 0 &&
-                      kOffTopk % 16 == 0,
-                  "shared-memory regions 16-byte aligned");
     static constexpr int kTile = 128 * NH * 2;                      // one exchanged 128-dim O tile: [NH / 4][128] x 4 bf16
+    // after the last product: the other output staging buffers, m, l, e and the weights, in the idle ring
+    static constexpr int kOffOut1 = kOffK + 49152;
+    static constexpr int kOffOwn = kOffOut1 + 3 * NH * 256;         // float m[NH], l[NH], e[NH] of this CTA
+    static constexpr int kOffFac = kOffOwn + 3 * NH * 4;            // float f[4 ranks][NH], 1/L, M, L, E [NH]
+    static_assert(kOffFac + 8 * NH * 4 <= kOffP, "within the ring");
     static_assert(3 * kTile <= kQ, "the sent tiles fit in the query rows");
-    static_assert(6 * kTile <= kQ + kFp4Stage, "the received tiles fit before the second output buffer");
+    static_assert(6 * kTile <= kQ + 49152, "the received tiles end before the second output buffer");
     static_assert(NH * 128 * 2 <= 2 * kP, "an output tile must fit in the P^T buffers");
-    static_assert(sizeof(TopkRowScratch<kClThreads, kFusedVpt, 4>) <= 2 * kFp4Stage, "the fused top-k's scratch");
-    static constexpr int kTmemCols = 512;  // S: [2 buffers][64 keys]; O^T: [4 tiles][NH heads]
+    // (m, l, e, fault) of rank c's head h, written by that rank while this CTA may still be multiplying: the two 16-byte
+    // pieces of a P^T row behind its 48 keys, which no product reads, in each of the two buffers
+    static __host__ __device__ constexpr int stat(int c, int h) {
+        return kOffP + (c >> 1) * kP + h * 128 + (((6 + (c & 1)) ^ (h & 7)) << 4);
+    }
+    static_assert(kOffKsc % 16 == 0 && kOffMask % 16 == 0 && kOffAlpha % 16 == 0 && kOffVote % 16 == 0 &&
+                      kOffOwn % 16 == 0 && kOffFac % 16 == 0 && kOffFault % 16 == 0 && kOffRope % 16 == 0 &&
+                      kOffBar % 16 == 0 && kOffOut1 % 1024 == 0,
+                  "shared-memory regions 16-byte aligned");
+    static constexpr int kTmemCols = 512;  // S: [2 buffers][64 columns, 48 used]; O^T: [4 tiles][NH heads]
 };
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -101,41 +135,53 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t scale, uint32_t (&o)
     o[3] = __byte_perm(g[2], g[3], 0x7632);
 }
 
-// 8 code bytes / one block scale of a row, zero when the key is masked (row < 0).
-__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int row, uint64_t policy) {
-    uint2 c;
+// *p if `in`, else -1, in the register that will be used: a branch or a copy around the load would wait for it here, and an
+// ordinary load the compiler moves down to its first use, a tile later.
+__device__ __forceinline__ int load_int_if(const int32_t* p, bool in) {
+    int v;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %4, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
-        "@p ld.global.L1::no_allocate.L2::cache_hint.v2.u32 {%0, %1}, [%2], %3;\n\t}"
-        : "=&r"(c.x), "=&r"(c.y)
-        : "l"(p), "l"(policy), "r"(row)
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, -1;\n\t@p ld.global.b32 %0, [%1];\n\t}"
+        : "=&r"(v)
+        : "l"(p), "r"((uint32_t)in)
         : "memory");
-    return c;
-}
-__device__ __forceinline__ uint32_t load_block_scale(const uint8_t* p, int row, uint64_t policy) {
-    uint32_t b;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %3, 0;\n\tmov.u32 %0, 0;\n\t"
-        "@p ld.global.L1::no_allocate.L2::cache_hint.u8 %0, [%1], %2;\n\t}"
-        : "=&r"(b)
-        : "l"(p), "l"(policy), "r"(row)
-        : "memory");
-    return b;
+    return v;
 }
 
-// 64 columns of a 16-lane accumulator (M = 64): lane 4 r + c of the warp gets, for row r and r + 8, columns
+__device__ __forceinline__ float load_float_if(const float* p, bool in) {  // 0 if not
+    float v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t@p ld.global.f32 %0, [%1];\n\t}"
+        : "=&f"(v)
+        : "l"(p), "r"((uint32_t)in)
+        : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// 48 columns of a 16-lane accumulator (M = 64): lane 4 r + c of the warp gets, for row r and r + 8, columns
 // 8 i + 2 c, 8 i + 2 c + 1 in registers 4 i, 4 i + 1 and 4 i + 2, 4 i + 3.  Valid after tmem_wait_ld().
-__device__ __forceinline__ void tmem_ld_16x64_nowait(uint32_t taddr, float (&v)[32]) {
+__device__ __forceinline__ void tmem_ld_16x48_nowait(uint32_t taddr, float (&v)[24]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23])
+                 : "r"(taddr + 32)
+                 : "memory");
 }
 
 // Two fp32 values in one register pair (packed arithmetic halves the instructions of the softmax).
@@ -172,30 +218,29 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-template <int NH, bool FUSED>
+template <int NH>
 __global__ void __launch_bounds__(kClThreads, 1)
     attn_fp4_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap, AttnArgs a) {
     using L = Fp4Smem<NH>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sP = smem_u32(smem + L::kOffP);
     // the row scales of keys 2 p and 2 p + 1 of a stage, then the same times sm_scale log2(e)
     float* s_ksc = reinterpret_cast<float*>(smem + L::kOffKsc);
     uint8_t* s_mask8 = smem + L::kOffMask;
     float* s_alpha = reinterpret_cast<float*>(smem + L::kOffAlpha);
     int* s_vote = reinterpret_cast<int*>(smem + L::kOffVote);
-    float* s_own = reinterpret_cast<float*>(smem + L::kOffOwn);
-    // tile i: key stage, S columns and P^T buffer i & 1
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // [2] stage widened (widening warps)
-    uint64_t* sfull = full + 2;                                         // [2] S in TMEM
+    // half h of tile i: ring slot (2 i + h) % 5; scales and mask i % 3; S columns and P^T buffer i & 1
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // [5] widened (widening warps)
+    uint64_t* pvdone = full + kFp4Ring;                                 // [5] multiplied into O^T
+    uint64_t* sfull = pvdone + kFp4Ring;                                // [2] S in TMEM
     uint64_t* pfull = sfull + 2;                                        // [2] P^T written (4 softmax warps)
-    uint64_t* pvdone = pfull + 2;                                       // [2] O^T += V^T P^T done
-    uint64_t* qfull = pvdone + 2;                                       // query rows loaded
+    uint64_t* qfull = pfull + 2;                                        // query rows loaded
     uint64_t* rdone = qfull + 1;                                        // O^T rescaled (4 softmax warps)
     uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + L::kOffXfull);  // [3] each received tile slot loaded
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(xfull + 3);
     volatile int* s_fault = reinterpret_cast<volatile int*>(smem + L::kOffFault);
     float* s_rc = reinterpret_cast<float*>(smem + L::kOffRope);
+    float* s_own = reinterpret_cast<float*>(smem + L::kOffOwn);  // written after the last product
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int crank = (int)cluster_ctarank(), csize = (int)cluster_nctarank();
@@ -204,11 +249,14 @@ __global__ void __launch_bounds__(kClThreads, 1)
     const int hg = (cid / a.nsplit) % a.hg_count;
     const int row = cid / (a.nsplit * a.hg_count);
     if (tid == 0) {
-        for (int b = 0; b < 2; ++b) {
+        DSA_STAMP(0);
+        for (int b = 0; b < kFp4Ring; ++b) {
             mbar_init(&full[b], kFp4Widen);
+            mbar_init(&pvdone[b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 1);
             mbar_init(&pfull[b], 4);
-            mbar_init(&pvdone[b], 1);
         }
         mbar_init(qfull, 1);
         mbar_init(rdone, 4);
@@ -227,36 +275,23 @@ __global__ void __launch_bounds__(kClThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const uint32_t tS = tmem, tO = tmem + 2 * kFp4Keys;
+    if (tid == 0) DSA_STAMP(1);
+    const uint32_t tS = tmem, tO = tmem + 128;
     if (csize > 1) cluster_arrive_relaxed();  // phase 0: this CTA has started (waited on before DSMEM use)
 
     // Position, request, block tables and query rows: inputs that no kernel of the layer step writes, read while the
     // preceding kernel finishes.  Top-k indices, cache rows and every output come after the wait.
     const int r = a.q_req ? a.q_req[row] : row;
-    const int ww = warp - 8, gt = tid - 256;  // widening warp and thread
-    const bool bt_cached = a.main_bt.max_blocks <= kBtCache;
-    constexpr int kBtPer = kBtCache / kFp4WidenThreads;
-    int btv[kBtPer];
-    if (ww >= 0) {
-        const bool r_in = bt_cached && r >= 0 && r < a.main_bt.batch;
-#pragma unroll
-        for (int u = 0; u < kBtPer; ++u) {
-            const int b = gt + u * kFp4WidenThreads;
-            btv[u] = r_in && b < a.main_bt.max_blocks ? __ldg(a.main_bt.table + (long long)r * a.main_bt.max_blocks + b) : -1;
-        }
-    }
     const int m = a.q_pos[row];
     const bool row_ok = r >= 0 && r < a.main_bt.batch && r < a.swa_bt.batch && m >= 0;
     if (!row_ok && tid == 0) *s_fault = 1;
     const int n_vis = row_ok ? entries_formed((long long)m + 1, a.kind_w, a.kind_s) : 0;
-    const int n_comp = (FUSED || a.topk) ? a.k : n_vis;
+    const int n_comp = a.topk ? a.k : n_vis;
     const int wlo = max(0, m - a.window + 1);
     const int n_keys = row_ok ? n_comp + (m - wlo + 1) : 0;
     const int n_tiles = (n_keys + kFp4Keys - 1) / kFp4Keys;
     const int g_lo = split * a.cps, g_hi = min(n_tiles, g_lo + a.cps);
     const int n_mine = g_hi > g_lo + crank ? (g_hi - g_lo - crank + csize - 1) / csize : 0;
-    int* s_bt = reinterpret_cast<int*>(smem + L::kOffBt);
-    int* s_swb = reinterpret_cast<int*>(smem + L::kOffSwb);
     if (warp == 0 && lane < a.rope.rope_dim / 2) {  // R_m^-1 of the output: cos and sin of each pair's angle at m
         float c = 1.f, sn = 0.f;
         if (row_ok) rope_cos_sin(m, a.rope, lane, &c, &sn);
@@ -270,166 +305,151 @@ __global__ void __launch_bounds__(kClThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(qfull);
     }
-    int swbv = -1;
-    if (ww >= 0 && gt < 8 && n_mine > 0) {
-        const int lb = wlo / kBlockPositions + gt;
-        if (row_ok && lb <= m / kBlockPositions && lb < a.swa_bt.max_blocks)
-            swbv = __ldg(a.swa_bt.table + (long long)r * a.swa_bt.max_blocks + lb);
-    }
-    auto store_tables = [&]() {  // by the widening warps; a key then resolves with one global load at most
-        if (bt_cached)
-#pragma unroll
-            for (int u = 0; u < kBtPer; ++u) {
-                const int b = gt + u * kFp4WidenThreads;
-                if (b < a.main_bt.max_blocks) s_bt[b] = btv[u];
-            }
-        if (gt < 8) s_swb[gt] = swbv;
-        named_bar_sync(1, kFp4WidenThreads);
-    };
-    if constexpr (FUSED) {
-        if (ww >= 0 && n_mine > 0) store_tables();
-    }
     pdl_wait();  // global memory the preceding kernel writes, and every output, only below
     pdl_launch_dependents();
+    if (tid == 0) DSA_STAMP(2);
     if (!row_ok && tid == 0 && crank == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
-    int* s_topk = reinterpret_cast<int*>(smem + L::kOffTopk);
-    if constexpr (FUSED) {
-        // the row's top-k of the indexer scores on this cluster (one cluster of four CTAs per row), every selected
-        // entry written into each CTA's s_topk (and topk_out); its scratch is the key stages, idle until then.  Its
-        // first cluster barrier completes phase 0.
-        cg::cluster_group cluster = cg::this_cluster();
-        cluster_wait();
-        auto& ts = *reinterpret_cast<TopkRowScratch<kClThreads, kFusedVpt, 4>*>(smem + L::kOffK);
-        int32_t* tout = a.topk_out + (long long)row * a.k;
-        auto emit = [&](int pos, int idx) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) *cluster.map_shared_rank(s_topk + pos, c) = idx;
-            tout[pos] = idx;
-        };
-        const int nv_row = a.n_valid[row];  // the same in every CTA of the cluster
-        if (nv_row < 0 || nv_row > a.score_ld) {
-            if (tid == 0 && crank == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
-            for (int i = crank * kClThreads + tid; i < a.k; i += 4 * kClThreads) emit(i, -1);
-        } else {
-            topk_row_cluster<kClThreads, kFusedVpt, 4>(cluster, ts, a.scores + (long long)row * a.score_ld, nv_row,
-                                                       a.k, emit, a.status, 23);
-        }
-        cluster.sync();  // every CTA's s_topk complete; the scratch (key stages) no longer read by a peer
-    }
     bool ok = true;
 
-    if (ww >= 0) {
+    if (warp >= 8) {
         // ---- widening warps ----------------------------------------------------------------------------
-        // decode rows (one query row per request): a gathered row serves this query row only and leaves L2 first
-        const uint64_t policy = a.q_req ? l2_evict_normal() : l2_evict_first();
-        // lane u < 8: key u of the warp's 8 in tile i.  Step 1: its top-k index (no dependent load).
-        auto key_id = [&](int i, int* id) -> int {  // the key's index in the row, -1 if there is none
-            *id = -1;
-            if (lane >= kFp4PerWarp || i >= n_mine) return -1;
+        const int ww = warp - 8;
+        // A key is resolved in three steps, a tile apart, so that no load waits for another: lanes 0-5, key `lane` of the
+        // warp's 6 in tile i, j its index in the row (-1: none).  Step 1: its entry (top-k index; -1: none) or position.
+        const int main_shift = __ffs(a.main.rows_per_block) - 1;  // 64 or 2 rows a block; the window's 256
+        const int32_t* const row_topk = a.topk + (long long)row * a.k;
+        auto key_index = [&](int i) -> int {
             const int j = (g_lo + crank + csize * i) * kFp4Keys + ww * kFp4PerWarp + lane;
-            if (j < n_comp) *id = FUSED ? s_topk[j] : (a.topk ? __ldg(a.topk + (long long)row * a.k + j) : j);
-            return j < n_keys ? j : -1;
+            return lane < kFp4PerWarp && i < n_mine && j < n_keys ? j : -1;
         };
-        // Step 2: index -> pool row (-1: none), and whether the pool is the window's.
-        auto key_row = [&](int j, int id, bool* window) -> int {
-            *window = j >= n_comp;
-            if (j < 0) return -1;
-            int pb, nb, at, epb;  // physical block, blocks of the pool, row within the block, rows of a block
-            if (j < n_comp) {
-                if (id < 0) return -1;
-                epb = a.main.rows_per_block, nb = a.main.num_blocks;
-                const int lb = id / epb;
-                const bool in = id < n_vis && lb < a.main_bt.max_blocks && (!bt_cached || DSA_IDX_OK(lb, kBtCache, a.status));
-                pb = !in ? -1 : bt_cached ? s_bt[lb] : __ldg(a.main_bt.table + (long long)r * a.main_bt.max_blocks + lb);
-                at = id - lb * epb;
-            } else {
-                const int pos = wlo + (j - n_comp), lb = pos / kBlockPositions;
-                const int sb = lb - wlo / kBlockPositions;  // the window (<= 1024 positions) spans <= 5 blocks
-                epb = kBlockPositions, nb = a.swa.num_blocks;
-                pb = DSA_IDX_OK(sb, 8, a.status) ? s_swb[sb] : -1;
-                at = pos - lb * kBlockPositions;
-            }
-            if (pb < 0 || pb >= nb) {
+        auto key_entry = [&](int j) -> int { return load_int_if(row_topk + max(j, 0), a.topk && j >= 0 && j < n_comp); };
+        auto key_id = [&](int j, int entry) -> int { return j >= n_comp ? wlo + (j - n_comp) : (a.topk ? entry : j); };
+        // Step 2: the physical block, from the block table (-1: unmapped, beyond the table or not visible).
+        auto key_block = [&](int j, int id) -> int {
+            const bool window = j >= n_comp;
+            const dsa_block_table_t& bt = window ? a.swa_bt : a.main_bt;
+            const int lb = max(id, 0) >> (window ? 8 : main_shift);
+            return load_int_if(bt.table + (long long)r * bt.max_blocks + lb,
+                               j >= 0 && id >= 0 && (window || id < n_vis) && lb < bt.max_blocks);
+        };
+        // Step 3: the pool row (-1: none).
+        auto key_row = [&](int j, int id, int block) -> int {
+            if (j < 0 || id < 0) return -1;
+            const bool window = j >= n_comp;
+            if (block < 0 || block >= (window ? a.swa.num_blocks : a.main.num_blocks)) {
                 report(a.status, DSA_ERR_DEVICE_FAULT);
                 *s_fault = 1;
                 return -1;
             }
-            return pb * epb + at;
+            const int shift = window ? 8 : main_shift;
+            return (block << shift) + (id & ((1 << shift) - 1));
         };
-        const uint8_t* const main_lane = static_cast<const uint8_t*>(a.main.data) + lane * 8;
-        const uint8_t* const swa_lane = static_cast<const uint8_t*>(a.swa.data) + lane * 8;
-        uint2 code[2][kFp4PerWarp];
-        uint32_t bsc[2][kFp4PerWarp];
-        float ksc[2];         // lanes 0-7: the row scales
-        uint32_t valid[2];    // the warp's 8 mask bits
-        auto issue = [&](int b, int j, int id) {
-            bool window;
-            const int kr = key_row(j, id, &window);
-            valid[b] = __ballot_sync(0xffffffffu, kr >= 0) & 0xffu;
-            const uint32_t wm = __ballot_sync(0xffffffffu, window);
-            ksc[b] = 0.f;
-            if (kr >= 0) ksc[b] = (window ? a.swa.scale : a.main.scale)[kr];
+        // Converting, lane l = 16 q + t: of each pair of the warp's rows row q, and of each half of the dims block t (16 dims:
+        // 16-byte pieces 2 (t & 3), 2 (t & 3) + 1 of 64-dim chunk t >> 2 of the half).  Lanes of odd chunks store their
+        // second piece first, so that eight neighbouring lanes cover all banks.
+        const int q = lane >> 4, t = lane & 15;
+        const uint32_t raw = smem_u32(smem + L::kOffRaw) + ww * (kFp4PerWarp * kFp4BlockRow);
+        const uint32_t raw_codes = raw + q * kFp4BlockRow + t * 8, raw_scale = raw + q * kFp4BlockRow + kD / 2 + t;
+        const int hf = (t >> 2) & 1, p0 = 2 * (t & 3) + hf;
+        uint32_t dst[kFp4Pairs][2];  // where the lane's pieces of its row of each pair go, within a ring slot
 #pragma unroll
-            for (int u = 0; u < kFp4PerWarp; ++u) {
-                const int v = __shfl_sync(0xffffffffu, kr, u);
-                const uint8_t* p = ((wm >> u) & 1 ? swa_lane : main_lane) + (long long)max(v, 0) * kFp4BlockRow;
-                code[b][u] = load_codes(p, v, policy);
-                bsc[b][u] = load_block_scale(p + (kD / 2 - 7 * lane), v, policy);
+        for (int u = 0; u < kFp4Pairs; ++u)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int kk = ww * kFp4PerWarp + 2 * u + q;
+                dst[u][g] = sK + (t >> 2) * kFp4Chunk + (kk >> 3) * 1024 + (kk & 7) * 128 + (((p0 ^ g) ^ (kk & 7)) << 4);
             }
+        // Copying, lanes 0-17: of a pair's row lane / 9, 16-byte piece lane % 9 of a half (8 of codes, one of 16 scales).
+        const int cr = lane >= 9 ? 1 : 0, cp = lane - 9 * cr;
+        const uint32_t cp_off = cp < 8 ? cp * 16 : kD / 2, cp_step = cp < 8 ? kD / 4 : 16;  // half 0, and to half 1
+        uint64_t src[kFp4Pairs];     // global address of the lane's piece (half 0) of the row of each pair
+        uint32_t src_bytes[kFp4Pairs];  // 16, or 0 to fill with zeros (a masked key)
+        // the rows of a tile, by the lanes that own them (kr: pool row or -1): their addresses to the copying lanes
+        auto aim = [&](int kr, bool window) {
+            const uint8_t* data = static_cast<const uint8_t*>(window ? a.swa.data : a.main.data);
+            const uint64_t at = reinterpret_cast<uint64_t>(data) + (uint64_t)max(kr, 0) * kFp4BlockRow;
+            const uint32_t valid = __ballot_sync(0xffffffffu, kr >= 0);
+#pragma unroll
+            for (int u = 0; u < kFp4Pairs; ++u) {
+                src[u] = __shfl_sync(0xffffffffu, at, 2 * u + cr) + cp_off;
+                src_bytes[u] = (valid >> (2 * u + cr)) & 1 ? 16u : 0u;
+            }
+            return valid;
         };
-        // Lane l holds block l (16 dims): 16-byte pieces 2 (l & 3), 2 (l & 3) + 1 of 64-dim chunk l >> 2.  Lanes of odd
-        // chunks store their second piece first, so that eight neighbouring lanes cover all banks.
-        const int hf = (lane >> 2) & 1, p0 = 2 * (lane & 3) + hf;
-        const uint32_t dst0 = sK + (lane >> 2) * (kFp4Keys * 128) + ww * 1024;  // the warp's 8-row group
-        auto widen = [&](int b, int i) {
-            const int st = i & 1;
-            if (i >= 2) ok = ok && mbar_wait_bounded(&pvdone[st], ((i >> 1) - 1) & 1, kWaitLimitNs);  // stage free
-            if (gt == 0) DSA_TRACE(i, 0);
-            if (ok) {
-                if (lane < kFp4PerWarp) {
-                    float* k = s_ksc + st * 2 * kFp4Keys + (ww * kFp4PerWarp + lane) / 2 * 4 + (lane & 1);
-                    k[0] = ksc[b];
-                    k[2] = ksc[b] * a.scale_log2;
-                }
-                if (lane == 0) s_mask8[st * 8 + ww] = (uint8_t)valid[b];
-#pragma unroll
-                for (int u = 0; u < kFp4PerWarp; ++u) {
-                    const uint32_t s2 = block_scale_2p118(bsc[b][u]);
-                    const uint32_t base = dst0 + st * kFp4Stage + u * 128;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t o[4];
-                        widen8((h ^ hf) ? code[b][u].y : code[b][u].x, s2, o);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + (((p0 ^ h) ^ u) << 4)),
-                                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                     : "memory");
-                    }
-                }
-            }
-            fence_proxy_async_smem();  // the bf16 rows -> visible to the tensor core (async proxy)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
-            if (gt == 0) DSA_TRACE(i, 1);
+        auto copy = [&](int h, int u) {  // one group
+            if (lane < 18)
+                cp_async16_nc(raw + (2 * u + cr) * kFp4BlockRow + cp_off + h * cp_step,
+                              reinterpret_cast<const void*>(src[u] + h * cp_step), src_bytes[u]);
+            cp_async_commit();
         };
         if (n_mine > 0) {
-            int id0, id1, id2;
-            const int j0 = key_id(0, &id0), j1 = key_id(1, &id1);
-            if constexpr (!FUSED) store_tables();
-            issue(0, j0, id0);
-            issue(1, j1, id1);
-            int j2 = key_id(2, &id2);
-            // two tiles a turn (register buffers 0 and 1); tiles past the end resolve to nothing and are not widened
-#pragma unroll 1
-            for (int i = 0; i < n_mine; i += 2) {
+            const int j0 = key_index(0), e0 = key_entry(j0), e1 = key_entry(key_index(1));
+            int entry = key_entry(key_index(2));                       // of tile i + 2, loop-carried
+            const int id0 = key_id(j0, e0), b0 = key_block(j0, id0);
+            int id = key_id(key_index(1), e1), block = key_block(key_index(1), id);  // of tile i + 1
+            int kr = key_row(j0, id0, b0);
+            bool window = j0 >= n_comp;
+            uint32_t valid = aim(kr, window);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (i + b < n_mine) {
-                        widen(b, i + b);
-                        issue(b, j2, id2);  // tile i + b + 2
-                        j2 = key_id(i + b + 3, &id2);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < kFp4Pairs; ++u) copy(h, u);
+            float ksc = load_float_if((window ? a.swa.scale : a.main.scale) + max(kr, 0), kr >= 0);
+            int slot = 0, kt = 0;
+            uint32_t lap = 0;  // of the ring
+#pragma unroll 1
+            for (int i = 0; i < n_mine; ++i) {
+                // tile i + 1's rows, whose copies follow each part of tile i that has been converted
+                const int j1 = key_index(i + 1), j2 = key_index(i + 2);
+                kr = key_row(j1, id, block);
+                window = j1 >= n_comp;
+                id = key_id(j2, entry);
+                block = key_block(j2, id);
+                entry = key_entry(key_index(i + 3));
+                const uint32_t mask = valid;
+                const float scale = ksc;
+                valid = aim(kr, window);
+                ksc = load_float_if((window ? a.swa.scale : a.main.scale) + max(kr, 0), kr >= 0);
+                if (ww == 0 && lane == 0) DSA_TRACE(i, 0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (lap > 0) ok = ok && wait_bar(&pvdone[slot], (lap - 1) & 1);
+                    if (h == 0 && ok) {
+                        if (lane < kFp4PerWarp) {
+                            float* k = s_ksc + kt * 2 * kFp4Keys + (ww * kFp4PerWarp + lane) / 2 * 4 + (lane & 1);
+                            k[0] = scale;
+                            k[2] = scale * a.scale_log2;
+                        }
+                        if (lane == 0) s_mask8[kt * 8 + ww] = (uint8_t)mask;
                     }
+#pragma unroll
+                    for (int u = 0; u < kFp4Pairs; ++u) {
+                        cp_async_wait_group<2 * kFp4Pairs - 1>();  // this part of tile i, six groups ago
+                        __syncwarp();
+                        const uint2 code = lds64(raw_codes + 2 * u * kFp4BlockRow + h * (kD / 4));
+                        const uint32_t s2 = block_scale_2p118(lds8(raw_scale + 2 * u * kFp4BlockRow + h * 16));
+                        __syncwarp();
+                        copy(h, u);  // the same part of tile i + 1
+                        if (ok) {
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                uint32_t o[4];
+                                widen8((g ^ hf) ? code.y : code.x, s2, o);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst[u][g] + slot * kFp4Half),
+                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                             : "memory");
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();  // the bf16 rows -> visible to the tensor core (async proxy)
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[slot]);
+                    if (++slot == kFp4Ring) slot = 0, ++lap;
                 }
+                if (++kt == kFp4Tiles) kt = 0;
+                if (ww == 0 && lane == 0) DSA_TRACE(i, 1);
             }
+            cp_async_wait_all();
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
@@ -437,53 +457,64 @@ __global__ void __launch_bounds__(kClThreads, 1)
         // ---- O^T += V^T P^T, issued by one elected lane ------------------------------------------------------
         const uint32_t idesc_o = idesc_bf16(NH, 1, 128);
         uint32_t rescales = 0;
+        int slot = 0;
         for (int i = 0; i < n_mine; ++i) {
             const int b = i & 1;
-            ok = mbar_wait_bounded(&pfull[b], (i >> 1) & 1, kWaitLimitNs);  // P^T written (so S done, the stage full)
+            ok = wait_bar(&pfull[b], (i >> 1) & 1);  // P^T written (so S done, the stage full)
             if (ok && (s_vote[b * 4] | s_vote[b * 4 + 1] | s_vote[b * 4 + 2] | s_vote[b * 4 + 3]))
-                ok = mbar_wait_bounded(rdone, rescales++ & 1, kWaitLimitNs);
+                ok = wait_bar(rdone, rescales++ & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            if (tid == 160) DSA_TRACE(i, 6);
-            const uint64_t dv = sw128_desc(sK + b * kFp4Stage, kFp4Keys * 128, 1024);
+            if (lane == 0) DSA_TRACE(i, 6);
             const uint64_t dp = sw128_desc(sP + b * L::kP, 16, 1024);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t dv = sw128_desc(sK + slot * kFp4Half, kFp4Chunk, 1024);
 #pragma unroll
-                for (int ks = 0; ks < kFp4Keys / 16; ++ks)
-                    mma_bf16_ss_elect(tO + mt * NH,
-                                      dv + (uint64_t)(((2 * mt) * (kFp4Keys * 128) + (2 * ks) * 1024) >> 4),
-                                      dp + (uint64_t)((ks * 32) >> 4), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
-            mma_commit_elect(&pvdone[b]);
-            if (tid == 160) DSA_TRACE(i, 7);
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int ks = 0; ks < kFp4Keys / 16; ++ks)
+                        mma_bf16_ss_elect(tO + (2 * h + mt) * NH,
+                                          dv + (uint64_t)(((2 * mt) * kFp4Chunk + (2 * ks) * 1024) >> 4),
+                                          dp + (uint64_t)((ks * 32) >> 4), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
+                mma_commit_elect(&pvdone[slot]);
+                if (++slot == kFp4Ring) slot = 0;
+            }
+            if (lane == 0) DSA_TRACE(i, 7);
         }
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
-    } else if (warp == 4) {
-        // ---- S = Q K^T, issued by one elected lane -----------------------------------------------------------
+    } else if (warp == 4 || warp == 6) {
+        // ---- S = Q K^T of every other tile, issued by one elected lane (one warp alone issues slower than the tensor
+        // cores multiply) ------------------------------------------------------------------------------------
+        const int b = warp == 6;
         const uint32_t idesc_s = idesc_bf16(kFp4Keys, 0, 64);
         const uint64_t dq = sw128_desc(sQ, 16, 1024);
-        if (n_mine > 0) ok = mbar_wait_bounded(qfull, 0, kWaitLimitNs);
-        for (int i = 0; i < n_mine; ++i) {
-            const int b = i & 1;
-            if (i >= 2) ok = ok && mbar_wait_bounded(&pfull[b], ((i >> 1) - 1) & 1, kWaitLimitNs);  // S buffer read
-            ok = ok && mbar_wait_bounded(&full[b], (i >> 1) & 1, kWaitLimitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            if (tid == 128) DSA_TRACE(i, 2);
-            const uint64_t dk = sw128_desc(sK + b * kFp4Stage, 16, 1024);
+        if (n_mine > b) ok = wait_bar(qfull, 0);
+        for (int i = b; i < n_mine; i += 2) {
+            if (i >= 2) ok = ok && wait_bar(&pfull[b], ((i >> 1) - 1) & 1);  // S buffer read
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
-                const uint64_t off = (uint64_t)((((ks >> 2) * (64 * 128)) + (ks & 3) * 32) >> 4);  // 64-row chunks, both
-                mma_bf16_ss_elect(tS + b * kFp4Keys, dq + off, dk + off, idesc_s, ks > 0 ? 1u : 0u);
+            for (int h = 0; h < 2; ++h) {
+                const int n = 2 * i + h, slot = n % kFp4Ring;
+                ok = ok && wait_bar(&full[slot], (n / kFp4Ring) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0 && h == 0) DSA_TRACE(i, 2);
+                const uint64_t dk = sw128_desc(sK + slot * kFp4Half, 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < kD / 32; ++ks)
+                    mma_bf16_ss_elect(tS + b * 64, dq + (uint64_t)(((((ks >> 2) + 4 * h) * 8192) + (ks & 3) * 32) >> 4),
+                                      dk + (uint64_t)((((ks >> 2) * kFp4Chunk) + (ks & 3) * 32) >> 4), idesc_s,
+                                      h + ks > 0 ? 1u : 0u);
             }
+            if (!ok) break;
             mma_commit_elect(&sfull[b]);
-            if (tid == 128) DSA_TRACE(i, 3);
+            if (lane == 0) DSA_TRACE(i, 3);
         }
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
     } else if (warp < 4) {
-        // ---- softmax warps: heads 16 warp + lane / 4 and + 8, keys 8 i + 2 (lane % 4), + 1 ------------------
+        // ---- softmax warps: heads 16 warp + lane / 4 and + 8, keys 8 e + 2 (lane % 4), + 1 ------------------
         const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
         const int hr = lane >> 2, c = lane & 3;
         // m_run: the head's running maximum, lazy: it moves only when exceeded by more than 2^8, so O^T is rarely
@@ -492,12 +523,13 @@ __global__ void __launch_bounds__(kClThreads, 1)
         uint64_t l_run[2] = {0ull, 0ull};
         // O^T times alpha per head, when a head's maximum moved in tile i: after the other warps' votes for the tile are
         // in (their P^T is written) and the product of tile i - 1 is done; the product of tile i waits for it
+        auto wait_pv = [&](int i) { return wait_bar(&pvdone[(2 * i + 1) % kFp4Ring], ((2 * i + 1) / kFp4Ring) & 1); };
         auto rescale = [&](int i) {
             const int b = i & 1;
-            ok = ok && mbar_wait_bounded(&pfull[b], (i >> 1) & 1, kWaitLimitNs);
+            ok = ok && wait_bar(&pfull[b], (i >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || !(s_vote[b * 4] | s_vote[b * 4 + 1] | s_vote[b * 4 + 2] | s_vote[b * 4 + 3])) return;
-            ok = mbar_wait_bounded(&pvdone[b ^ 1], ((i - 1) >> 1) & 1, kWaitLimitNs);
+            ok = wait_pv(i - 1);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc_fence_after();
@@ -519,21 +551,21 @@ __global__ void __launch_bounds__(kClThreads, 1)
             if (lane == 0) mbar_arrive(rdone);
         };
         for (int i = 0; i < n_mine; ++i) {
-            const int b = i & 1;
+            const int b = i & 1, kt = i % kFp4Tiles;
             if (i > 0) rescale(i - 1);
-            ok = ok && mbar_wait_bounded(&full[b], (i >> 1) & 1, kWaitLimitNs);  // the stage's scales and mask
-            ok = ok && mbar_wait_bounded(&sfull[b], (i >> 1) & 1, kWaitLimitNs);
-            if (i >= 2) ok = ok && mbar_wait_bounded(&pvdone[b], ((i >> 1) - 1) & 1, kWaitLimitNs);  // P^T buffer free
+            ok = ok && wait_bar(&full[2 * i % kFp4Ring], (2 * i / kFp4Ring) & 1);  // the tile's scales and mask
+            ok = ok && wait_bar(&sfull[b], (i >> 1) & 1);
+            if (i >= 2) ok = ok && wait_pv(i - 2);  // P^T buffer free
             ok = __all_sync(0xffffffffu, ok);
             if (tid == 0) DSA_TRACE(i, 4);
             float alpha[2] = {1.f, 1.f};
             bool resc = false;
             if (ok) {
                 tc_fence_after();
-                float sv[32];  // logits of head h in 4 e + 2 h, 4 e + 2 h + 1: keys 8 e + 2 c, + 1
-                tmem_ld_16x64_nowait(tS + b * kFp4Keys + lane_off, sv);
-                const float4* k4 = reinterpret_cast<const float4*>(s_ksc + b * 2 * kFp4Keys) + c;
-                const uint64_t vm = *reinterpret_cast<const uint64_t*>(s_mask8 + b * 8);
+                float sv[24];  // logits of head h in 4 e + 2 h, 4 e + 2 h + 1: keys 8 e + 2 c, + 1
+                tmem_ld_16x48_nowait(tS + b * 64 + lane_off, sv);
+                const float4* k4 = reinterpret_cast<const float4*>(s_ksc + kt * 2 * kFp4Keys) + c;
+                const uint64_t vm = *reinterpret_cast<const uint64_t*>(s_mask8 + kt * 8);
                 float m0[2];  // the logits are taken relative to m0: the running maximum, 0 before the first key
                 uint64_t neg[2];
 #pragma unroll
@@ -542,9 +574,9 @@ __global__ void __launch_bounds__(kClThreads, 1)
                     neg[h] = pack_f32x2(-m0[h], -m0[h]);
                 }
                 tmem_wait_ld();
-                tmem_regs_after_wait<32>(sv);
+                tmem_regs_after_wait<24>(sv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < kFp4Groups; ++e) {
                     const float4 k = k4[4 * e];
                     const uint64_t kl = pack_f32x2(k.z, k.w);
 #pragma unroll
@@ -552,10 +584,11 @@ __global__ void __launch_bounds__(kClThreads, 1)
                         unpack_f32x2(fma_f32x2(pack_f32x2(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]), kl, neg[h]),
                                      &sv[4 * e + 2 * h], &sv[4 * e + 2 * h + 1]);
                 }
-                if (vm != ~0ull) {
+                if (vm != kFp4AllValid) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t bits = (uint32_t)(vm >> (8 * e)) >> (2 * c);
+                    for (int e = 0; e < kFp4Groups; ++e) {
+                        const int kk = 8 * e + 2 * c;  // and kk + 1: the same warp's, six keys being three pairs
+                        const uint32_t bits = (uint32_t)(vm >> (kk / kFp4PerWarp * 8 + kk % kFp4PerWarp));
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             if (!(bits & 1)) sv[4 * e + 2 * h] = -INFINITY;
@@ -568,7 +601,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     mx[h] = fmaxf(sv[2 * h], sv[2 * h + 1]);
 #pragma unroll
-                    for (int e = 1; e < 8; ++e) mx[h] = fmaxf(mx[h], fmaxf(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]));
+                    for (int e = 1; e < kFp4Groups; ++e) mx[h] = fmaxf(mx[h], fmaxf(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]));
                     mx[h] = quad_max(mx[h]);
                 }
 #pragma unroll
@@ -579,7 +612,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
                         resc = i > 0;
                         m_run[h] = m_new;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < kFp4Groups; ++e) {
                             sv[4 * e + 2 * h] -= mx[h];
                             sv[4 * e + 2 * h + 1] -= mx[h];
                         }
@@ -589,7 +622,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 const int head0 = warp * 16 + hr;
                 const uint32_t prow = sP + b * L::kP + head0 * 128 + 4 * c;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < kFp4Groups; ++e) {
                     const float4 k = k4[4 * e];
                     const uint64_t ks = pack_f32x2(k.x, k.y);
 #pragma unroll
@@ -622,7 +655,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
         }
         if (n_mine > 0) {  // the last product must be complete before O^T is read
             rescale(n_mine - 1);
-            ok = ok && mbar_wait_bounded(&pvdone[(n_mine - 1) & 1], ((n_mine - 1) >> 1) & 1, kWaitLimitNs);
+            ok = ok && wait_pv(n_mine - 1);
             tc_fence_after();
         }
 #pragma unroll
@@ -642,10 +675,10 @@ __global__ void __launch_bounds__(kClThreads, 1)
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
     }
 
-    attn_finish<NH, L, FUSED, kFp4Shift, true>(a, &omap, smem, tmem, tO, row, split, hg, crank, csize, n_mine, ok);
+    attn_finish<NH, L, false, kFp4Shift, true>(a, &omap, smem, tmem, tO, row, split, hg, crank, csize, n_mine, ok);
 }
 
-template <int NH, bool FUSED>
+template <int NH>
 static dsa_status_t launch(AttnArgs a, int cl, cudaStream_t st) {
     using L = Fp4Smem<NH>;
     a.scale_log2 *= (float)(1 << kFp4Shift);
@@ -654,24 +687,23 @@ static dsa_status_t launch(AttnArgs a, int cl, cudaStream_t st) {
     if (!make_out_map(&omap, a.out8 ? static_cast<void*>(a.out8) : static_cast<void*>(a.out), (uint64_t)a.rows * a.heads,
                       NH, a.out8 != nullptr))
         return DSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(attn_fp4_kernel<NH, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) !=
+    if (cudaFuncSetAttribute(attn_fp4_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) !=
         cudaSuccess)
         return DSA_ERR_CUDA;
     const long long grid = (long long)a.rows * a.hg_count * a.nsplit * cl;
     if (grid > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
-    cudaError_t e = launch_pdl_cluster(attn_fp4_kernel<NH, FUSED>, dim3((unsigned)grid), dim3(kClThreads), L::kAlloc, st,
+    cudaError_t e = launch_pdl_cluster(attn_fp4_kernel<NH>, dim3((unsigned)grid), dim3(kClThreads), L::kAlloc, st,
                                        cl, qmap, omap, a);
     if (e == cudaSuccess && a.nsplit > 1) e = launch_attn_combine(a, st);
     if (e != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();
 }
 
-dsa_status_t launch_attn_fp4(const AttnArgs& a, int hg, int cl, bool fused, cudaStream_t st) {
-    if (fused) return launch<64, true>(a, cl, st);
+dsa_status_t launch_attn_fp4(const AttnArgs& a, int hg, int cl, cudaStream_t st) {
     switch (hg) {
-        case 16: return launch<16, false>(a, cl, st);
-        case 32: return launch<32, false>(a, cl, st);
-        default: return launch<64, false>(a, cl, st);
+        case 16: return launch<16>(a, cl, st);
+        case 32: return launch<32>(a, cl, st);
+        default: return launch<64>(a, cl, st);
     }
 }
 
