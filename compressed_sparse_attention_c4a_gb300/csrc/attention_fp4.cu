@@ -7,16 +7,29 @@
 //
 // A code times its block scale has at most 6 significant bits, so the rows are widened to bf16 exactly and both products
 // run on bf16 tensor cores; the row scale multiplies the key's logit and its probability (a power of two: no rounding).
+#include <algorithm>
+
 #include "attention.cuh"
 
 namespace dsa {
 
-// Work split as the bf16 kernel (attention.cu): a cluster of CL CTAs per (query row, group of NH <= 64 heads, key split),
-// tile i of a CTA being the split's tile crank + CL i of 48 keys.  Inside a CTA, 16 warps:
-//   warps 8-15  widen: each owns 6 keys of every tile.  Lanes 0-5 resolve the keys (top-k index -> block table -> row)
-//               ahead; the rows' bytes are copied into shared memory with cp.async, each quarter of the warp's share
-//               again as soon as it is converted, so a tile's copies have a whole tile's time; the codes become bf16
-//               and are stored 128B-swizzled as [64-dim chunk][48 keys][128 B], the first 256 dims, then the others;
+// Two kernels over the same warp roles.
+//
+// Few rows (attn_fp4_kernel<NH, false>): as the bf16 kernel (attention.cu), a cluster of CL CTAs per (query row, group of
+// NH <= 64 heads, key split), tile i of a CTA being the split's tile crank + CL i of 48 keys, merged by attn_finish.
+// Many rows (attn_fp4_kernel<NH, true>: a row in one CTA, no split): one CTA per SM takes units (row, head group) one after
+// another, and everything runs on from one to the next: the next row's keys are resolved, copied and widened and its first
+// logits computed before the last row's O^T has been stored.  (One CTA a row spent 22K of its 62K cycles, 640 keys, before
+// the first tile and after the last.)
+//
+// The tiles of a CTA form one stream, described by a ring of six entries: the keys' addresses, scales and mask, and whether
+// the tile is the first or last of its row or the last of all.
+//   warp 7      resolves: two tiles at a time, three keys a lane (top-k index -> block table -> row address, row scale);
+//   warps 8-15  widen: each owns 6 keys of every tile.  The rows' bytes are copied into shared memory with cp.async, each
+//               half of the warp's share again as soon as it is converted, so a tile's copies have a whole tile's time;
+//               the codes become bf16 and are stored 128B-swizzled as [64-dim chunk][48 keys][128 B], the first 256 dims,
+//               then the others.  Many rows: between two half-tiles, when a row's last product is done, these warps read
+//               its O^T from TMEM, rotate and store it;
 //   warps 4, 6  S = Q K^T (M = 64 heads, N = 48 keys) of even and odd tiles;
 //   warp 5      O^T += V^T P^T (four tiles of M = 128 dims, N = NH heads, K = 48 keys);
 //   warps 0-3   softmax: 16 heads a warp, a head's 48 logits over the 4 lanes of a quad (the 16-lane TMEM load spreads a
@@ -26,42 +39,42 @@ namespace dsa {
 // cycles: with two stages of 64 keys that chain, and not any unit, set the pace.  The rows go through shared memory and
 // not straight into registers: 227 KB of shared memory leave the L1 cache about 220 lines, which the rows of one tile fill,
 // and further loads wait for lines when they are issued.
-constexpr int kFp4Ring = 5;                            // half-tiles
+constexpr int kFp4Ring = 5;                            // widened half-tiles
 constexpr int kFp4Half = kFp4Keys * (kD / 2) * 2;
 constexpr int kFp4Chunk = kFp4Keys * 128;              // bytes of a 64-dim chunk
-constexpr int kFp4Tiles = 3;                           // tiles whose scales and masks are kept
+constexpr int kFp4Entries = 6;                         // described tiles
 constexpr int kFp4Widen = 8;                           // widening warps, two on each of the SM's four schedulers
 constexpr int kFp4PerWarp = kFp4Keys / kFp4Widen;      // keys of a tile per widening warp
 constexpr int kFp4Pairs = kFp4PerWarp / 2;             // a warp converts two rows at a time
 constexpr int kFp4Groups = kFp4Keys / 8;               // groups of 8 keys (the softmax's columns)
-constexpr uint64_t kFp4AllValid = 0x3F3F3F3F3F3F3F3Full;  // a mask byte per widening warp, a bit per key
-static_assert(kFp4PerWarp == 6, "six mask bits a warp");
+constexpr uint64_t kFp4AllValid = (1ull << kFp4Keys) - 1;
+constexpr uint64_t kFp4Fault = 1ull << 63;             // mask bit: a key of the tile hit a device fault
+// what an entry says of its tile
+constexpr int kFirst = 1, kLast = 2, kFinal = 4, kOdd = 8;  // of its row; of the stream; the row's ordinal is odd
 // Widened values carry 2^-8: e2m1 bits placed in a bf16 are 2^-126 of the value, and the factor that undoes it times a
 // block scale of up to 448 must stay below 2^128, so it is 2^118.
 constexpr int kFp4Shift = 8;
 
-// Bounded wait (2 s of %globaltimer).  The try suspends the warp in hardware for up to kSuspendNs at a time: measured,
-// spinning on the default, short suspension, the waiting warps took a quarter of all issue slots from the softmax and the
-// widening.
-constexpr uint32_t kSuspendNs = 100000;
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-    const uint32_t addr = smem_u32(bar);
-    auto attempt = [&]() {
+// Bounded wait (2 s of %globaltimer).  Only the first try is inline: the kernel's roles run side by side and share the
+// instruction caches, and with every wait's loop, every tile loop unrolled and the rare paths inline the schedulers
+// mostly waited for instructions (3.9 cycles of it per issued instruction).
+__device__ __noinline__ bool wait_bar_slow(uint32_t addr, uint32_t parity) {
+    const uint64_t t0 = global_ns();
+    while (true) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
-            : "r"(addr), "r"(parity), "r"(kSuspendNs)
+            : "r"(addr), "r"(parity), "r"(20000u)  // suspended for up to 20 us at a time
             : "memory");
-        return done != 0;
-    };
-    if (attempt()) return true;
-    const uint64_t t0 = global_ns();
-    while (!attempt())
+        if (done) return true;
         if (global_ns() - t0 > kWaitLimitNs) return false;
-    return true;
+    }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_bar_slow(smem_u32(bar), parity);
 }
 
 template <int NH>
@@ -72,15 +85,20 @@ struct Fp4Smem {
     static constexpr int kOffK = kOffQ + kQ;                        // ring of widened half-tiles; received tiles
     static constexpr int kOffP = kOffK + kFp4Ring * kFp4Half;       // two P^T buffers; output staging at the end
     static constexpr int kOffRaw = kOffP + 2 * kP;                  // [48 keys][288 B]: a tile's rows as stored
-    static constexpr int kOffKsc = kOffRaw + kFp4Keys * kFp4BlockRow;  // float [3][24][4]: see s_ksc
-    static constexpr int kOffMask = kOffKsc + kFp4Tiles * kFp4Keys * 8;  // uint8 [3][8]: valid keys of each widening warp
-    static constexpr int kOffAlpha = kOffMask + 32;                 // float [2][NH]
-    static constexpr int kOffVote = kOffAlpha + 2 * NH * 4;         // int [2][4]
-    static constexpr int kOffFault = kOffVote + 32;                 // int: a key of this CTA hit a device fault
+    static constexpr int kOffAddr = kOffRaw + kFp4Keys * kFp4BlockRow;  // uint64 [6][48]: address of a key's row, 0 masked
+    static constexpr int kOffKsc = kOffAddr + kFp4Entries * kFp4Keys * 8;  // float [6][24][4]: see s_ksc
+    static constexpr int kOffMask = kOffKsc + kFp4Entries * kFp4Keys * 8;  // uint64 [6]: valid keys, kFp4Fault
+    static constexpr int kOffInfo = kOffMask + kFp4Entries * 8;     // int [6][4]: flags, unit, position
+    static constexpr int kOffAlpha = kOffInfo + kFp4Entries * 16;   // float [2][NH]
+    static constexpr int kOffVote = kOffAlpha + 2 * NH * 4;         // int [2][4]: a softmax warp's vote for a rescale
+    static constexpr int kOffPinfo = kOffVote + 32;                 // int [2]: flags of the tile in a P^T buffer
+    static constexpr int kOffInv = kOffPinfo + 16;                  // float [2][NH]: output factor of a finished row
+    static constexpr int kOffRow = kOffInv + 2 * NH * 4;            // int [2][4]: its unit, -, position, fault
+    static constexpr int kOffFault = kOffRow + 32;                  // int: a key of this CTA hit a device fault
     static constexpr int kOffRope = kOffFault + 16;                 // float [32][2]: cos, sin of each pair's angle at m
-    static constexpr int kBars = 2 * kFp4Ring + 10;
+    static constexpr int kBars = 2 * kFp4Ring + 3 * kFp4Entries + 12;
     static constexpr int kOffBar = kOffRope + 256;                  // kBars mbarriers, TMEM address
-    static constexpr int kOffXfull = kOffBar + (kBars - 3) * 8;     // the last three: received tile slots
+    static constexpr int kOffXfull = kOffBar + (kBars - 4) * 8;     // three of the last four: received tile slots
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
     static constexpr int kAlloc = kBytes;                           // the base is declared 1024-byte aligned
     static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
@@ -98,9 +116,10 @@ struct Fp4Smem {
     static __host__ __device__ constexpr int stat(int c, int h) {
         return kOffP + (c >> 1) * kP + h * 128 + (((6 + (c & 1)) ^ (h & 7)) << 4);
     }
-    static_assert(kOffKsc % 16 == 0 && kOffMask % 16 == 0 && kOffAlpha % 16 == 0 && kOffVote % 16 == 0 &&
-                      kOffOwn % 16 == 0 && kOffFac % 16 == 0 && kOffFault % 16 == 0 && kOffRope % 16 == 0 &&
-                      kOffBar % 16 == 0 && kOffOut1 % 1024 == 0,
+    static_assert(kOffRaw % 16 == 0 && kOffAddr % 16 == 0 && kOffKsc % 16 == 0 && kOffMask % 16 == 0 &&
+                      kOffInfo % 16 == 0 && kOffAlpha % 16 == 0 && kOffVote % 16 == 0 && kOffInv % 16 == 0 &&
+                      kOffRow % 16 == 0 && kOffOwn % 16 == 0 && kOffFac % 16 == 0 && kOffFault % 16 == 0 &&
+                      kOffRope % 16 == 0 && kOffBar % 16 == 0 && kOffOut1 % 1024 == 0,
                   "shared-memory regions 16-byte aligned");
     static constexpr int kTmemCols = 512;  // S: [2 buffers][64 columns, 48 used]; O^T: [4 tiles][NH heads]
 };
@@ -218,41 +237,134 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
+// O^T of the calling warp's quadrant times alpha per head (a rare step, kept out of the loops).
 template <int NH>
+__device__ __noinline__ void rescale_quadrant(uint32_t taddr, const float* alpha) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < 4 * NH; c0 += 16) {
+        float v[16];
+        tmem_ld16(taddr + c0, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] *= alpha[c0 % NH + e];
+        tmem_st16(taddr + c0, v);
+    }
+    tmem_wait_st();
+}
+
+// A finished row's output, by the eight widening warps (ww): O^T from TMEM, times the row's factor per head, rotated by
+// R_m^-1, to global memory.  Warp quadrant = 32 dims of each 128-dim tile, lane = dim, half of the heads.  Neighbouring
+// lanes (a pair of dims) exchange one value per pair of heads: the even lane then holds both dims of the first head, the
+// odd lane those of the second, and stores them as one word: half a 128-byte line per head and quadrant.
+template <int NH>
+__device__ __noinline__ void store_row(const RopeTable& rope, uint16_t* out_row, uint32_t taddr, const float* inv, int ww,
+                                       int m, bool fault) {
+    constexpr int kHeads = NH / 2, kStep = 8;
+    const int lane = threadIdx.x & 31, quad = ww & 3, hbase = (ww >> 2) * kHeads;
+    const bool odd = lane & 1;
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;
+    const int first_rot = kD - rope.rope_dim;
+    uint16_t* const out = out_row + (hbase + (odd ? 1 : 0)) * kD;
+    taddr += ((uint32_t)(quad * 32) << 16) + hbase;
+#pragma unroll 1
+    for (int tt = 0; tt < 4; ++tt) {
+        const int dim = tt * 128 + quad * 32 + (lane & ~1);  // the pair's even dim
+        const bool rotated = __any_sync(0xffffffffu, dim >= first_rot);
+        float cs = 1.f, sn = 0.f;
+        if (rotated && dim >= first_rot && !fault) rope_cos_sin(m, rope, (dim - first_rot) >> 1, &cs, &sn);
+        uint32_t* to = reinterpret_cast<uint32_t*>(out + dim);
+        float v[kStep];
+        tmem_ld_nowait<kStep>(taddr + tt * NH, v);
+#pragma unroll 1
+        for (int h0 = 0; h0 < kHeads; h0 += kStep) {
+            tmem_wait_ld();
+            tmem_regs_after_wait<kStep>(v);
+            float x[kStep];
+#pragma unroll
+            for (int e = 0; e < kStep; e += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(inv + hbase + h0 + e);
+                x[e] = v[e] * f.x, x[e + 1] = v[e + 1] * f.y, x[e + 2] = v[e + 2] * f.z, x[e + 3] = v[e + 3] * f.w;
+            }
+            if (h0 + kStep < kHeads) tmem_ld_nowait<kStep>(taddr + tt * NH + h0 + kStep, v);
+#pragma unroll
+            for (int e = 0; e < kStep; e += 2) {
+                uint32_t w;
+                if (!rotated) {
+                    w = bf16x2_rn(x[e], x[e + 1]);
+                    w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), pick);
+                } else {
+                    const float recv = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 1], 1);
+                    const float lo = odd ? recv : x[e], hi = odd ? x[e + 1] : recv;
+                    w = bf16x2_rn(lo * cs + hi * sn, hi * cs - lo * sn);
+                }
+                to[e * (kD / 2)] = fault ? 0u : w;
+            }
+            to += kStep * (kD / 2);
+        }
+    }
+}
+
+// The unit (query row, head group) that a CTA works on and its share of the row's tiles.
+struct Unit {
+    int row, hg, r, m;
+    int n_vis, n_comp, wlo, n_keys;
+    int first, step, end, tiles;  // the CTA's tile i is the row's tile first + step i < end; tiles >= 1 (if there is none,
+                                  // one of masked keys)
+    bool ok;
+};
+
+template <int NH, bool ROWS>
 __global__ void __launch_bounds__(kClThreads, 1)
-    attn_fp4_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap, AttnArgs a) {
+    attn_fp4_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
+                    const __grid_constant__ AttnArgs a) {
     using L = Fp4Smem<NH>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sP = smem_u32(smem + L::kOffP);
-    // the row scales of keys 2 p and 2 p + 1 of a stage, then the same times sm_scale log2(e)
+    uint64_t* s_addr = reinterpret_cast<uint64_t*>(smem + L::kOffAddr);
+    // the row scales of keys 2 p and 2 p + 1 of a tile, then the same times sm_scale log2(e)
     float* s_ksc = reinterpret_cast<float*>(smem + L::kOffKsc);
-    uint8_t* s_mask8 = smem + L::kOffMask;
+    uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + L::kOffMask);
+    int* s_info = reinterpret_cast<int*>(smem + L::kOffInfo);
     float* s_alpha = reinterpret_cast<float*>(smem + L::kOffAlpha);
     int* s_vote = reinterpret_cast<int*>(smem + L::kOffVote);
-    // half h of tile i: ring slot (2 i + h) % 5; scales and mask i % 3; S columns and P^T buffer i & 1
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // [5] widened (widening warps)
+    int* s_pinfo = reinterpret_cast<int*>(smem + L::kOffPinfo);
+    float* s_inv = reinterpret_cast<float*>(smem + L::kOffInv);
+    int* s_orow = reinterpret_cast<int*>(smem + L::kOffRow);
+    // tile g: entry g % 6; half h in ring slot (2 g + h) % 5; S columns and P^T buffer g & 1
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);  // [5] half-tile widened (widening warps)
     uint64_t* pvdone = full + kFp4Ring;                                 // [5] multiplied into O^T
-    uint64_t* sfull = pvdone + kFp4Ring;                                // [2] S in TMEM
+    uint64_t* rfull = pvdone + kFp4Ring;                                // [6] entry: addresses, mask, flags
+    uint64_t* kfull = rfull + kFp4Entries;                              // [6] entry: scales
+    uint64_t* kfree = kfull + kFp4Entries;                              // [6] entry read (softmax warps, next S warp)
+    uint64_t* sfull = kfree + kFp4Entries;                              // [2] S in TMEM
     uint64_t* pfull = sfull + 2;                                        // [2] P^T written (4 softmax warps)
     uint64_t* qfull = pfull + 2;                                        // query rows loaded
     uint64_t* rdone = qfull + 1;                                        // O^T rescaled (4 softmax warps)
+    uint64_t* ostat = rdone + 1;                                        // a row's factors written (4 softmax warps)
+    uint64_t* ofree = ostat + 1;                                        // its O^T read (widening warps)
     uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + L::kOffXfull);  // [3] each received tile slot loaded
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(xfull + 3);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(xfull + 4);
     volatile int* s_fault = reinterpret_cast<volatile int*>(smem + L::kOffFault);
     float* s_rc = reinterpret_cast<float*>(smem + L::kOffRope);
     float* s_own = reinterpret_cast<float*>(smem + L::kOffOwn);  // written after the last product
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int crank = (int)cluster_ctarank(), csize = (int)cluster_nctarank();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
+    const int crank = ROWS ? 0 : (int)cluster_ctarank(), csize = ROWS ? 1 : (int)cluster_nctarank();
     const int cid = blockIdx.x / csize;
-    const int split = cid % a.nsplit;
-    const int hg = (cid / a.nsplit) % a.hg_count;
-    const int row = cid / (a.nsplit * a.hg_count);
+    const int split = ROWS ? 0 : cid % a.nsplit;
+    // units: ROWS: blockIdx.x, + gridDim.x, ... of rows * head groups; else the one of this cluster
+    const int unit0 = ROWS ? (int)blockIdx.x : cid / a.nsplit, units = a.rows * a.hg_count;
+    const int unit_step = ROWS ? (int)gridDim.x : units;
     if (tid == 0) {
         DSA_STAMP(0);
         for (int b = 0; b < kFp4Ring; ++b) {
             mbar_init(&full[b], kFp4Widen);
             mbar_init(&pvdone[b], 1);
+        }
+        for (int b = 0; b < kFp4Entries; ++b) {
+            mbar_init(&rfull[b], 1);
+            mbar_init(&kfull[b], 1);
+            mbar_init(&kfree[b], 5);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sfull[b], 1);
@@ -260,6 +372,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
         }
         mbar_init(qfull, 1);
         mbar_init(rdone, 4);
+        mbar_init(ostat, 4);
+        mbar_init(ofree, kFp4Widen);
         for (int b = 0; b < 3; ++b) mbar_init(&xfull[b], 1);
         *s_fault = 0;
         fence_barrier_init();
@@ -275,75 +389,156 @@ __global__ void __launch_bounds__(kClThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    if (tid == 0) DSA_STAMP(1);
     const uint32_t tS = tmem, tO = tmem + 128;
-    if (csize > 1) cluster_arrive_relaxed();  // phase 0: this CTA has started (waited on before DSMEM use)
+    if constexpr (!ROWS)
+        if (csize > 1) cluster_arrive_relaxed();  // phase 0: this CTA has started (waited on before DSMEM use)
 
     // Position, request, block tables and query rows: inputs that no kernel of the layer step writes, read while the
     // preceding kernel finishes.  Top-k indices, cache rows and every output come after the wait.
-    const int r = a.q_req ? a.q_req[row] : row;
-    const int m = a.q_pos[row];
-    const bool row_ok = r >= 0 && r < a.main_bt.batch && r < a.swa_bt.batch && m >= 0;
-    if (!row_ok && tid == 0) *s_fault = 1;
-    const int n_vis = row_ok ? entries_formed((long long)m + 1, a.kind_w, a.kind_s) : 0;
-    const int n_comp = a.topk ? a.k : n_vis;
-    const int wlo = max(0, m - a.window + 1);
-    const int n_keys = row_ok ? n_comp + (m - wlo + 1) : 0;
-    const int n_tiles = (n_keys + kFp4Keys - 1) / kFp4Keys;
-    const int g_lo = split * a.cps, g_hi = min(n_tiles, g_lo + a.cps);
-    const int n_mine = g_hi > g_lo + crank ? (g_hi - g_lo - crank + csize - 1) / csize : 0;
-    if (warp == 0 && lane < a.rope.rope_dim / 2) {  // R_m^-1 of the output: cos and sin of each pair's angle at m
-        float c = 1.f, sn = 0.f;
-        if (row_ok) rope_cos_sin(m, a.rope, lane, &c, &sn);
-        s_rc[2 * lane] = c;
-        s_rc[2 * lane + 1] = sn;
-    }
-    if (warp == 4 && n_mine > 0) {  // the query rows, one 64-dim box per lane
+    auto row_of = [&](int unit) { return unit / a.hg_count; };
+    auto make_unit = [&](int unit, int r, int m) {
+        Unit u;
+        u.row = row_of(unit);
+        u.hg = unit - u.row * a.hg_count;
+        u.r = r;
+        u.m = m;
+        u.ok = r >= 0 && r < a.main_bt.batch && r < a.swa_bt.batch && m >= 0;
+        u.n_vis = u.ok ? entries_formed((long long)m + 1, a.kind_w, a.kind_s) : 0;
+        u.n_comp = a.topk ? a.k : u.n_vis;
+        u.wlo = max(0, m - a.window + 1);
+        u.n_keys = u.ok ? u.n_comp + (m - u.wlo + 1) : 0;
+        const int n_tiles = (u.n_keys + kFp4Keys - 1) / kFp4Keys;
+        u.first = (ROWS ? 0 : split * a.cps) + crank;
+        u.step = csize;
+        u.end = ROWS ? n_tiles : min(n_tiles, (split + 1) * a.cps);
+        u.tiles = u.end > u.first ? (u.end - u.first + csize - 1) / csize : 1;
+        return u;
+    };
+    auto load_q = [&](int unit) {  // by one warp: one 64-dim box per lane
+        const int row = row_of(unit);
         if (lane == 0) mbar_expect_tx(qfull, NH * kD * 2);
         __syncwarp();
-        if (lane < kD / 64) tma_load_2d(smem + L::kOffQ + lane * 8192, &qmap, lane * 64, row * a.heads + hg * NH, qfull);
+        if (lane < kD / 64)
+            tma_load_2d(smem + L::kOffQ + lane * 8192, &qmap, lane * 64, row * a.heads + (unit - row * a.hg_count) * NH, qfull);
         __syncwarp();
         if (lane == 0) mbar_arrive(qfull);
+    };
+    if (warp == 4) load_q(unit0);
+    int r0 = 0, m0 = 0;
+    if (warp == 7 || warp == 3) {
+        r0 = a.q_req ? a.q_req[row_of(unit0)] : row_of(unit0);
+        m0 = a.q_pos[row_of(unit0)];
     }
+    if constexpr (!ROWS)
+        if (warp == 3 && lane < a.rope.rope_dim / 2) {  // R_m^-1 of the output: cos and sin of each pair's angle at m
+            float c = 1.f, sn = 0.f;
+            if (m0 >= 0) rope_cos_sin(m0, a.rope, lane, &c, &sn);
+            s_rc[2 * lane] = c;
+            s_rc[2 * lane + 1] = sn;
+        }
     pdl_wait();  // global memory the preceding kernel writes, and every output, only below
     pdl_launch_dependents();
     if (tid == 0) DSA_STAMP(2);
-    if (!row_ok && tid == 0 && crank == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
     bool ok = true;
+    auto entry_wait = [&](uint64_t* bars, int g) { return wait_bar(&bars[g % kFp4Entries], (g / kFp4Entries) & 1); };
 
-    if (warp >= 8) {
-        // ---- widening warps ----------------------------------------------------------------------------
-        const int ww = warp - 8;
-        // A key is resolved in three steps, a tile apart, so that no load waits for another: lanes 0-5, key `lane` of the
-        // warp's 6 in tile i, j its index in the row (-1: none).  Step 1: its entry (top-k index; -1: none) or position.
+    if (warp == 7) {
+        // ---- resolve: every unit's tiles, two at a time: key kk = lane + 32 e of the two tiles' 96 ---------------
         const int main_shift = __ffs(a.main.rows_per_block) - 1;  // 64 or 2 rows a block; the window's 256
-        const int32_t* const row_topk = a.topk + (long long)row * a.k;
-        auto key_index = [&](int i) -> int {
-            const int j = (g_lo + crank + csize * i) * kFp4Keys + ww * kFp4PerWarp + lane;
-            return lane < kFp4PerWarp && i < n_mine && j < n_keys ? j : -1;
-        };
-        auto key_entry = [&](int j) -> int { return load_int_if(row_topk + max(j, 0), a.topk && j >= 0 && j < n_comp); };
-        auto key_id = [&](int j, int entry) -> int { return j >= n_comp ? wlo + (j - n_comp) : (a.topk ? entry : j); };
-        // Step 2: the physical block, from the block table (-1: unmapped, beyond the table or not visible).
-        auto key_block = [&](int j, int id) -> int {
-            const bool window = j >= n_comp;
-            const dsa_block_table_t& bt = window ? a.swa_bt : a.main_bt;
-            const int lb = max(id, 0) >> (window ? 8 : main_shift);
-            return load_int_if(bt.table + (long long)r * bt.max_blocks + lb,
-                               j >= 0 && id >= 0 && (window || id < n_vis) && lb < bt.max_blocks);
-        };
-        // Step 3: the pool row (-1: none).
-        auto key_row = [&](int j, int id, int block) -> int {
-            if (j < 0 || id < 0) return -1;
-            const bool window = j >= n_comp;
-            if (block < 0 || block >= (window ? a.swa.num_blocks : a.main.num_blocks)) {
-                report(a.status, DSA_ERR_DEVICE_FAULT);
-                *s_fault = 1;
-                return -1;
+        int g = 0;
+        for (int unit = unit0, ord = 0; unit < units && ok; unit += unit_step, ++ord) {
+            const Unit u = make_unit(unit, r0, m0);
+            if (unit + unit_step < units) {  // the next unit's, in flight meanwhile
+                const int next = row_of(unit + unit_step);
+                r0 = a.q_req ? load_int_if(a.q_req + next, true) : next;
+                m0 = load_int_if(a.q_pos + next, true);
             }
-            const int shift = window ? 8 : main_shift;
-            return (block << shift) + (id & ((1 << shift) - 1));
-        };
+            if (!u.ok && lane == 0 && crank == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
+            const int32_t* const row_topk = a.topk + (long long)u.row * a.k;
+            auto key_index = [&](int i, int e) -> int {  // of the row, -1: none
+                const int kk = lane + 32 * e, t = i + kk / kFp4Keys;
+                const int tile = u.first + u.step * t, j = tile * kFp4Keys + kk % kFp4Keys;
+                return tile < u.end && j < u.n_keys ? j : -1;
+            };
+            int entry[3];  // top-k indices of the next two tiles' keys (-1: none)
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                const int j = key_index(0, e);
+                entry[e] = load_int_if(row_topk + max(j, 0), a.topk && j >= 0 && j < u.n_comp);
+            }
+            for (int i = 0; i < u.tiles && ok; i += 2) {
+                const bool two = i + 1 < u.tiles;
+                if (g >= kFp4Entries) ok = entry_wait(kfree, g - kFp4Entries);
+                if (two && g + 1 >= kFp4Entries) ok = ok && entry_wait(kfree, g + 1 - kFp4Entries);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                int j[3], id[3], block[3], row[3];
+                uint32_t valid[3], bad = !u.ok;
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    j[e] = key_index(i, e);
+                    const bool window = j[e] >= u.n_comp;
+                    id[e] = j[e] < 0 ? -1 : window ? u.wlo + (j[e] - u.n_comp) : (a.topk ? entry[e] : j[e]);
+                    const dsa_block_table_t& bt = window ? a.swa_bt : a.main_bt;
+                    const int lb = max(id[e], 0) >> (window ? 8 : main_shift);
+                    block[e] = load_int_if(bt.table + (long long)u.r * bt.max_blocks + lb,
+                                           id[e] >= 0 && (window || id[e] < u.n_vis) && lb < bt.max_blocks);
+                }
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const int jn = key_index(i + 2, e);
+                    entry[e] = load_int_if(row_topk + max(jn, 0), a.topk && jn >= 0 && jn < u.n_comp);
+                }
+                float scale[3];
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const bool window = j[e] >= u.n_comp;
+                    const dsa_pool_t& pool = window ? a.swa : a.main;
+                    row[e] = -1;
+                    if (id[e] >= 0) {
+                        if (block[e] < 0 || block[e] >= pool.num_blocks) bad |= 2u;
+                        else row[e] = (block[e] << (window ? 8 : main_shift)) + (id[e] & (window ? 255 : (1 << main_shift) - 1));
+                    }
+                    scale[e] = load_float_if(pool.scale + max(row[e], 0), row[e] >= 0);
+                    valid[e] = __ballot_sync(0xffffffffu, row[e] >= 0);
+                    const int kk = lane + 32 * e, entry_at = (g + kk / kFp4Keys) % kFp4Entries;
+                    if (two || kk < kFp4Keys)
+                        s_addr[entry_at * kFp4Keys + kk % kFp4Keys] =
+                            row[e] < 0 ? 0ull : reinterpret_cast<uint64_t>(pool.data) + (uint64_t)row[e] * kFp4BlockRow;
+                }
+                bad = __any_sync(0xffffffffu, bad != 0);
+                if (bad && u.ok && lane == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
+                if (lane < 2 && (lane == 0 || two)) {
+                    const int t = i + lane, at = (g + lane) % kFp4Entries;
+                    const uint64_t mask = lane == 0 ? (uint64_t)valid[0] | (uint64_t)(valid[1] & 0xffffu) << 32
+                                                    : (uint64_t)(valid[1] >> 16) | (uint64_t)valid[2] << 16;
+                    s_mask[at] = mask | (bad ? kFp4Fault : 0ull);
+                    const bool last = t + 1 == u.tiles;
+                    s_info[4 * at] = (t == 0 ? kFirst : 0) | (last ? kLast : 0) | (ord & 1 ? kOdd : 0) |
+                                     (last && unit + unit_step >= units ? kFinal : 0);
+                    s_info[4 * at + 1] = unit;
+                    s_info[4 * at + 2] = u.m;
+                }
+                __syncwarp();
+                if (lane < 2 && (lane == 0 || two)) mbar_arrive(&rfull[(g + lane) % kFp4Entries]);
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const int kk = lane + 32 * e, at = (g + kk / kFp4Keys) % kFp4Entries, key = kk % kFp4Keys;
+                    if (two || kk < kFp4Keys) {
+                        float* k = s_ksc + at * 2 * kFp4Keys + key / 2 * 4 + (key & 1);
+                        k[0] = scale[e];
+                        k[2] = scale[e] * a.scale_log2;
+                    }
+                }
+                __syncwarp();
+                if (lane < 2 && (lane == 0 || two)) mbar_arrive(&kfull[(g + lane) % kFp4Entries]);
+                g += two ? 2 : 1;
+            }
+        }
+        if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
+    } else if (warp >= 8) {
+        // ---- widen -------------------------------------------------------------------------------------------
+        const int ww = warp - 8;
         // Converting, lane l = 16 q + t: of each pair of the warp's rows row q, and of each half of the dims block t (16 dims:
         // 16-byte pieces 2 (t & 3), 2 (t & 3) + 1 of 64-dim chunk t >> 2 of the half).  Lanes of odd chunks store their
         // second piece first, so that eight neighbouring lanes cover all banks.
@@ -351,137 +546,162 @@ __global__ void __launch_bounds__(kClThreads, 1)
         const uint32_t raw = smem_u32(smem + L::kOffRaw) + ww * (kFp4PerWarp * kFp4BlockRow);
         const uint32_t raw_codes = raw + q * kFp4BlockRow + t * 8, raw_scale = raw + q * kFp4BlockRow + kD / 2 + t;
         const int hf = (t >> 2) & 1, p0 = 2 * (t & 3) + hf;
-        uint32_t dst[kFp4Pairs][2];  // where the lane's pieces of its row of each pair go, within a ring slot
-#pragma unroll
-        for (int u = 0; u < kFp4Pairs; ++u)
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int kk = ww * kFp4PerWarp + 2 * u + q;
-                dst[u][g] = sK + (t >> 2) * kFp4Chunk + (kk >> 3) * 1024 + (kk & 7) * 128 + (((p0 ^ g) ^ (kk & 7)) << 4);
-            }
+        const uint32_t dst0 = sK + (t >> 2) * kFp4Chunk;
         // Copying, lanes 0-17: of a pair's row lane / 9, 16-byte piece lane % 9 of a half (8 of codes, one of 16 scales).
         const int cr = lane >= 9 ? 1 : 0, cp = lane - 9 * cr;
         const uint32_t cp_off = cp < 8 ? cp * 16 : kD / 2, cp_step = cp < 8 ? kD / 4 : 16;  // half 0, and to half 1
-        uint64_t src[kFp4Pairs];     // global address of the lane's piece (half 0) of the row of each pair
+        uint64_t src[kFp4Pairs];        // global address of the lane's piece (half 0) of the row of each pair
         uint32_t src_bytes[kFp4Pairs];  // 16, or 0 to fill with zeros (a masked key)
-        // the rows of a tile, by the lanes that own them (kr: pool row or -1): their addresses to the copying lanes
-        auto aim = [&](int kr, bool window) {
-            const uint8_t* data = static_cast<const uint8_t*>(window ? a.swa.data : a.main.data);
-            const uint64_t at = reinterpret_cast<uint64_t>(data) + (uint64_t)max(kr, 0) * kFp4BlockRow;
-            const uint32_t valid = __ballot_sync(0xffffffffu, kr >= 0);
+        auto aim = [&](int g) {         // at tile g's rows
 #pragma unroll
             for (int u = 0; u < kFp4Pairs; ++u) {
-                src[u] = __shfl_sync(0xffffffffu, at, 2 * u + cr) + cp_off;
-                src_bytes[u] = (valid >> (2 * u + cr)) & 1 ? 16u : 0u;
+                const uint64_t at = s_addr[g % kFp4Entries * kFp4Keys + ww * kFp4PerWarp + 2 * u + cr];
+                src[u] = (at ? at : reinterpret_cast<uint64_t>(a.main.data)) + cp_off;
+                src_bytes[u] = at ? 16u : 0u;
             }
-            return valid;
         };
-        auto copy = [&](int h, int u) {  // one group
+        auto copy = [&](int h) {  // one group: a half of the warp's rows
             if (lane < 18)
-                cp_async16_nc(raw + (2 * u + cr) * kFp4BlockRow + cp_off + h * cp_step,
-                              reinterpret_cast<const void*>(src[u] + h * cp_step), src_bytes[u]);
+#pragma unroll
+                for (int u = 0; u < kFp4Pairs; ++u)
+                    cp_async16_nc(raw + (2 * u + cr) * kFp4BlockRow + cp_off + h * cp_step,
+                                  reinterpret_cast<const void*>(src[u] + h * cp_step), src_bytes[u]);
             cp_async_commit();
         };
-        if (n_mine > 0) {
-            const int j0 = key_index(0), e0 = key_entry(j0), e1 = key_entry(key_index(1));
-            int entry = key_entry(key_index(2));                       // of tile i + 2, loop-carried
-            const int id0 = key_id(j0, e0), b0 = key_block(j0, id0);
-            int id = key_id(key_index(1), e1), block = key_block(key_index(1), id);  // of tile i + 1
-            int kr = key_row(j0, id0, b0);
-            bool window = j0 >= n_comp;
-            uint32_t valid = aim(kr, window);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int u = 0; u < kFp4Pairs; ++u) copy(h, u);
-            float ksc = load_float_if((window ? a.swa.scale : a.main.scale) + max(kr, 0), kr >= 0);
-            int slot = 0, kt = 0;
-            uint32_t lap = 0;  // of the ring
-#pragma unroll 1
-            for (int i = 0; i < n_mine; ++i) {
-                // tile i + 1's rows, whose copies follow each part of tile i that has been converted
-                const int j1 = key_index(i + 1), j2 = key_index(i + 2);
-                kr = key_row(j1, id, block);
-                window = j1 >= n_comp;
-                id = key_id(j2, entry);
-                block = key_block(j2, id);
-                entry = key_entry(key_index(i + 3));
-                const uint32_t mask = valid;
-                const float scale = ksc;
-                valid = aim(kr, window);
-                ksc = load_float_if((window ? a.swa.scale : a.main.scale) + max(kr, 0), kr >= 0);
-                if (ww == 0 && lane == 0) DSA_TRACE(i, 0);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (lap > 0) ok = ok && wait_bar(&pvdone[slot], (lap - 1) & 1);
-                    if (h == 0 && ok) {
-                        if (lane < kFp4PerWarp) {
-                            float* k = s_ksc + kt * 2 * kFp4Keys + (ww * kFp4PerWarp + lane) / 2 * 4 + (lane & 1);
-                            k[0] = scale;
-                            k[2] = scale * a.scale_log2;
-                        }
-                        if (lane == 0) s_mask8[kt * 8 + ww] = (uint8_t)mask;
-                    }
-#pragma unroll
-                    for (int u = 0; u < kFp4Pairs; ++u) {
-                        cp_async_wait_group<2 * kFp4Pairs - 1>();  // this part of tile i, six groups ago
-                        __syncwarp();
-                        const uint2 code = lds64(raw_codes + 2 * u * kFp4BlockRow + h * (kD / 4));
-                        const uint32_t s2 = block_scale_2p118(lds8(raw_scale + 2 * u * kFp4BlockRow + h * 16));
-                        __syncwarp();
-                        copy(h, u);  // the same part of tile i + 1
-                        if (ok) {
-#pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                uint32_t o[4];
-                                widen8((g ^ hf) ? code.y : code.x, s2, o);
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst[u][g] + slot * kFp4Half),
-                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                             : "memory");
-                            }
-                        }
-                    }
-                    fence_proxy_async_smem();  // the bf16 rows -> visible to the tensor core (async proxy)
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[slot]);
-                    if (++slot == kFp4Ring) slot = 0, ++lap;
-                }
-                if (++kt == kFp4Tiles) kt = 0;
-                if (ww == 0 && lane == 0) DSA_TRACE(i, 1);
-            }
-            cp_async_wait_all();
+        ok = __all_sync(0xffffffffu, entry_wait(rfull, 0));
+        if (ok) {
+            aim(0);
+            copy(0);
+            copy(1);
         }
-        ok = __all_sync(0xffffffffu, ok);
+        int done = 0;  // rows stored
+        auto output = [&]() {  // the next finished row, whose last product is known to be complete
+            const int par = done & 1;
+            ok = __all_sync(0xffffffffu, wait_bar(ostat, par));
+            if (!ok) return;
+            const int unit = s_orow[par * 4], row = row_of(unit);
+            tc_fence_after();
+            store_row<NH>(a.rope, a.out + ((long long)row * a.heads + (unit - row * a.hg_count) * NH) * kD, tO, s_inv + par * NH,
+                          ww, s_orow[par * 4 + 2], s_orow[par * 4 + 3]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ofree);  // the next row's products may begin
+            ++done;
+        };
+        int ends[3] = {0, 0, 0}, n_ends = 0;  // half-tiles after which the next rows' products are complete
+        int slot = 0;
+        uint32_t lap = 0;  // of the ring
+#pragma unroll 1
+        for (int g = 0; ok; ++g) {
+            const int info = s_info[4 * (g % kFp4Entries)];
+            const bool final = info & kFinal, last = info & kLast;
+            if (final) {
+#pragma unroll
+                for (int u = 0; u < kFp4Pairs; ++u) src_bytes[u] = 0u;
+            } else {  // tile g + 1's rows, whose copies follow each part of tile g that has been converted
+                ok = __all_sync(0xffffffffu, entry_wait(rfull, g + 1));
+                if (!ok) break;
+                aim(g + 1);
+            }
+            if (ww == 0 && lane == 0) DSA_TRACE(g, 0);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (lap > 0) ok = ok && wait_bar(&pvdone[slot], (lap - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if constexpr (ROWS)
+                    if (ok && n_ends > 0 && ends[0] + kFp4Ring == 2 * g + h) {  // that was a row's last product
+                        output();
+                        ends[0] = ends[1], ends[1] = ends[2], --n_ends;
+                    }
+                if (!ok) break;
+                cp_async_wait_group<1>();  // this half of tile g's rows, two groups ago
+                __syncwarp();
+                uint2 code[kFp4Pairs];
+                uint32_t byte[kFp4Pairs];
+#pragma unroll
+                for (int u = 0; u < kFp4Pairs; ++u) {
+                    code[u] = lds64(raw_codes + 2 * u * kFp4BlockRow + h * (kD / 4));
+                    byte[u] = lds8(raw_scale + 2 * u * kFp4BlockRow + h * 16);
+                }
+                __syncwarp();
+                copy(h);  // the same half of tile g + 1's
+                const uint32_t to = dst0 + slot * kFp4Half;
+#pragma unroll 1
+                for (int u = 0; u < kFp4Pairs; ++u) {
+                    const int kk = ww * kFp4PerWarp + 2 * u + q;
+                    const uint32_t at = to + (kk >> 3) * 1024 + (kk & 7) * 128, s2 = block_scale_2p118(byte[0]);
+                    const uint32_t piece = (p0 ^ (kk & 7)) << 4;
+                    uint32_t o[4], o2[4];
+                    widen8(hf ? code[0].y : code[0].x, s2, o);
+                    widen8(hf ? code[0].x : code[0].y, s2, o2);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + piece), "r"(o[0]), "r"(o[1]),
+                                 "r"(o[2]), "r"(o[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (piece ^ 16u)), "r"(o2[0]), "r"(o2[1]),
+                                 "r"(o2[2]), "r"(o2[3])
+                                 : "memory");
+                    code[0] = code[1], code[1] = code[2], byte[0] = byte[1], byte[1] = byte[2];
+                }
+                fence_proxy_async_smem();  // the bf16 rows -> visible to the tensor core (async proxy)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[slot]);
+                if (++slot == kFp4Ring) slot = 0, ++lap;
+            }
+            if (ww == 0 && lane == 0) DSA_TRACE(g, 1);
+            if constexpr (ROWS)
+                if (last) {
+                    const int end = 2 * g + 1;
+                    if (n_ends == 0) ends[0] = end;
+                    else if (n_ends == 1) ends[1] = end;
+                    else ends[2] = end;
+                    ++n_ends;
+                }
+            if (final) break;
+        }
+        if constexpr (ROWS)
+            while (ok && n_ends > 0) {
+                ok = __all_sync(0xffffffffu, wait_bar(&pvdone[ends[0] % kFp4Ring], (ends[0] / kFp4Ring) & 1));
+                if (ok) output();
+                ends[0] = ends[1], ends[1] = ends[2], --n_ends;
+            }
+        cp_async_wait_all();
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
     } else if (warp == 5) {
         // ---- O^T += V^T P^T, issued by one elected lane ------------------------------------------------------
         const uint32_t idesc_o = idesc_bf16(NH, 1, 128);
-        uint32_t rescales = 0;
+        uint32_t rescales = 0, rows = 0;
         int slot = 0;
-        for (int i = 0; i < n_mine; ++i) {
-            const int b = i & 1;
-            ok = wait_bar(&pfull[b], (i >> 1) & 1);  // P^T written (so S done, the stage full)
+        for (int g = 0; ok; ++g) {
+            const int b = g & 1;
+            ok = wait_bar(&pfull[b], (g >> 1) & 1);  // P^T written (so S done, the half-tiles full)
+            const int info = s_pinfo[b];
             if (ok && (s_vote[b * 4] | s_vote[b * 4 + 1] | s_vote[b * 4 + 2] | s_vote[b * 4 + 3]))
                 ok = wait_bar(rdone, rescales++ & 1);
+            if constexpr (ROWS)
+                if (info & kFirst) {  // the previous row's O^T has been read
+                    if (rows > 0) ok = ok && wait_bar(ofree, (rows - 1) & 1);
+                    ++rows;
+                }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) DSA_TRACE(i, 6);
+            if (lane == 0) DSA_TRACE(g, 6);
             const uint64_t dp = sw128_desc(sP + b * L::kP, 16, 1024);
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 const uint64_t dv = sw128_desc(sK + slot * kFp4Half, kFp4Chunk, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                     for (int ks = 0; ks < kFp4Keys / 16; ++ks)
                         mma_bf16_ss_elect(tO + (2 * h + mt) * NH,
                                           dv + (uint64_t)(((2 * mt) * kFp4Chunk + (2 * ks) * 1024) >> 4),
-                                          dp + (uint64_t)((ks * 32) >> 4), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
+                                          dp + (uint64_t)((ks * 32) >> 4), idesc_o, (!(info & kFirst) || ks > 0) ? 1u : 0u);
                 mma_commit_elect(&pvdone[slot]);
                 if (++slot == kFp4Ring) slot = 0;
             }
-            if (lane == 0) DSA_TRACE(i, 7);
+            if (lane == 0) DSA_TRACE(g, 7);
+            if (info & kFinal) break;
         }
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
     } else if (warp == 4 || warp == 6) {
@@ -490,192 +710,266 @@ __global__ void __launch_bounds__(kClThreads, 1)
         const int b = warp == 6;
         const uint32_t idesc_s = idesc_bf16(kFp4Keys, 0, 64);
         const uint64_t dq = sw128_desc(sQ, 16, 1024);
-        if (n_mine > b) ok = wait_bar(qfull, 0);
-        for (int i = b; i < n_mine; i += 2) {
-            if (i >= 2) ok = ok && wait_bar(&pfull[b], ((i >> 1) - 1) & 1);  // S buffer read
-#pragma unroll
+        for (int g = b;; g += 2) {
+            if (g > 0) {  // is there a tile g?
+                ok = ok && entry_wait(rfull, g - 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const bool end = s_info[4 * ((g - 1) % kFp4Entries)] & kFinal;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kfree[(g - 1) % kFp4Entries]);
+                if (end) break;
+            }
+            if (g >= 2) ok = ok && wait_bar(&pfull[b], ((g >> 1) - 1) & 1);  // S buffer read
+            int info = 0;
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                const int n = 2 * i + h, slot = n % kFp4Ring;
+                const int n = 2 * g + h, slot = n % kFp4Ring;
                 ok = ok && wait_bar(&full[slot], (n / kFp4Ring) & 1);
+                if (h == 0) {
+                    info = s_info[4 * (g % kFp4Entries)];
+                    ok = ok && wait_bar(qfull, info & kOdd ? 1 : 0);  // the row's queries
+                }
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0 && h == 0) DSA_TRACE(i, 2);
+                if (lane == 0 && h == 0) DSA_TRACE(g, 2);
                 const uint64_t dk = sw128_desc(sK + slot * kFp4Half, 16, 1024);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c)  // 64-dim chunks: 64 query rows / 48 key rows apart
 #pragma unroll
-                for (int ks = 0; ks < kD / 32; ++ks)
-                    mma_bf16_ss_elect(tS + b * 64, dq + (uint64_t)(((((ks >> 2) + 4 * h) * 8192) + (ks & 3) * 32) >> 4),
-                                      dk + (uint64_t)((((ks >> 2) * kFp4Chunk) + (ks & 3) * 32) >> 4), idesc_s,
-                                      h + ks > 0 ? 1u : 0u);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16_ss_elect(tS + b * 64, dq + (uint64_t)(((4 * h + c) * 8192 + ks * 32) >> 4),
+                                          dk + (uint64_t)((c * kFp4Chunk + ks * 32) >> 4), idesc_s,
+                                          h + c + ks > 0 ? 1u : 0u);
             }
             if (!ok) break;
+            const int unit = s_info[4 * (g % kFp4Entries) + 1];
             mma_commit_elect(&sfull[b]);
-            if (lane == 0) DSA_TRACE(i, 3);
+            if (lane == 0) DSA_TRACE(g, 3);
+            if (info & kFinal) break;
+            if constexpr (ROWS) {
+                if ((info & kFirst) && unit + unit_step < units && lane == 0) {  // the next unit's queries, towards L2
+                    const int row = row_of(unit + unit_step);
+                    const long long qrow = (long long)row * a.heads + (unit + unit_step - row * a.hg_count) * NH;
+                    prefetch_l2(a.q + qrow * kD, NH * kD * 2);
+                }
+                if (info & kLast) {  // the row's last product: the next queries take their place
+                    ok = wait_bar(&sfull[b], (g >> 1) & 1);
+                    if (g > 0) ok = ok && wait_bar(&sfull[b ^ 1], ((g - 1) >> 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    load_q(unit + unit_step);
+                }
+            }
         }
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
     } else if (warp < 4) {
-        // ---- softmax warps: heads 16 warp + lane / 4 and + 8, keys 8 e + 2 (lane % 4), + 1 ------------------
+        // ---- softmax: heads 16 warp + lane / 4 and + 8, keys 8 e + 2 (lane % 4), + 1 -----------------------------
         const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        const int hr = lane >> 2, c = lane & 3;
+        const int hr = lane >> 2, c = lane & 3, head0 = warp * 16 + hr;
         // m_run: the head's running maximum, lazy: it moves only when exceeded by more than 2^8, so O^T is rarely
         // rescaled and exp2(s - m) <= 2^8.  l_run: the lane's share of the sum of the fp32 probabilities, two halves
         float m_run[2] = {-INFINITY, -INFINITY};
         uint64_t l_run[2] = {0ull, 0ull};
-        // O^T times alpha per head, when a head's maximum moved in tile i: after the other warps' votes for the tile are
-        // in (their P^T is written) and the product of tile i - 1 is done; the product of tile i waits for it
-        auto wait_pv = [&](int i) { return wait_bar(&pvdone[(2 * i + 1) % kFp4Ring], ((2 * i + 1) / kFp4Ring) & 1); };
-        auto rescale = [&](int i) {
-            const int b = i & 1;
-            ok = ok && wait_bar(&pfull[b], (i >> 1) & 1);
+        uint64_t seen = 0;  // the row's masks' fault bits
+        int rows = 0;
+        auto wait_pv = [&](int g) { return wait_bar(&pvdone[(2 * g + 1) % kFp4Ring], ((2 * g + 1) / kFp4Ring) & 1); };
+        // O^T times alpha per head, when a head's maximum moved in tile g: after the other warps' votes for the tile are
+        // in (their P^T is written) and the product of tile g - 1 is done; the product of tile g waits for it
+        auto rescale = [&](int g) {
+            const int b = g & 1;
+            ok = ok && wait_bar(&pfull[b], (g >> 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || !(s_vote[b * 4] | s_vote[b * 4 + 1] | s_vote[b * 4 + 2] | s_vote[b * 4 + 3])) return;
-            ok = wait_pv(i - 1);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = __all_sync(0xffffffffu, wait_pv(g - 1));
             if (ok) {
                 tc_fence_after();
-#pragma unroll 1
-                for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-                    for (int c0 = 0; c0 < NH; c0 += 16) {
-                        float v[16];
-                        tmem_ld16(tO + mt * NH + lane_off + c0, v);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] *= s_alpha[b * NH + c0 + e];
-                        tmem_st16(tO + mt * NH + lane_off + c0, v);
-                    }
-                }
-                tmem_wait_st();
+                rescale_quadrant<NH>(tO + lane_off, s_alpha + b * NH);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(rdone);
         };
-        for (int i = 0; i < n_mine; ++i) {
-            const int b = i & 1, kt = i % kFp4Tiles;
-            if (i > 0) rescale(i - 1);
-            ok = ok && wait_bar(&full[2 * i % kFp4Ring], (2 * i / kFp4Ring) & 1);  // the tile's scales and mask
-            ok = ok && wait_bar(&sfull[b], (i >> 1) & 1);
-            if (i >= 2) ok = ok && wait_pv(i - 2);  // P^T buffer free
+        for (int g = 0;; ++g) {
+            const int b = g & 1, at = g % kFp4Entries;
+            if (g > 0) rescale(g - 1);
+            ok = ok && entry_wait(kfull, g);  // the tile's scales, mask and flags
+            ok = ok && wait_bar(&sfull[b], (g >> 1) & 1);
+            if (g >= 2) ok = ok && wait_pv(g - 2);  // P^T buffer free
             ok = __all_sync(0xffffffffu, ok);
-            if (tid == 0) DSA_TRACE(i, 4);
+            if (!ok) break;
+            if (tid == 0) DSA_TRACE(g, 4);
+            const int info = s_info[4 * at], unit = s_info[4 * at + 1], pos = s_info[4 * at + 2];
+            if (info & kFirst) {
+                m_run[0] = m_run[1] = -INFINITY;
+                l_run[0] = l_run[1] = 0ull;
+                seen = 0;
+            }
             float alpha[2] = {1.f, 1.f};
             bool resc = false;
-            if (ok) {
-                tc_fence_after();
-                float sv[24];  // logits of head h in 4 e + 2 h, 4 e + 2 h + 1: keys 8 e + 2 c, + 1
-                tmem_ld_16x48_nowait(tS + b * 64 + lane_off, sv);
-                const float4* k4 = reinterpret_cast<const float4*>(s_ksc + kt * 2 * kFp4Keys) + c;
-                const uint64_t vm = *reinterpret_cast<const uint64_t*>(s_mask8 + kt * 8);
-                float m0[2];  // the logits are taken relative to m0: the running maximum, 0 before the first key
-                uint64_t neg[2];
+            tc_fence_after();
+            float sv[24];  // logits of head h in 4 e + 2 h, 4 e + 2 h + 1: keys 8 e + 2 c, + 1
+            tmem_ld_16x48_nowait(tS + b * 64 + lane_off, sv);
+            const float4* k4 = reinterpret_cast<const float4*>(s_ksc + at * 2 * kFp4Keys) + c;
+            const uint64_t vm = s_mask[at];
+            seen |= vm;
+            float m0[2];  // the logits are taken relative to m0: the running maximum, 0 before the first key
+            uint64_t neg[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    m0[h] = m_run[h] == -INFINITY ? 0.f : m_run[h];
-                    neg[h] = pack_f32x2(-m0[h], -m0[h]);
-                }
-                tmem_wait_ld();
-                tmem_regs_after_wait<24>(sv);
+            for (int h = 0; h < 2; ++h) {
+                m0[h] = m_run[h] == -INFINITY ? 0.f : m_run[h];
+                neg[h] = pack_f32x2(-m0[h], -m0[h]);
+            }
+            tmem_wait_ld();
+            tmem_regs_after_wait<24>(sv);
 #pragma unroll
-                for (int e = 0; e < kFp4Groups; ++e) {
-                    const float4 k = k4[4 * e];
-                    const uint64_t kl = pack_f32x2(k.z, k.w);
+            for (int e = 0; e < kFp4Groups; ++e) {
+                const float4 k = k4[4 * e];
+                const uint64_t kl = pack_f32x2(k.z, k.w);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        unpack_f32x2(fma_f32x2(pack_f32x2(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]), kl, neg[h]),
-                                     &sv[4 * e + 2 * h], &sv[4 * e + 2 * h + 1]);
-                }
-                if (vm != kFp4AllValid) {
-#pragma unroll
-                    for (int e = 0; e < kFp4Groups; ++e) {
-                        const int kk = 8 * e + 2 * c;  // and kk + 1: the same warp's, six keys being three pairs
-                        const uint32_t bits = (uint32_t)(vm >> (kk / kFp4PerWarp * 8 + kk % kFp4PerWarp));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!(bits & 1)) sv[4 * e + 2 * h] = -INFINITY;
-                            if (!(bits & 2)) sv[4 * e + 2 * h + 1] = -INFINITY;
-                        }
-                    }
-                }
-                float mx[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mx[h] = fmaxf(sv[2 * h], sv[2 * h + 1]);
-#pragma unroll
-                    for (int e = 1; e < kFp4Groups; ++e) mx[h] = fmaxf(mx[h], fmaxf(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]));
-                    mx[h] = quad_max(mx[h]);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (mx[h] > (m_run[h] == -INFINITY ? -INFINITY : kLazyLog2)) {  // also the first finite maximum
-                        const float m_new = m0[h] + mx[h];
-                        alpha[h] = exp2f(m_run[h] - m_new);
-                        resc = i > 0;
-                        m_run[h] = m_new;
-#pragma unroll
-                        for (int e = 0; e < kFp4Groups; ++e) {
-                            sv[4 * e + 2 * h] -= mx[h];
-                            sv[4 * e + 2 * h + 1] -= mx[h];
-                        }
-                    }
-                }
-                uint64_t sum[2] = {0ull, 0ull};
-                const int head0 = warp * 16 + hr;
-                const uint32_t prow = sP + b * L::kP + head0 * 128 + 4 * c;
+                for (int h = 0; h < 2; ++h)
+                    unpack_f32x2(fma_f32x2(pack_f32x2(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]), kl, neg[h]),
+                                 &sv[4 * e + 2 * h], &sv[4 * e + 2 * h + 1]);
+            }
+            if ((vm & kFp4AllValid) != kFp4AllValid) {
 #pragma unroll
                 for (int e = 0; e < kFp4Groups; ++e) {
-                    const float4 k = k4[4 * e];
-                    const uint64_t ks = pack_f32x2(k.x, k.y);
+                    const uint32_t bits = (uint32_t)(vm >> (8 * e)) >> (2 * c);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint64_t p = pack_f32x2(ex2_sfu(sv[4 * e + 2 * h]), ex2_sfu(sv[4 * e + 2 * h + 1]));
-                        sum[h] = add_f32x2(sum[h], p);
-                        float p0, p1;  // the probability that multiplies the codes carries the row scale
-                        unpack_f32x2(mul_f32x2(p, ks), &p0, &p1);
-                        if (NH == 64 || head0 + 8 * h < NH)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + h * 1024 + ((e ^ (hr & 7)) << 4)),
-                                         "r"(bf16x2_rn(p0, p1))
-                                         : "memory");
+                        if (!(bits & 1)) sv[4 * e + 2 * h] = -INFINITY;
+                        if (!(bits & 2)) sv[4 * e + 2 * h + 1] = -INFINITY;
                     }
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) l_run[h] = fma_f32x2(l_run[h], pack_f32x2(alpha[h], alpha[h]), sum[h]);
             }
+            float mx[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(sv[2 * h], sv[2 * h + 1]);
+#pragma unroll
+                for (int e = 1; e < kFp4Groups; ++e) mx[h] = fmaxf(mx[h], fmaxf(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]));
+                mx[h] = quad_max(mx[h]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (mx[h] > (m_run[h] == -INFINITY ? -INFINITY : kLazyLog2)) {  // also the first finite maximum
+                    const float m_new = m0[h] + mx[h];
+                    alpha[h] = exp2f(m_run[h] - m_new);
+                    resc = !(info & kFirst);
+                    m_run[h] = m_new;
+#pragma unroll
+                    for (int e = 0; e < kFp4Groups; ++e) {
+                        sv[4 * e + 2 * h] -= mx[h];
+                        sv[4 * e + 2 * h + 1] -= mx[h];
+                    }
+                }
+            }
+            uint64_t sum[2] = {0ull, 0ull};
+            const uint32_t prow = sP + b * L::kP + head0 * 128 + 4 * c;
+#pragma unroll
+            for (int e = 0; e < kFp4Groups; ++e) {
+                const float4 k = k4[4 * e];
+                const uint64_t ks = pack_f32x2(k.x, k.y);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t p = pack_f32x2(ex2_sfu(sv[4 * e + 2 * h]), ex2_sfu(sv[4 * e + 2 * h + 1]));
+                    sum[h] = add_f32x2(sum[h], p);
+                    float p0, p1;  // the probability that multiplies the codes carries the row scale
+                    unpack_f32x2(mul_f32x2(p, ks), &p0, &p1);
+                    if (NH == 64 || head0 + 8 * h < NH)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + h * 1024 + ((e ^ (hr & 7)) << 4)),
+                                     "r"(bf16x2_rn(p0, p1))
+                                     : "memory");
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) l_run[h] = fma_f32x2(l_run[h], pack_f32x2(alpha[h], alpha[h]), sum[h]);
             if (c == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (NH == 64 || warp * 16 + hr + 8 * h < NH) s_alpha[b * NH + warp * 16 + hr + 8 * h] = alpha[h];
+                    if (NH == 64 || head0 + 8 * h < NH) s_alpha[b * NH + head0 + 8 * h] = alpha[h];
             }
             const bool any = __any_sync(0xffffffffu, resc);
-            if (lane == 0) s_vote[b * 4 + warp] = any ? 1 : 0;
+            if (lane == 0) {
+                s_vote[b * 4 + warp] = any ? 1 : 0;
+                if (warp == 0) s_pinfo[b] = info;
+            }
             fence_proxy_async_smem();  // P^T stores -> async proxy
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[b]);
-            if (tid == 0) DSA_TRACE(i, 5);
-        }
-        if (n_mine > 0) {  // the last product must be complete before O^T is read
-            rescale(n_mine - 1);
-            ok = ok && wait_pv(n_mine - 1);
-            tc_fence_after();
-        }
+            if (lane == 0) {
+                mbar_arrive(&pfull[b]);
+                mbar_arrive(&kfree[at]);
+            }
+            if (tid == 0) DSA_TRACE(g, 5);
+            if (info & kLast) {
+                const bool fault = seen & kFp4Fault;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int head = warp * 16 + hr + 8 * h;
-            float l0, l1;
-            unpack_f32x2(l_run[h], &l0, &l1);
-            const float l = quad_sum(l0 + l1);
-            if (c == 0 && head < NH) {
-                // a NaN among masked or absent maxima only: give the partial a weight, so that the NaN reaches the row
-                s_own[head] = m_run[h] == -INFINITY && l != l ? 0.f : m_run[h];
-                s_own[NH + head] = l;
-                s_own[2 * NH + head] = l;
+                for (int h = 0; h < 2; ++h) {
+                    const int head = head0 + 8 * h;
+                    float l0, l1;
+                    unpack_f32x2(l_run[h], &l0, &l1);
+                    const float l = quad_sum(l0 + l1);
+                    if (c != 0 || (NH < 64 && head >= NH)) continue;
+                    if constexpr (ROWS) {  // the output's factor, and the log-sum-exp
+                        const bool some = !(l <= 0.f) && !fault;
+                        s_inv[(rows & 1) * NH + head] = some ? (float)(1 << kFp4Shift) / l : 0.f;
+                        const int row = row_of(unit);
+                        if (a.lse)
+                            a.lse[(long long)row * a.heads + (unit - row * a.hg_count) * NH + head] =
+                                some ? (m_run[h] + log2f(l)) / kLog2e : -INFINITY;
+                    } else {  // read after the last product (their place is in the ring)
+                        l_run[h] = pack_f32x2(l, 0.f);
+                    }
+                }
+                if constexpr (ROWS) {
+                    if (tid == 0) {
+                        s_orow[(rows & 1) * 4] = unit;
+                        s_orow[(rows & 1) * 4 + 2] = pos;
+                        s_orow[(rows & 1) * 4 + 3] = fault;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ostat);
+                    ++rows;
+                }
+            }
+            if (info & kFinal) {
+                rescale(g);
+                if constexpr (!ROWS) {  // the last product must be complete before O^T is read
+                    ok = __all_sync(0xffffffffu, ok && wait_pv(g));
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int head = head0 + 8 * h;
+                        float l, l1;
+                        unpack_f32x2(l_run[h], &l, &l1);
+                        if (c == 0 && (NH == 64 || head < NH)) {
+                            // a NaN among masked or absent maxima only: give the partial a weight, so that the NaN
+                            // reaches the row
+                            s_own[head] = m_run[h] == -INFINITY && l != l ? 0.f : m_run[h];
+                            s_own[NH + head] = l;
+                            s_own[2 * NH + head] = l;
+                        }
+                    }
+                    if (tid == 0 && (seen & kFp4Fault)) *s_fault = 1;
+                }
+                break;
             }
         }
-        ok = __all_sync(0xffffffffu, ok);
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
     }
 
-    attn_finish<NH, L, false, kFp4Shift, true>(a, &omap, smem, tmem, tO, row, split, hg, crank, csize, n_mine, ok);
+    if constexpr (ROWS) {
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 0) tmem_dealloc(tmem, L::kTmemCols);
+    } else {
+        const int row = row_of(unit0);
+        attn_finish<NH, L, false, kFp4Shift, true>(a, &omap, smem, tmem, tO, row, split, unit0 - row * a.hg_count, crank,
+                                                   csize, 1, ok);
+    }
 }
 
 template <int NH>
@@ -687,13 +981,20 @@ static dsa_status_t launch(AttnArgs a, int cl, cudaStream_t st) {
     if (!make_out_map(&omap, a.out8 ? static_cast<void*>(a.out8) : static_cast<void*>(a.out), (uint64_t)a.rows * a.heads,
                       NH, a.out8 != nullptr))
         return DSA_ERR_CUDA;
-    if (cudaFuncSetAttribute(attn_fp4_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) !=
-        cudaSuccess)
-        return DSA_ERR_CUDA;
-    const long long grid = (long long)a.rows * a.hg_count * a.nsplit * cl;
+    const long long units = (long long)a.rows * a.hg_count, grid = units * a.nsplit * cl;
     if (grid > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
-    cudaError_t e = launch_pdl_cluster(attn_fp4_kernel<NH>, dim3((unsigned)grid), dim3(kClThreads), L::kAlloc, st,
-                                       cl, qmap, omap, a);
+    // whole rows in a CTA, written as bf16: the kernel that runs on from row to row (the e4m3 output needs each 128-dim
+    // block's largest value first)
+    const bool rows = cl == 1 && a.nsplit == 1 && !a.out8;
+    auto kernel = rows ? attn_fp4_kernel<NH, true> : attn_fp4_kernel<NH, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    cudaError_t e;
+    if (rows)
+        e = launch_pdl(kernel, dim3((unsigned)std::min<long long>(units, sm_count())), dim3(kClThreads), L::kAlloc, st,
+                       qmap, omap, a);
+    else
+        e = launch_pdl_cluster(kernel, dim3((unsigned)grid), dim3(kClThreads), L::kAlloc, st, cl, qmap, omap, a);
     if (e == cudaSuccess && a.nsplit > 1) e = launch_attn_combine(a, st);
     if (e != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();

@@ -506,3 +506,75 @@ def test_attention_when_the_running_maximum_moves(name):
     torch.cuda.synchronize()
     assert int(status) == 0
     _check(out, lse, _expected(case))
+
+
+@gpu
+@pytest.mark.parametrize("heads,nq", [(64, 500), (128, 170), (16, 700)])
+def test_attention_many_rows_in_turn(heads, nq):
+    """More rows than the GPU holds at once, of lengths from one key to many, in an order that mixes them."""
+    spec = S("many", cached=[0] * 2, new=[nq // 2, nq - nq // 2], queries="all", heads=heads, topk=150, window=128,
+             seed=70 + heads, **F)
+    case = _attn_case(spec, "random", seed=heads)
+    order = torch.randperm(nq, generator=torch.Generator().manual_seed(1))
+    for k in ("q", "q_pos", "q_req", "topk"):
+        case[k] = case[k][order].contiguous()
+    case["nvis"] = case["nvis"][order.numpy()]
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    _check(out, lse, _expected(case, range(0, nq, 3)))
+
+
+@gpu
+@pytest.mark.parametrize("rows,heads", [(3, 64), (200, 64), (200, 16)])
+def test_attention_faults_zero_their_rows_only(rows, heads):
+    """A position below zero, a request outside the tables, an unmapped or out-of-pool block of each pool, an entry that is
+    not visible: zeros, lse -inf and the device status; every other row is right."""
+    spec = S("faults", cached=[900 + i for i in range(rows)], new=[1] * rows, heads=heads, topk=40, seed=81, **F)
+    case = _attn_case(spec, "random", seed=5)
+    g = np.random.default_rng(0)
+    bad = {}
+    for i, j in enumerate(range(0, rows, 1 if rows < 10 else 7)):
+        kind = i % 6 if rows >= 10 else [1, 3, 5][i]
+        bad[j] = kind
+        if kind == 0:
+            case["q_pos"][j] = -1
+        elif kind == 1:
+            first = int(case["topk"][j][case["topk"][j] >= 0][0])
+            case["bt_main"][j, first // case["epb"]] = -1
+        elif kind == 2:
+            first = int(case["topk"][j][case["topk"][j] >= 0][0])
+            case["bt_main"][j, first // case["epb"]] = 10 ** 6
+        elif kind == 3:
+            case["bt_swa"][j, int(case["q_pos"][j]) // 256] = -1
+        elif kind == 4:
+            case["bt_swa"][j, int(case["q_pos"][j]) // 256] = 2 ** 30
+        else:
+            case["topk"][j, int((case["topk"][j] >= 0).nonzero()[0])] = int(case["nvis"][j])
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == dsa.DSA_ERR_DEVICE_FAULT
+    for j in bad:
+        assert not np64(out[j]).any() and np.isneginf(np64(lse[j])).all(), (j, bad[j])
+    _check(out, lse, _expected(case, [j for j in range(rows) if j not in bad][:40]) if rows > 3 else {})
+
+
+@gpu
+@pytest.mark.parametrize("rows", [4, 200])
+def test_a_row_of_nan_reaches_only_the_queries_that_read_it(rows):
+    spec = S("nan", cached=[600] * rows, new=[1] * rows, heads=64, topk=30, window=16, seed=91, **F)
+    case = _attn_case(spec, "random", seed=6)
+    hit = list(range(0, rows, 3))
+    for j in hit:      # the row of one of j's selected entries, or (every other) of its own window
+        if j % 2:
+            p = int(case["q_pos"][j]) - 3
+            case["swa_scale"][_physical(case["bt_swa"], j, p, 256)] = float("nan")
+        else:
+            i = int(case["topk"][j][case["topk"][j] >= 0][2])
+            case["main_scale"][_physical(case["bt_main"], j, i, case["epb"])] = float("nan")
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    for j in hit:
+        assert np.isnan(np64(out[j])).all() and np.isnan(np64(lse[j])).all(), j
+    _check(out, lse, _expected(case, [j for j in range(rows) if j not in hit][:40]))
