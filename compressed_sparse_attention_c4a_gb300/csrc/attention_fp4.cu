@@ -58,23 +58,17 @@ constexpr int kFp4Shift = 8;
 // Bounded wait (2 s of %globaltimer).  Only the first try is inline: the kernel's roles run side by side and share the
 // instruction caches, and with every wait's loop, every tile loop unrolled and the rare paths inline the schedulers
 // mostly waited for instructions (3.9 cycles of it per issued instruction).
-__device__ __noinline__ bool wait_bar_slow(uint32_t addr, uint32_t parity) {
+__device__ __noinline__ bool wait_bar_slow(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = global_ns();
-    while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity), "r"(20000u)  // suspended for up to 20 us at a time
-            : "memory");
-        if (done) return true;
-        if (global_ns() - t0 > kWaitLimitNs) return false;
-    }
+    do {
+#pragma unroll 1
+        for (int k = 0; k < 64; ++k)
+            if (mbar_try_wait(bar, parity)) return true;
+    } while (global_ns() - t0 <= kWaitLimitNs);
+    return false;
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_bar_slow(smem_u32(bar), parity);
+    return mbar_try_wait(bar, parity) || wait_bar_slow(bar, parity);
 }
 
 template <int NH>
@@ -203,6 +197,10 @@ __device__ __forceinline__ void tmem_ld_16x48_nowait(uint32_t taddr, float (&v)[
                  : "memory");
 }
 
+// A descriptor like d with this low word (address, leading offset): the sum of a descriptor and an offset within shared
+// memory carries nothing into the high word.
+__device__ __forceinline__ uint64_t desc_lo(uint64_t d, uint32_t lo) { return (d & 0xffffffff00000000ull) | lo; }
+
 // Two fp32 values in one register pair (packed arithmetic halves the instructions of the softmax).
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
     uint64_t d;
@@ -258,48 +256,52 @@ __device__ __noinline__ void rescale_quadrant(uint32_t taddr, const float* alpha
 template <int NH>
 __device__ __noinline__ void store_row(const RopeTable& rope, uint16_t* out_row, uint32_t taddr, const float* inv, int ww,
                                        int m, bool fault) {
-    constexpr int kHeads = NH / 2, kStep = 8;
+    constexpr int kHeads = NH / 2, kStep = kHeads < 16 ? kHeads : 16, kSteps = kHeads / kStep;
     const int lane = threadIdx.x & 31, quad = ww & 3, hbase = (ww >> 2) * kHeads;
     const bool odd = lane & 1;
     const uint32_t pick = odd ? 0x3276u : 0x5410u;
     const int first_rot = kD - rope.rope_dim;
-    uint16_t* const out = out_row + (hbase + (odd ? 1 : 0)) * kD;
+    uint16_t* const out = out_row + (hbase + (odd ? 1 : 0)) * kD + quad * 32 + (lane & ~1);
     taddr += ((uint32_t)(quad * 32) << 16) + hbase;
+    inv += hbase;
+    float v[kStep];
+    tmem_ld_nowait<kStep>(taddr, v);
 #pragma unroll 1
-    for (int tt = 0; tt < 4; ++tt) {
+    for (int n = 0; n < 4 * kSteps; ++n) {  // 128-dim tile n / kSteps, kStep heads
+        const int tt = n / kSteps, h0 = n % kSteps * kStep;
         const int dim = tt * 128 + quad * 32 + (lane & ~1);  // the pair's even dim
-        const bool rotated = __any_sync(0xffffffffu, dim >= first_rot);
-        float cs = 1.f, sn = 0.f;
-        if (rotated && dim >= first_rot && !fault) rope_cos_sin(m, rope, (dim - first_rot) >> 1, &cs, &sn);
-        uint32_t* to = reinterpret_cast<uint32_t*>(out + dim);
-        float v[kStep];
-        tmem_ld_nowait<kStep>(taddr + tt * NH, v);
-#pragma unroll 1
-        for (int h0 = 0; h0 < kHeads; h0 += kStep) {
-            tmem_wait_ld();
-            tmem_regs_after_wait<kStep>(v);
-            float x[kStep];
+        float x[kStep];
+        tmem_wait_ld();
+        tmem_regs_after_wait<kStep>(v);
 #pragma unroll
-            for (int e = 0; e < kStep; e += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(inv + hbase + h0 + e);
-                x[e] = v[e] * f.x, x[e + 1] = v[e + 1] * f.y, x[e + 2] = v[e + 2] * f.z, x[e + 3] = v[e + 3] * f.w;
-            }
-            if (h0 + kStep < kHeads) tmem_ld_nowait<kStep>(taddr + tt * NH + h0 + kStep, v);
-#pragma unroll
-            for (int e = 0; e < kStep; e += 2) {
-                uint32_t w;
-                if (!rotated) {
-                    w = bf16x2_rn(x[e], x[e + 1]);
-                    w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), pick);
-                } else {
-                    const float recv = __shfl_xor_sync(0xffffffffu, odd ? x[e] : x[e + 1], 1);
-                    const float lo = odd ? recv : x[e], hi = odd ? x[e + 1] : recv;
-                    w = bf16x2_rn(lo * cs + hi * sn, hi * cs - lo * sn);
-                }
-                to[e * (kD / 2)] = fault ? 0u : w;
-            }
-            to += kStep * (kD / 2);
+        for (int e = 0; e < kStep; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(inv + h0 + e);
+            x[e] = v[e] * f.x, x[e + 1] = v[e + 1] * f.y, x[e + 2] = v[e + 2] * f.z, x[e + 3] = v[e + 3] * f.w;
         }
+        if (n + 1 < 4 * kSteps) tmem_ld_nowait<kStep>(taddr + (n + 1) / kSteps * NH + (n + 1) % kSteps * kStep, v);
+        if (fault) {
+#pragma unroll
+            for (int e = 0; e < kStep; ++e) x[e] = 0.f;
+        }
+        uint32_t* const to = reinterpret_cast<uint32_t*>(out + h0 * kD + tt * 128);
+        uint32_t w[kStep / 2];
+        if (!__any_sync(0xffffffffu, dim >= first_rot)) {
+#pragma unroll
+            for (int e = 0; e < kStep / 2; ++e) w[e] = bf16x2_rn(x[2 * e], x[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < kStep / 2; ++e) w[e] = __byte_perm(w[e], __shfl_xor_sync(0xffffffffu, w[e], 1), pick);
+        } else {
+            float cs = 1.f, sn = 0.f;
+            if (dim >= first_rot && !fault) rope_cos_sin(m, rope, (dim - first_rot) >> 1, &cs, &sn);
+#pragma unroll
+            for (int e = 0; e < kStep / 2; ++e) {
+                const float recv = __shfl_xor_sync(0xffffffffu, odd ? x[2 * e] : x[2 * e + 1], 1);
+                const float lo = odd ? recv : x[2 * e], hi = odd ? x[2 * e + 1] : recv;
+                w[e] = bf16x2_rn(lo * cs + hi * sn, hi * cs - lo * sn);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kStep / 2; ++e) to[e * kD] = w[e];
     }
 }
 
@@ -388,8 +390,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
-    const uint32_t tS = tmem, tO = tmem + 128;
+    // all 512 columns are this CTA's, so its base is column 0
+    constexpr uint32_t tmem = 0, tS = 0, tO = 128;
     if constexpr (!ROWS)
         if (csize > 1) cluster_arrive_relaxed();  // phase 0: this CTA has started (waited on before DSMEM use)
 
@@ -626,21 +628,19 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 __syncwarp();
                 copy(h);  // the same half of tile g + 1's
                 const uint32_t to = dst0 + slot * kFp4Half;
-#pragma unroll 1
+#pragma unroll
                 for (int u = 0; u < kFp4Pairs; ++u) {
                     const int kk = ww * kFp4PerWarp + 2 * u + q;
-                    const uint32_t at = to + (kk >> 3) * 1024 + (kk & 7) * 128, s2 = block_scale_2p118(byte[0]);
+                    const uint32_t at = to + (kk >> 3) * 1024 + (kk & 7) * 128, s2 = block_scale_2p118(byte[u]);
                     const uint32_t piece = (p0 ^ (kk & 7)) << 4;
-                    uint32_t o[4], o2[4];
-                    widen8(hf ? code[0].y : code[0].x, s2, o);
-                    widen8(hf ? code[0].x : code[0].y, s2, o2);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + piece), "r"(o[0]), "r"(o[1]),
-                                 "r"(o[2]), "r"(o[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (piece ^ 16u)), "r"(o2[0]), "r"(o2[1]),
-                                 "r"(o2[2]), "r"(o2[3])
-                                 : "memory");
-                    code[0] = code[1], code[1] = code[2], byte[0] = byte[1], byte[1] = byte[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t o[4];
+                        widen8((e != 0) != (hf != 0) ? code[u].y : code[u].x, s2, o);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (piece ^ (16u * e))), "r"(o[0]),
+                                     "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                     : "memory");
+                    }
                 }
                 fence_proxy_async_smem();  // the bf16 rows -> visible to the tensor core (async proxy)
                 __syncwarp();
@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
     } else if (warp == 5) {
         // ---- O^T += V^T P^T, issued by one elected lane ------------------------------------------------------
         const uint32_t idesc_o = idesc_bf16(NH, 1, 128);
+        const uint64_t dp = sw128_desc(sP, 16, 1024), dv = sw128_desc(sK, kFp4Chunk, 1024);
         uint32_t rescales = 0, rows = 0;
         int slot = 0;
         for (int g = 0; ok; ++g) {
@@ -686,17 +687,18 @@ __global__ void __launch_bounds__(kClThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) DSA_TRACE(g, 6);
-            const uint64_t dp = sw128_desc(sP + b * L::kP, 16, 1024);
+            const uint32_t p_lo = __shfl_sync(0xffffffffu, (uint32_t)sw128_desc(sP + b * L::kP, 16, 1024), 0);
+            const uint32_t more = info & kFirst ? 0u : 1u;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                const uint64_t dv = sw128_desc(sK + slot * kFp4Half, kFp4Chunk, 1024);
-#pragma unroll 1
+                const uint32_t v_lo = __shfl_sync(0xffffffffu, (uint32_t)sw128_desc(sK + slot * kFp4Half, kFp4Chunk, 1024), 0);
+                const uint32_t d = __shfl_sync(0xffffffffu, tO + 2 * h * NH, 0);
+#pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                     for (int ks = 0; ks < kFp4Keys / 16; ++ks)
-                        mma_bf16_ss_elect(tO + (2 * h + mt) * NH,
-                                          dv + (uint64_t)(((2 * mt) * kFp4Chunk + (2 * ks) * 1024) >> 4),
-                                          dp + (uint64_t)((ks * 32) >> 4), idesc_o, (!(info & kFirst) || ks > 0) ? 1u : 0u);
+                        mma_bf16_ss_elect(d + mt * NH, desc_lo(dv, v_lo + (((2 * mt) * kFp4Chunk + (2 * ks) * 1024) >> 4)),
+                                          desc_lo(dp, p_lo + ((ks * 32) >> 4)), idesc_o, ks > 0 ? 1u : more);
                 mma_commit_elect(&pvdone[slot]);
                 if (++slot == kFp4Ring) slot = 0;
             }
@@ -734,14 +736,15 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (lane == 0 && h == 0) DSA_TRACE(g, 2);
-                const uint64_t dk = sw128_desc(sK + slot * kFp4Half, 16, 1024);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c)  // 64-dim chunks: 64 query rows / 48 key rows apart
+                // 64-dim chunks: 64 query rows / 48 key rows apart
+                const uint32_t q_lo = __shfl_sync(0xffffffffu, (uint32_t)dq + ((4 * h * 8192) >> 4), 0);
+                const uint32_t k_lo = __shfl_sync(0xffffffffu, (uint32_t)sw128_desc(sK + slot * kFp4Half, 16, 1024), 0);
+                const uint32_t d = __shfl_sync(0xffffffffu, tS + b * 64, 0);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16_ss_elect(tS + b * 64, dq + (uint64_t)(((4 * h + c) * 8192 + ks * 32) >> 4),
-                                          dk + (uint64_t)((c * kFp4Chunk + ks * 32) >> 4), idesc_s,
-                                          h + c + ks > 0 ? 1u : 0u);
+                for (int i = 0; i < 16; ++i)
+                    mma_bf16_ss_elect(d, desc_lo(dq, q_lo + (((i >> 2) * 8192 + (i & 3) * 32) >> 4)),
+                                      desc_lo(dq, k_lo + (((i >> 2) * kFp4Chunk + (i & 3) * 32) >> 4)), idesc_s,
+                                      i > 0 ? 1u : (uint32_t)h);
             }
             if (!ok) break;
             const int unit = s_info[4 * (g % kFp4Entries) + 1];
