@@ -9,7 +9,12 @@
 
 namespace dsa {
 
-constexpr int kRowThreads = 256;  // 8 warps, a row each
+constexpr int kRowThreads = 256;  // 8 warps, a row each, or four in turn
+
+// Rows per warp: four consecutive ones, whose addresses four lanes find side by side and whose loads are in flight
+// together, when there are enough rows for two blocks of such warps on every SM.  Measured, four against one: 131,072 rows
+// stored 38 against 47 us, 16,384 scattered rows read 5.0 against 5.6; 5,000 rows stored and read 6.6 against 5.9.
+static int rows_per_warp(long long n) { return n >= 2ll * 4 * 8 * sm_count() ? 4 : 1; }
 
 struct CacheWriteArgs {
     int batch, n;
@@ -19,6 +24,7 @@ struct CacheWriteArgs {
     dsa_pool_t pool;
     dsa_block_table_t bt;
     int32_t* status;
+    bool wide;  // x 32-byte aligned
 };
 
 // The request of new row j: the largest r with cu_new[r] <= j, by a search of 32 probes a step (one for up to 32
@@ -35,30 +41,62 @@ __device__ __forceinline__ int request_of(const int32_t* cu_new, int batch, int 
     return lo;
 }
 
-// One warp per row.  The schedule and the block table are read before waiting for the preceding kernel.
-template <int DIM>
+// physical_row() of a row below 2^32: a 32-bit division.
+__device__ __forceinline__ long long pool_row(const dsa_block_table_t& bt, int r, uint32_t row, const dsa_pool_t& pool) {
+    const uint32_t lb = row / (uint32_t)pool.rows_per_block;
+    if (lb >= (uint32_t)bt.max_blocks) return -1;
+    const int pb = __ldg(bt.table + (long long)r * bt.max_blocks + lb);
+    if (pb < 0 || pb >= pool.num_blocks) return -1;
+    return (long long)pb * pool.rows_per_block + (row - lb * (uint32_t)pool.rows_per_block);
+}
+
+// A warp takes R consecutive rows.  BLOCK: a pool of DSA_FP4_BLOCK, else any other.  The schedule and the block table are read before waiting for the preceding kernel.
+template <int DIM, int R, bool BLOCK>
 __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(CacheWriteArgs a) {
     constexpr int E = DIM / 32;
     const int lane = threadIdx.x & 31;
-    const long long j = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-    long long prow = -1;
-    bool live = false;
-    if (j < a.n && j < __ldg(a.cu_new + a.batch)) {
-        const int r = request_of(a.cu_new, a.batch, (int)j, lane);
-        const long long row = (long long)__ldg(a.start_row + r) + (j - __ldg(a.cu_new + r));
-        live = true;
-        prow = physical_row(a.bt, r, row, a.pool.rows_per_block, a.pool.num_blocks);
+    const long long j0 = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * R;
+    const int total = min(a.n, __ldg(a.cu_new + a.batch));
+    const int live = (int)min((long long)R, total - j0);
+    long long prow = -1;  // lane i < live: of row j0 + i
+    if (live > 0) {
+        int r = request_of(a.cu_new, a.batch, (int)j0, lane);
+        if constexpr (R > 1) {
+            const int last = request_of(a.cu_new, a.batch, (int)j0 + live - 1, lane);
+            for (int hi = last + 1; hi - r > 1;) {  // between the two
+                const int mid = (r + hi) / 2;
+                if (__ldg(a.cu_new + mid) <= j0 + lane) r = mid;
+                else hi = mid;
+            }
+        }
+        if (lane < live) {
+            const long long row = (long long)__ldg(a.start_row + r) + (j0 + lane - __ldg(a.cu_new + r));
+            if (row >= 0) prow = pool_row(a.bt, r, (uint32_t)row, a.pool);
+        }
     }
     pdl_wait();
     pdl_launch_dependents();
-    if (!live) return;
-    if (prow < 0) {
-        if (lane == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
-        return;
+    if (live <= 0) return;
+    if (lane < live && prow < 0) report(a.status, DSA_ERR_DEVICE_FAULT);
+    uint32_t u[R][E / 2];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < live) load_bf16_words<E>(a.x + (j0 + i) * DIM, lane, u[i], a.wide);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const long long to = __shfl_sync(0xffffffffu, prow, i);
+        if (i >= live || to < 0) continue;
+        if constexpr (BLOCK) {
+            uint32_t c[2];
+            float s;
+            const uint8_t bs = fp4_block_codes_bf16(u[i], c, &s);
+            store_fp4_block_row(a.pool, to, lane, c, bs, s);
+        } else {
+            float v[E];
+            bf16_words<E>(u[i], v);
+            store_row<E>(a.pool, to, lane, v);
+        }
     }
-    float v[E];
-    load_bf16<E>(a.x + j * DIM, lane, v);
-    store_row<E>(a.pool, prow, lane, v);
 }
 
 struct CacheReadArgs {
@@ -69,94 +107,120 @@ struct CacheReadArgs {
     dsa_block_table_t bt;
     uint16_t* out;
     int32_t* status;
+    bool wide;  // out 32-byte aligned
 };
 
-// The stored row `prow` as the warp's E values per lane.
+// A lane's part of a stored row as it lies in memory: E elements, the row's scale, the block's.
 template <int E>
-__device__ __forceinline__ void load_row(const dsa_pool_t& pool, long long prow, int lane, float (&v)[E]) {
+struct StoredRow {
+    uint32_t w[E / 2];
+    float scale;
+    uint32_t block;
+};
+
+template <int E>
+__device__ __forceinline__ void fetch_row(const dsa_pool_t& pool, long long prow, int lane, StoredRow<E>& row) {
     const uint8_t* base = static_cast<const uint8_t*>(pool.data);
     if (pool.dtype == DSA_BF16) {
-        load_bf16<E>(reinterpret_cast<const uint16_t*>(base) + prow * (E * 32), lane, v);
+        load_bf16_words<E>(reinterpret_cast<const uint16_t*>(base) + prow * (E * 32), lane, row.w, false);
         return;
     }
-    const float s = pool.scale[prow];
+    row.scale = pool.scale[prow];
     if (pool.dtype == DSA_FP8_E4M3) {
         const uint8_t* src = base + prow * (E * 32) + lane * E;
-        uint16_t c[E / 2];
         if constexpr (E == 16) {
             const uint4 u = *reinterpret_cast<const uint4*>(src);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) c[k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+            row.w[0] = u.x, row.w[1] = u.y, row.w[2] = u.z, row.w[3] = u.w;
+        } else if constexpr (E == 4) {
+            row.w[0] = *reinterpret_cast<const uint32_t*>(src);
         } else {
-#pragma unroll
-            for (int k = 0; k < E / 2; ++k) c[k] = reinterpret_cast<const uint16_t*>(src)[k];
-        }
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(c[k], __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            v[2 * k] = s * f.x;
-            v[2 * k + 1] = s * f.y;
+            row.w[0] = *reinterpret_cast<const uint16_t*>(src);
         }
         return;
     }
     // two e2m1 codes a byte, with a scale per row, or per row and block
     const bool block = pool.dtype == DSA_FP4_BLOCK;
-    const uint8_t* row = base + prow * (block ? kFp4BlockRow : E * 16);
-    float unit = s;
-    if constexpr (E == kFp4Block) {
-        if (block) {
-            const __half_raw h = __nv_cvt_fp8_to_halfraw(row[256 + lane], __NV_E4M3);
-            unit = s * __half2float(*reinterpret_cast<const __half*>(&h));
-        }
-    }
-    uint8_t c[E / 2];
+    const uint8_t* src = base + prow * (block ? kFp4BlockRow : E * 16);
     if constexpr (E == 16) {
-        const uint2 u = *reinterpret_cast<const uint2*>(row + lane * 8);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = (uint8_t)((k < 4 ? u.x : u.y) >> (8 * (k & 3)));
+        if (block) row.block = src[kFp4BlockRow - 32 + lane];
+        const uint2 u = *reinterpret_cast<const uint2*>(src + lane * 8);
+        row.w[0] = u.x, row.w[1] = u.y;
+    } else if constexpr (E == 4) {
+        row.w[0] = *reinterpret_cast<const uint16_t*>(src + lane * 2);
     } else {
+        row.w[0] = src[lane];
+    }
+}
+
+template <int E>
+__device__ __forceinline__ void row_values(int dtype, const StoredRow<E>& row, float (&v)[E]) {
+    if (dtype == DSA_FP8_E4M3) {
 #pragma unroll
-        for (int k = 0; k < E / 2; ++k) c[k] = row[lane * (E / 2) + k];
+        for (int k = 0; k < E / 2; ++k) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(row.w[k / 2] >> (16 * (k & 1))), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            v[2 * k] = row.scale * f.x;
+            v[2 * k + 1] = row.scale * f.y;
+        }
+        return;
+    }
+    float unit = row.scale;
+    if constexpr (E == kFp4Block) {
+        if (dtype == DSA_FP4_BLOCK) {
+            const __half_raw h = __nv_cvt_fp8_to_halfraw((uint8_t)row.block, __NV_E4M3);
+            unit = row.scale * __half2float(*reinterpret_cast<const __half*>(&h));
+        }
     }
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) {
-        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(c[k], __NV_E2M1);
+        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((uint8_t)(row.w[k / 4] >> (8 * (k & 3))), __NV_E2M1);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
         v[2 * k] = unit * f.x;
         v[2 * k + 1] = unit * f.y;
     }
 }
 
-// One warp per row.
-template <int DIM>
+// A warp takes R consecutive rows.
+template <int DIM, int R>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(CacheReadArgs a) {
     constexpr int E = DIM / 32;
     const int lane = threadIdx.x & 31;
-    const long long j = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const long long j0 = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * R;
     pdl_wait();
     pdl_launch_dependents();
-    if (j >= a.n) return;
-    const int id = __ldg(a.ids + j), r = __ldg(a.req + j);
-    long long prow = -1;
-    if (id >= 0 && r >= 0 && r < a.bt.batch)
-        prow = physical_row(a.bt, r, id, a.pool.rows_per_block, a.pool.num_blocks);
-    if (prow < 0 && id != -1 && lane == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
-    float v[E] = {};
-    if (prow >= 0) load_row<E>(a.pool, prow, lane, v);
-    uint32_t u[E / 2];
+    const int live = (int)min((long long)R, a.n - j0);
+    if (live <= 0) return;
+    long long prow = -1;  // lane i < live: of row j0 + i
+    if (lane < live) {
+        const int id = __ldg(a.ids + j0 + lane), r = __ldg(a.req + j0 + lane);
+        if (id >= 0 && r >= 0 && r < a.bt.batch)
+            prow = pool_row(a.bt, r, (uint32_t)id, a.pool);
+        if (prow < 0 && id != -1) report(a.status, DSA_ERR_DEVICE_FAULT);
+    }
+    StoredRow<E> row[R];
+    long long from[R];
 #pragma unroll
-    for (int k = 0; k < E / 2; ++k)
-        u[k] = (uint32_t)float_to_bf16(v[2 * k]) | ((uint32_t)float_to_bf16(v[2 * k + 1]) << 16);
-    uint16_t* dst = a.out + j * DIM + lane * E;
-    if constexpr (E == 16) {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-    } else if constexpr (E == 4) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
-    } else {
-        *reinterpret_cast<uint32_t*>(dst) = u[0];
+    for (int i = 0; i < R; ++i) {
+        from[i] = __shfl_sync(0xffffffffu, prow, i);
+        if (from[i] >= 0) fetch_row<E>(a.pool, from[i], lane, row[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (i >= live) break;
+        uint32_t u[E / 2] = {};
+        if (from[i] >= 0) {
+            if (a.pool.dtype == DSA_BF16) {
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k) u[k] = row[i].w[k];
+            } else {
+                float v[E];
+                row_values<E>(a.pool.dtype, row[i], v);
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k)
+                    u[k] = (uint32_t)float_to_bf16(v[2 * k]) | ((uint32_t)float_to_bf16(v[2 * k + 1]) << 16);
+            }
+        }
+        store_words<E / 2>(a.out + (j0 + i) * DIM + lane * E, u, a.wide);
     }
 }
 
@@ -178,12 +242,18 @@ extern "C" dsa_status_t dsa_cache_write(int32_t batch, const int32_t* cu_new, co
     const dsa_status_t e = check_rows(pool, bt);
     if (e != DSA_OK) return e;
     if (!cu_new || !start_row || !x || !aligned(x, 16) || bt->batch < batch) return DSA_ERR_INVALID_ARG;
-    const CacheWriteArgs a{batch, n, cu_new, start_row, static_cast<const uint16_t*>(x), *pool, *bt, dev_status};
-    const dim3 grid((unsigned)((n + 7ll) / 8)), block(kRowThreads);
+    const CacheWriteArgs a{batch, n, cu_new, start_row, static_cast<const uint16_t*>(x), *pool, *bt, dev_status, aligned(x, 32)};
+    const bool four = rows_per_warp(n) == 4;
+    const dim3 grid((unsigned)((n + (four ? 31ll : 7ll)) / (four ? 32 : 8))), block(kRowThreads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t err = pool->dim == 64    ? launch_pdl(cache_write_kernel<64>, grid, block, 0, st, a)
-                            : pool->dim == 128 ? launch_pdl(cache_write_kernel<128>, grid, block, 0, st, a)
-                                               : launch_pdl(cache_write_kernel<512>, grid, block, 0, st, a);
+    const cudaError_t err =
+        pool->dtype == DSA_FP4_BLOCK
+            ? launch_pdl(four ? cache_write_kernel<512, 4, true> : cache_write_kernel<512, 1, true>, grid, block, 0, st, a)
+        : pool->dim == 64
+            ? launch_pdl(four ? cache_write_kernel<64, 4, false> : cache_write_kernel<64, 1, false>, grid, block, 0, st, a)
+        : pool->dim == 128
+            ? launch_pdl(four ? cache_write_kernel<128, 4, false> : cache_write_kernel<128, 1, false>, grid, block, 0, st, a)
+            : launch_pdl(four ? cache_write_kernel<512, 4, false> : cache_write_kernel<512, 1, false>, grid, block, 0, st, a);
     if (err != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();
 }
@@ -196,12 +266,14 @@ extern "C" dsa_status_t dsa_cache_read(const dsa_pool_t* pool, const dsa_block_t
     const dsa_status_t e = check_rows(pool, bt);
     if (e != DSA_OK) return e;
     if (!req || !ids || !out || !aligned(out, 16)) return DSA_ERR_INVALID_ARG;
-    const CacheReadArgs a{n, req, ids, *pool, *bt, static_cast<uint16_t*>(out), dev_status};
-    const dim3 grid((unsigned)((n + 7ll) / 8)), block(kRowThreads);
+    const CacheReadArgs a{n, req, ids, *pool, *bt, static_cast<uint16_t*>(out), dev_status, aligned(out, 32)};
+    const bool four = rows_per_warp(n) == 4;
+    const dim3 grid((unsigned)((n + (four ? 31ll : 7ll)) / (four ? 32 : 8))), block(kRowThreads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t err = pool->dim == 64    ? launch_pdl(cache_read_kernel<64>, grid, block, 0, st, a)
-                            : pool->dim == 128 ? launch_pdl(cache_read_kernel<128>, grid, block, 0, st, a)
-                                               : launch_pdl(cache_read_kernel<512>, grid, block, 0, st, a);
+    const cudaError_t err =
+        pool->dim == 64    ? launch_pdl(four ? cache_read_kernel<64, 4> : cache_read_kernel<64, 1>, grid, block, 0, st, a)
+        : pool->dim == 128 ? launch_pdl(four ? cache_read_kernel<128, 4> : cache_read_kernel<128, 1>, grid, block, 0, st, a)
+                           : launch_pdl(four ? cache_read_kernel<512, 4> : cache_read_kernel<512, 1>, grid, block, 0, st, a);
     if (err != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();
 }

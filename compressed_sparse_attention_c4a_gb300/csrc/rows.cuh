@@ -60,32 +60,118 @@ __device__ __forceinline__ uint8_t fp4_block_codes(const float (&v)[kFp4Block], 
     return bs8;
 }
 
+// The same for a row of bf16 values (the lane's block as packed words), row scale included, with half the instructions.
+// A quotient q of a bf16 value (8 significant bits) by a scale (4) that is not one of the borders between two codes (3)
+// differs from it by more than 2^-8 of it, at least 2^-10.  So q may be off by 2^-20 before it is rounded to a multiple of
+// 2^-19, which every border is: the fused multiply-add adds 24, whose neighbours are 2^-19 apart, to v (1 / (s bs)), and
+// 24 is taken off again.  The reciprocal's 2^-23 makes 2^-20.6 at the largest border, 5; from 8 on (a scale at the end of
+// e4m3's range) the code is the largest either way.
+__device__ __forceinline__ uint8_t fp4_block_codes_bf16(uint32_t (&u)[kFp4Block / 2], uint32_t (&c)[2], float* s) {
+    uint32_t m2 = 0u;
+#pragma unroll
+    for (int k = 0; k < kFp4Block / 2; ++k) m2 = __vmaxu2(m2, u[k] & 0x7fff7fffu);
+    const uint32_t m = max(m2 << 16, m2 & 0xffff0000u);
+    float inv_s;
+    fp4_block_row_scale(warp_abs_max_bits(m), s, &inv_s);
+    float a = __uint_as_float(m) * inv_s;
+    if (inv_s == 0.f) {  // the row holds an infinity or a NaN
+        a = 0.f;
+#pragma unroll
+        for (int k = 0; k < kFp4Block / 2; ++k) u[k] = 0u;
+    }
+    const float a0 = a * (1.f / 6.f);  // and a correction, which makes it the quotient
+    const uint8_t bs8 = float_to_e4m3(fmaf(fmaf(-a0, 6.f, a), 1.f / 6.f, a0));
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(bs8, __NV_E4M3);
+    const float bs = __half2float(*reinterpret_cast<const __half*>(&h));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(bs));
+    r = bs > 0.f ? r : 0.f;
+    if (inv_s > 0x1p100f) {  // a row of tiny values: r / s could leave fp32's range
+#pragma unroll
+        for (int k = 0; k < kFp4Block / 2; ++k) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(u[k]) : "r"(0x5F805F80u));  // 2^64
+        inv_s *= 0x1p-64f;
+    }
+    r *= inv_s;
+    c[0] = c[1] = 0u;
+#pragma unroll
+    for (int k = 0; k < kFp4Block / 2; ++k) {
+        const float v[2] = {__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u)};
+        uint64_t t;
+        asm("{\n\t.reg .b64 v, k, c;\n\t"
+            "mov.b64 v, {%1, %2};\n\tmov.b64 k, {%3, %3};\n\tmov.b64 c, {%4, %4};\n\t"
+            "fma.rn.f32x2 v, v, k, c;\n\tmov.b64 c, {%5, %5};\n\tadd.rn.f32x2 %0, v, c;\n\t}"
+            : "=l"(t)
+            : "f"(v[0]), "f"(v[1]), "f"(r), "f"(24.f), "f"(-24.f));
+        c[k / 4] |= (uint32_t)float2_to_e2m1x2(__uint_as_float((uint32_t)t), __uint_as_float((uint32_t)(t >> 32)))
+                    << (8 * (k % 4));
+    }
+    return bs8;
+}
+
 // ---- rows ------------------------------------------------------------------------------------------------------
 // A warp owns a row, each lane E = dim / 32 consecutive elements.
 template <int E>
-__device__ __forceinline__ void load_bf16(const uint16_t* row, int lane, float (&v)[E]) {
+__device__ __forceinline__ void load_bf16_words(const uint16_t* row, int lane, uint32_t (&u)[E / 2], bool wide) {
     const uint16_t* p = row + lane * E;
     if constexpr (E == 16) {
-        uint4 a = *reinterpret_cast<const uint4*>(p);
-        uint4 b = *reinterpret_cast<const uint4*>(p + 8);
-        uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[2 * k] = __uint_as_float(u[k] << 16);
-            v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+        if (wide) {  // 32-byte aligned: one access (two of 16 bytes each touch half of every sector)
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                         : "l"(p)
+                         : "memory");
+            return;
         }
+        const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 8);
+        u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
     } else if constexpr (E == 4) {
-        uint2 a = *reinterpret_cast<const uint2*>(p);
-        v[0] = __uint_as_float(a.x << 16);
-        v[1] = __uint_as_float(a.x & 0xffff0000u);
-        v[2] = __uint_as_float(a.y << 16);
-        v[3] = __uint_as_float(a.y & 0xffff0000u);
+        const uint2 a = *reinterpret_cast<const uint2*>(p);
+        u[0] = a.x, u[1] = a.y;
     } else {
         static_assert(E == 2, "row width");
-        uint32_t a = *reinterpret_cast<const uint32_t*>(p);
-        v[0] = __uint_as_float(a << 16);
-        v[1] = __uint_as_float(a & 0xffff0000u);
+        u[0] = *reinterpret_cast<const uint32_t*>(p);
     }
+}
+template <int E>
+__device__ __forceinline__ void bf16_words(const uint32_t (&u)[E / 2], float (&v)[E]) {
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+        v[2 * k] = __uint_as_float(u[k] << 16);
+        v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+}
+template <int E>
+__device__ __forceinline__ void load_bf16(const uint16_t* row, int lane, float (&v)[E]) {
+    uint32_t u[E / 2];
+    load_bf16_words<E>(row, lane, u, false);
+    bf16_words<E>(u, v);
+}
+
+// N words to consecutive memory.
+template <int N>
+__device__ __forceinline__ void store_words(uint16_t* p, const uint32_t (&u)[N], bool wide) {
+    if constexpr (N == 8) {
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                         "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                         : "memory");
+            return;
+        }
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    } else {
+        static_assert(N == 1, "words");
+        *reinterpret_cast<uint32_t*>(p) = u[0];
+    }
+}
+
+__device__ __forceinline__ void store_fp4_block_row(const dsa_pool_t& pool, long long prow, int lane, const uint32_t (&c)[2],
+                                                    uint8_t bs, float s) {
+    uint8_t* dst = reinterpret_cast<uint8_t*>(pool.data) + prow * kFp4BlockRow;
+    *reinterpret_cast<uint2*>(dst + lane * 8) = make_uint2(c[0], c[1]);
+    dst[256 + lane] = bs;
+    if (lane == 0) pool.scale[prow] = s;
 }
 
 // Store one row (the warp's E values per lane) into a pool row: bf16, e4m3 + amax/448 scale, e2m1 + amax/6, or e2m1
@@ -93,29 +179,18 @@ __device__ __forceinline__ void load_bf16(const uint16_t* row, int lane, float (
 template <int E>
 __device__ __forceinline__ void store_row(const dsa_pool_t& pool, long long prow, int lane, const float (&v)[E]) {
     if (pool.dtype == DSA_BF16) {
-        uint16_t* dst = reinterpret_cast<uint16_t*>(pool.data) + prow * (E * 32) + lane * E;
         uint32_t u[E / 2];
 #pragma unroll
         for (int k = 0; k < E / 2; ++k)
             u[k] = (uint32_t)float_to_bf16(v[2 * k]) | ((uint32_t)float_to_bf16(v[2 * k + 1]) << 16);
-        if constexpr (E == 16) {
-            reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-            reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-        } else if constexpr (E == 4) {
-            *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[1]);
-        } else {
-            *reinterpret_cast<uint32_t*>(dst) = u[0];
-        }
+        store_words<E / 2>(reinterpret_cast<uint16_t*>(pool.data) + prow * (E * 32) + lane * E, u, false);
     } else if (pool.dtype == DSA_FP4_BLOCK) {
         if constexpr (E == kFp4Block) {  // a lane holds one block
             float inv_s, s;
             fp4_block_row_scale(warp_abs_max_bits(lane_abs_max_bits<E>(v)), &s, &inv_s);
             uint32_t c[2];
             const uint8_t bs = fp4_block_codes(v, __uint_as_float(lane_abs_max_bits<E>(v)), inv_s, c);
-            uint8_t* dst = reinterpret_cast<uint8_t*>(pool.data) + prow * kFp4BlockRow;
-            *reinterpret_cast<uint2*>(dst + lane * 8) = make_uint2(c[0], c[1]);
-            dst[256 + lane] = bs;
-            if (lane == 0) pool.scale[prow] = s;
+            store_fp4_block_row(pool, prow, lane, c, bs, s);
         }
     } else if (pool.dtype == DSA_FP4_E2M1) {  // e2m1 codes, two per byte, scale amax / 6
         float amax = 0.f;
