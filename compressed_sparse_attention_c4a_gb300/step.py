@@ -77,8 +77,8 @@ class LayerStep:
         # static share; off by default (measured slower on the decode batch: more query-group switches)
         self.dynamic_split = dynamic_split
         self.side = None
-        # fused_select: decode rows take the top-k and the attention in one call (one kernel when one cluster of
-        # four CTAs per row holds all 64 heads, rows of at most 16,384 scores and k <= 512); off by default: on
+        # fused_select: decode rows take the top-k and the attention in one call (one kernel over bf16 or e4m3 rows when one
+        # cluster of four CTAs per row holds all 64 heads, rows of at most 16,384 scores and k <= 512); off by default: on
         # the decode batch it measures level with the two launches (41.75 against 41.86 us a step; 38.1 against
         # 38.8 us with e2m1 indexer keys), its top-k phase running slower inside the attention kernel than the
         # top-k kernel alone
@@ -86,7 +86,7 @@ class LayerStep:
         self.select_attend_kernels = 2
         if self.fused_select:
             one = (tuple(self.attn_plan) == (64, 4, 1, 1) and spec.heads == 64 and self.ld <= 16384
-                   and spec.topk <= 512)
+                   and spec.topk <= 512 and spec.main_dtype != "fp4_block")
             self.select_attend_kernels = 1 if one else 1 + self.attn_plan[3]
 
     # ---- stages ------------------------------------------------------------------------

@@ -390,7 +390,7 @@ dsa_status_t dsa_sparse_attn_prefill(int32_t nq, int32_t heads, const void* q, c
  * scores     [batch][ld] fp32, 16-byte aligned, ld a multiple of 4;  n_visible [batch] int32
  * topk_out   [batch][k] int32 (required): the selected entry ids, exactly as dsa_topk writes them
  * Other arguments as dsa_sparse_attn_decode with topk = topk_out (workspace sized for max_keys = k + window).
- * One kernel when one cluster of four CTAs per row holds all heads without a key split (64 heads, at most
+ * One kernel over bf16 or e4m3 rows when one cluster of four CTAs per row holds all heads without a key split (64 heads, at most
  * 38 rows on a 152-SM GPU), ld <= 16,384 and k <= 512 (dsa_attn_plan(batch, heads, k + window) gives
  * (64, 4, 1, 1)); else the two calls in sequence.  Programmatic dependent launch as dsa_sparse_attn_decode:
  * scores and n_visible are read after the wait.  Errors: those of both calls.

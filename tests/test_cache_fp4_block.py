@@ -578,3 +578,286 @@ def test_a_row_of_nan_reaches_only_the_queries_that_read_it(rows):
     for j in hit:
         assert np.isnan(np64(out[j])).all() and np.isnan(np64(lse[j])).all(), j
     _check(out, lse, _expected(case, [j for j in range(rows) if j not in hit][:40]))
+
+
+@gpu
+@pytest.mark.parametrize("epb", [64, 256])
+def test_many_rows_at_16_byte_addresses(epb):
+    """Enough rows that a warp takes four, requests that begin and end inside such a group, empty ones between them; x and
+    out start 16 bytes past a 32-byte boundary."""
+    counts, first = [9001, 0, 0, 1, 37, 0, 700, 2, 0, 1259], [3, 0, 5, 64, 250, 1, 0, 63, 9, 77]
+    total = sum(counts)
+    bt, blocks = _paged(counts, first, epb, 5)
+    x = torch.empty(total * D + 8, dtype=torch.bfloat16, device="cuda")[8:].view(total, D)
+    x.copy_(_awkward_rows(total, 12))
+    assert x.data_ptr() % 32 == 16
+    cu, start = _schedule(counts, first)
+    gd = torch.full((blocks * epb, 288), 17, dtype=torch.uint8, device="cuda")
+    gs, status = torch.full((blocks * epb,), 5.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pool, table = dsa.pool(gd, epb, gs, fmt="fp4_block"), bt.cuda()
+    dsa.dsa_cache_write(cu.cuda(), start.cuda(), x, pool, dsa.block_table(table), dev_status=status)
+    req = np.repeat(np.arange(len(counts)), counts)
+    ids = np.concatenate([np.arange(n) + f for n, f in zip(counts, first)]).astype(int)
+    out = torch.empty((total + 1) * D + 8, dtype=torch.bfloat16, device="cuda")[8:].view(total + 1, D)
+    out.fill_(3.0)
+    order = np.random.default_rng(3).permutation(total)
+    dsa.dsa_cache_read(pool, dsa.block_table(table), torch.tensor(req[order], dtype=torch.int32, device="cuda"),
+                       torch.tensor(ids[order], dtype=torch.int32, device="cuda"), out, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    want, ws = codecs.fp4_block_quantize_rows(np64(x))
+    assert np.array_equal(np64(out)[:-1], codecs.fp4_block_dequantize_rows(want, ws)[order])
+    assert (np64(out)[-1] == 3.0).all()                                          # behind the n rows
+    rows = np.array([_physical(bt, r, i, epb) for r, i in zip(req, ids)])
+    rest = np.setdiff1d(np.arange(blocks * epb), rows)
+    assert (gd.cpu().numpy()[rest] == 17).all() and (np64(gs)[rest] == 5.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("name", ["ragged", "many_rows", "heads16"])
+def test_attention_through_the_other_entry_points(name):
+    """The call with the library's own scratch, and top-k and attention in one call: the same bits.  e4m3 output with an
+    amax / 448 scale per 128 dims: half an e4m3 step (2^-4 of the value, 2^-10 of the scale below its normal range) on top
+    of the attention's own error, which here has no bf16 rounding of the output."""
+    spec = ATTN[name]
+    case = _attn_case(spec, "random", seed=spec.seed)
+    nq, nvis = case["nq"], case["nvis"]
+    g = torch.Generator().manual_seed(2)
+    ld = (int(nvis.max()) + 3) // 4 * 4 + 4
+    scores = torch.randn((nq, ld), generator=g).cuda()
+    n_visible = torch.tensor(nvis, dtype=torch.int32, device="cuda")
+    topk = torch.full((nq, spec.topk), -7, dtype=torch.int32, device="cuda")
+    dsa.dsa_topk(scores, n_visible, spec.topk, topk)
+    case["topk"] = topk.cpu()
+    dev = _on_gpu(case)
+    out, lse, status, ws = _run(case, dev)
+    main, bt, swa, sbt = _pools(case, dev)
+    rope = dsa.rope(64)
+    o2, l2 = torch.full_like(out, 4.0), torch.full_like(lse, 4.0)
+    dsa.dsa_sparse_attn_decode_static(dev["q"], dev["q_pos"], spec.kind, topk, spec.topk, main, bt, swa, sbt, spec.window,
+                                      SM, rope, o2, l2, dev_status=status)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    o3, l3, t3 = torch.full_like(out, 4.0), torch.full_like(lse, 4.0), torch.full_like(topk, -7)
+    dsa.dsa_topk_sparse_attn_decode(dev["q"], dev["q_pos"], spec.kind, scores, n_visible, spec.topk, t3, main, bt, swa, sbt,
+                                    spec.window, SM, rope, o3, l3, workspace=ws, dev_status=status)
+    assert torch.equal(topk, t3) and torch.equal(out, o3) and torch.equal(lse, l3)
+    o8 = torch.zeros((nq, spec.heads, D), dtype=torch.uint8, device="cuda")
+    s8, l8 = torch.zeros((nq, spec.heads, 4), device="cuda"), torch.full_like(lse, 4.0)
+    dsa.dsa_sparse_attn_q8(dev["q"], dev["q_pos"], dev["q_req"], spec.kind, topk, spec.topk, main, bt, swa, sbt, spec.window,
+                           SM, rope, o8, s8, l8, workspace=ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and torch.equal(lse, l8)
+    sc = np.repeat(np64(s8), 128, axis=-1)
+    got = codecs.e4m3_decode(o8.cpu().numpy()) * sc
+    for j, (o, l, reach, eps) in _expected(case).items():
+        tol = (2 * U + 4 * eps[:, None] + 2.0 ** -16) * reach
+        tol = tol + np.maximum(2.0 ** -4 * (np.abs(o) + tol), 2.0 ** -10 * sc[j]) + 1e-30
+        assert np.all(np.abs(got[j] - o) <= tol), j
+
+
+@gpu
+@pytest.mark.parametrize("name", ["ragged", "prefill_many"])
+def test_rows_that_no_query_selects_are_never_used(name):
+    """Every row that is neither selected nor in a window, NaN scales and all: the same bits."""
+    spec = ATTN[name]
+    case = _attn_case(spec, "random", seed=spec.seed)
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    pos, req, tk, epb = np64(case["q_pos"]), np64(case["q_req"]), np64(case["topk"]).astype(int), case["epb"]
+    keep, keep_w = set(), set()
+    for j in range(case["nq"]):
+        r, m = int(req[j]), int(pos[j])
+        keep |= {_physical(case["bt_main"], r, i, epb) for i in tk[j] if i >= 0}
+        keep_w |= {_physical(case["bt_swa"], r, i, 256) for i in range(max(0, m - spec.window + 1), m + 1)}
+    for data, scale, kept in ((case["main_data"], case["main_scale"], keep), (case["swa_data"], case["swa_scale"], keep_w)):
+        drop = torch.tensor(np.setdiff1d(np.arange(data.shape[0]), sorted(kept)))
+        data[drop], scale[drop] = 0x7F, float("nan")
+    o2, l2, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == 0 and torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@gpu
+def test_the_same_entry_twice_counts_twice():
+    spec = ATTN["ragged"]
+    case = _attn_case(spec, "random", seed=spec.seed)
+    tk = case["topk"]
+    for j in range(case["nq"]):
+        got = tk[j][tk[j] >= 0]
+        if len(got):
+            tk[j] = got[torch.arange(spec.topk) % max(1, len(got) // 3)]
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    _check(out, lse, _expected(case))
+
+
+@gpu
+def test_offsets_beyond_32_bits():
+    """Blocks at the end of a pool of 4.8 GB: stored, read back and attended to; the bytes at the offsets' low 32 bits keep
+    their values."""
+    blocks, epb, n = 262144, 64, 200
+    data = torch.empty((blocks * epb, 288), dtype=torch.uint8, device="cuda")
+    scale = torch.empty((blocks * epb,), device="cuda")
+    far = [blocks - 1, blocks - 4, blocks - 2, blocks - 3]
+    assert far[1] * epb * 288 > 2 ** 32
+    low = [(b * epb * 288 % 2 ** 32) // 288 for b in far]
+    for row in low:
+        data[row:row + epb + 1], scale[row:row + epb + 1] = 23, 0.5
+    x = _awkward_rows(n, 9)
+    x[5::8] = x[4::8]                   # no row so tiny or large that it alone decides the softmax
+    x[6::8] = x[0::8]
+    x = (x.float() * 2.0 ** -6).to(torch.bfloat16)
+    bt = torch.tensor([far], dtype=torch.int32)
+    cu, start = _schedule([n], [0])
+    gbt = bt.cuda()
+    pool, table = dsa.pool(data, epb, scale, fmt="fp4_block"), dsa.block_table(gbt)
+    dsa.dsa_cache_write(cu.cuda(), start.cuda(), x.cuda(), pool, table)
+    ids = torch.arange(n, dtype=torch.int32, device="cuda")
+    out = torch.empty((n, D), dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_cache_read(pool, table, torch.zeros_like(ids), ids, out)
+    vals = codecs.fp4_block_dequantize_rows(*codecs.fp4_block_quantize_rows(np64(x)))
+    assert np.array_equal(np64(out), vals)
+    for row in low:
+        assert bool((data[row:row + epb + 1] == 23).all()) and bool((scale[row:row + epb + 1] == 0.5).all())
+    # the same rows in a small pool give the same attention
+    pos = torch.tensor([4 * n + 7], dtype=torch.int32, device="cuda")            # all n entries visible
+    q = _bf16(np.random.default_rng(1).standard_normal((1, 64, D))).cuda()
+    swa = torch.zeros((256 * 4, 288), dtype=torch.uint8, device="cuda")
+    ss = torch.ones(1024, device="cuda")
+    sbt = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    topk = torch.randperm(n, generator=torch.Generator().manual_seed(4))[:96].to(torch.int32).cuda().view(1, 96)
+    small = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    sd, sc = torch.empty((256, 288), dtype=torch.uint8, device="cuda"), torch.empty(256, device="cuda")
+    for i, b in enumerate(far):
+        sd[i * 64:i * 64 + 64], sc[i * 64:i * 64 + 64] = data[b * 64:b * 64 + 64], scale[b * 64:b * 64 + 64]
+    res = []
+    for p, t in ((pool, table), (dsa.pool(sd, epb, sc, fmt="fp4_block"), dsa.block_table(small))):
+        o, l = torch.zeros((1, 64, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 64), device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = torch.empty(max(16, dsa.dsa_attn_workspace_size(1, 64, 96 + 128)), dtype=torch.uint8, device="cuda")
+        dsa.dsa_sparse_attn_decode(q, pos, "c4a", topk, 96, p, t, dsa.pool(swa, 256, ss, fmt="fp4_block"),
+                                   dsa.block_table(sbt), 128, SM, dsa.rope(64), o, l, ws, dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        res.append((o, l))
+    assert np.isfinite(np64(res[0][0])).all() and np64(res[0][0]).any()
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+
+
+def _append_and_attend(case, dev, x, cu, start, out, lse, ws, status, stream=None):
+    """A decode step as served: the new window rows stored, then attention over both caches."""
+    spec = case["spec"]
+    main, bt, swa, sbt = _pools(case, dev)
+    dsa.dsa_cache_write(cu, start, x, swa, sbt, dev_status=status, stream=stream)
+    dsa.dsa_sparse_attn_decode(dev["q"], dev["q_pos"], spec.kind, dev["topk"], spec.topk, main, bt, swa, sbt, spec.window, SM,
+                               dsa.rope(64), out, lse, ws, dev_status=status, stream=stream)
+
+
+@gpu
+@pytest.mark.parametrize("name", ["heads16", "many_rows"])
+def test_append_and_attend_eager_on_a_stream_and_in_two_graphs(name):
+    """Rows stored and attended to in one go: against the 64-bit form over the stored rows; on another stream; and captured
+    twice with one workspace, the graphs replayed in turn over changed inputs: the same bits as eager calls."""
+    spec = ATTN[name]
+    case = _attn_case(spec, "random", seed=spec.seed)
+    nq = case["nq"]
+    dev = _on_gpu(case)
+    cu = torch.arange(nq + 1, dtype=torch.int32, device="cuda")
+    xs = [_bf16(np.random.default_rng(20 + i).standard_normal((nq, D))).cuda() for i in range(3)]
+    x = xs[0].clone()
+    ws = torch.empty(max(16, dsa.dsa_attn_workspace_size(nq, spec.heads, spec.topk + spec.window)), dtype=torch.uint8,
+                     device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def buffers():
+        return (torch.full((nq, spec.heads, D), 9.0, dtype=torch.bfloat16, device="cuda"),
+                torch.full((nq, spec.heads), 9.0, device="cuda"))
+
+    eager = []
+    for xi in xs:
+        x.copy_(xi)
+        o, l = buffers()
+        _append_and_attend(case, dev, x, cu, dev["q_pos"], o, l, ws, status)
+        torch.cuda.synchronize()
+        eager.append((o, l))
+    assert not torch.equal(eager[0][0], eager[1][0])
+    stored = dict(case, swa_data=dev["swa_data"].cpu(), swa_scale=dev["swa_scale"].cpu())
+    _check(*eager[2], _expected(stored, range(0, nq, max(1, nq // 12))))
+    # another stream
+    side = torch.cuda.Stream()
+    x.copy_(xs[0])
+    o, l = buffers()
+    side.wait_stream(torch.cuda.current_stream())
+    _append_and_attend(case, dev, x, cu, dev["q_pos"], o, l, ws, status, stream=side)
+    side.synchronize()
+    assert torch.equal(o, eager[0][0]) and torch.equal(l, eager[0][1])
+    # two graphs
+    graphs = []
+    for _ in range(2):
+        o, l = buffers()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _append_and_attend(case, dev, x, cu, dev["q_pos"], o, l, ws, status)
+        graphs.append((g, o, l))
+    for which, i in ((0, 1), (1, 2), (0, 0), (1, 1), (0, 2)):
+        x.copy_(xs[i])
+        g, o, l = graphs[which]
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager[i][0]) and torch.equal(l, eager[i][1]), (which, i)
+    assert int(status) == 0
+
+
+@gpu
+def test_two_calls_at_once():
+    """Calls on two streams with a workspace each, over one cache: each as if alone."""
+    cases = [_attn_case(ATTN[n], "random", seed=ATTN[n].seed) for n in ("heads16", "many_rows")]
+    devs = [_on_gpu(c) for c in cases]
+    alone = [_run(c, d)[:2] for c, d in zip(cases, devs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = []
+        for c, d, s in zip(cases, devs, streams):
+            with torch.cuda.stream(s):
+                got.append(_run(c, d, stream=s))
+        torch.cuda.synchronize()
+        for (o, l, status, _), (ao, al) in zip(got, alone):
+            assert int(status) == 0 and torch.equal(o, ao) and torch.equal(l, al)
+
+
+@gpu
+@pytest.mark.parametrize("kind,cached,new,queries", [("c4a", [2100, 39, 7], [1, 1, 1], "last"),
+                                                     ("c4a", [1000, 0], [37, 81], "all"),
+                                                     ("c128a", [5000, 126], [1, 1], "last")])
+def test_layer_step_over_block_caches(kind, cached, new, queries):
+    """Compress, index, select and attend as one layer step with both caches in 4 bits: the attention against the 64-bit form
+    over the rows that the step stored and the entries that it selected; fused calls and a second stream give the same bits."""
+    from compressed_sparse_attention_c4a_gb300.step import LayerStep
+    spec = synth.CaseSpec("step", kind=kind, cached=cached, new=new, queries=queries, idx_heads=16 if kind == "c4a" else 0,
+                          topk=64 if kind == "c4a" else 0, main_dtype="fp4_block", swa_dtype="fp4_block", seed=71)
+    runs = []
+    for opts in ({}, {"fused_select": True}, {"two_streams": True}):
+        case = synth.make_case(spec, "cpu")
+        dev = _on_gpu(case)
+        step = LayerStep(dev, **opts)
+        step.run()
+        torch.cuda.synchronize()
+        assert int(step.status) == 0
+        runs.append((step, dev, case))
+    step, dev, case = runs[0]
+    w, s = synth.WINDOW[kind]
+    pos = np64(case["q_pos"])
+    case["nvis"] = np.where(pos + 1 < w, 0, (pos + 1 - w) // s + 1)
+    for k in ("main_data", "main_scale", "swa_data", "swa_scale"):
+        case[k] = dev[k].cpu()
+    if kind == "c4a":
+        case["topk"] = step.topk.cpu()
+        for j in range(case["nq"]):
+            picked = case["topk"][j][case["topk"][j] >= 0]
+            assert len(set(picked.tolist())) == len(picked) == min(int(case["nvis"][j]), 64)
+    _check(step.out, step.lse, _expected(case))
+    for other, d, _ in runs[1:]:
+        assert torch.equal(other.out, step.out) and torch.equal(other.lse, step.lse)
+        assert torch.equal(d["main_data"], dev["main_data"]) and torch.equal(d["swa_data"], dev["swa_data"])
