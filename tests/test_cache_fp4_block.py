@@ -861,3 +861,17 @@ def test_layer_step_over_block_caches(kind, cached, new, queries):
     for other, d, _ in runs[1:]:
         assert torch.equal(other.out, step.out) and torch.equal(other.lse, step.lse)
         assert torch.equal(d["main_data"], dev["main_data"]) and torch.equal(d["swa_data"], dev["swa_data"])
+
+
+@gpu
+@pytest.mark.parametrize("heads,topk,window", [(64, 1, 1), (64, 3, 2), (128, 40, 30), (16, 2, 60)])
+def test_many_rows_of_one_or_two_tiles(heads, topk, window):
+    """Rows so short that a CTA's next rows are resolved, multiplied and normalised while the first is still being stored: every
+    row, its log-sum-exp and its own position's rotation."""
+    spec = S("tiny", cached=[0] * 3, new=[700, 500, 311], queries="all", heads=heads, topk=topk, window=window,
+             seed=90 + heads + topk, **F)
+    case = _attn_case(spec, "random", seed=heads + topk)
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    _check(out, lse, _expected(case))
