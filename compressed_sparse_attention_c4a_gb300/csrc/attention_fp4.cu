@@ -59,7 +59,8 @@ constexpr int kFp4Groups = kFp4Keys / 8;               // groups of 8 keys (the 
 constexpr uint64_t kFp4AllValid = (1ull << kFp4Keys) - 1;
 constexpr uint64_t kFp4Fault = 1ull << 63;             // mask bit: a key of the tile hit a device fault
 // what an entry says of its tile
-constexpr int kFirst = 1, kLast = 2, kFinal = 4, kOdd = 8;  // of its row; of the stream; the row's ordinal is odd
+constexpr int kFirst = 1, kLast = 2, kFinal = 4;  // of its row; of the stream
+constexpr int kOdd = 8, kOdd2 = 16;               // the two lowest bits of the row's ordinal
 // Widened values carry 2^-8: e2m1 bits placed in a bf16 are 2^-126 of the value, and the factor that undoes it times a
 // block scale of up to 448 must stay below 2^128, so it is 2^118.
 constexpr int kFp4Shift = 8;
@@ -99,7 +100,7 @@ struct Fp4Smem {
     static constexpr int kOffRow = kOffInv + 2 * NH * 4;            // int [2][4]: its unit, -, position, fault
     static constexpr int kOffFault = kOffRow + 32;                  // int: a key of this CTA hit a device fault
     static constexpr int kOffRope = kOffFault + 16;                 // float [32][2]: cos, sin of each pair's angle at m
-    static constexpr int kBars = 2 * kFp4Ring + 3 * kFp4Entries + 12;
+    static constexpr int kBars = 2 * kFp4Ring + 3 * kFp4Entries + 13;
     static constexpr int kOffBar = kOffRope + 256;                  // kBars mbarriers, TMEM address
     static constexpr int kOffXfull = kOffBar + (kBars - 4) * 8;     // three of the last four: received tile slots
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
@@ -350,8 +351,10 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
     uint64_t* kfree = kfull + kFp4Entries;                              // [6] entry read (softmax warps, next S warp)
     uint64_t* sfull = kfree + kFp4Entries;                              // [2] S in TMEM
     uint64_t* pfull = sfull + 2;                                        // [2] P^T written (4 softmax warps)
-    uint64_t* qfull = pfull + 2;                                        // query rows loaded
-    uint64_t* rdone = qfull + 1;                                        // O^T rescaled (4 softmax warps)
+    // [2] query rows loaded, by the parity of the row's ordinal: an S warp sees every second tile only, and with one barrier
+    // it could wait for row r + 1 by parity before row r's load is complete
+    uint64_t* qfull = pfull + 2;
+    uint64_t* rdone = qfull + 2;                                        // O^T rescaled (4 softmax warps)
     uint64_t* ostat = rdone + 1;                                        // a row's factors written (4 softmax warps)
     uint64_t* ofree = ostat + 1;                                        // its O^T read (widening warps)
     uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + L::kOffXfull);  // [3] each received tile slot loaded
@@ -383,7 +386,8 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
             mbar_init(&sfull[b], 1);
             mbar_init(&pfull[b], 4);
         }
-        mbar_init(qfull, 1);
+        mbar_init(&qfull[0], 1);
+        mbar_init(&qfull[1], 1);
         mbar_init(rdone, 4);
         mbar_init(ostat, 4);
         mbar_init(ofree, 8);
@@ -427,16 +431,17 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         u.tiles = u.end > u.first ? (u.end - u.first + csize - 1) / csize : 1;
         return u;
     };
-    auto load_q = [&](int unit) {  // by one warp: one 64-dim box per lane
+    auto load_q = [&](int unit, int odd) {  // by one warp: one 64-dim box per lane
         const int row = row_of(unit);
-        if (lane == 0) mbar_expect_tx(qfull, NH * kD * 2);
+        if (lane == 0) mbar_expect_tx(&qfull[odd], NH * kD * 2);
         __syncwarp();
         if (lane < kD / 64)
-            tma_load_2d(smem + L::kOffQ + lane * 8192, &qmap, lane * 64, row * a.heads + (unit - row * a.hg_count) * NH, qfull);
+            tma_load_2d(smem + L::kOffQ + lane * 8192, &qmap, lane * 64, row * a.heads + (unit - row * a.hg_count) * NH,
+                        &qfull[odd]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(qfull);
+        if (lane == 0) mbar_arrive(&qfull[odd]);
     };
-    if (warp == 4) load_q(unit0);
+    if (warp == 4) load_q(unit0, 0);
     int r0 = 0, m0 = 0;
     if (warp == 7 || warp == 3) {
         r0 = a.q_req ? a.q_req[row_of(unit0)] : row_of(unit0);
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                                                     : (uint64_t)(valid[1] >> 16) | (uint64_t)valid[2] << 16;
                     s_mask[at] = mask | (bad ? kFp4Fault : 0ull);
                     const bool last = t + 1 == u.tiles;
-                    s_info[4 * at] = (t == 0 ? kFirst : 0) | (last ? kLast : 0) | (ord & 1 ? kOdd : 0) |
+                    s_info[4 * at] = (t == 0 ? kFirst : 0) | (last ? kLast : 0) | (ord & 3) * kOdd |
                                      (last && unit + unit_step >= units ? kFinal : 0);
                     s_info[4 * at + 1] = unit;
                     s_info[4 * at + 2] = u.m;
@@ -741,7 +746,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                 ok = ok && wait_bar(&full[slot], (n / kFp4Ring) & 1);
                 if (h == 0) {
                     info = s_info[4 * (g % kFp4Entries)];
-                    ok = ok && wait_bar(qfull, info & kOdd ? 1 : 0);  // the row's queries
+                    ok = ok && wait_bar(&qfull[info & kOdd ? 1 : 0], info & kOdd2 ? 1 : 0);  // the row's queries
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -773,7 +778,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                     if (g > 0) ok = ok && wait_bar(&sfull[b ^ 1], ((g - 1) >> 1) & 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    load_q(unit + unit_step);
+                    load_q(unit + unit_step, info & kOdd ? 0 : 1);
                 }
             }
         }
