@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
 
     // Position, request, block tables and query rows: inputs that no kernel of the layer step writes, read while the
     // preceding kernel finishes.  Top-k indices, cache rows and every output come after the wait.
-    auto row_of = [&](int unit) { return unit / a.hg_count; };
+    auto row_of = [&](int unit) { return unit >> (a.hg_count - 1); };  // one head group a row, or two
     auto make_unit = [&](int unit, int r, int m) {
         Unit u;
         u.row = row_of(unit);
@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         u.r = r;
         u.m = m;
         u.ok = r >= 0 && r < a.main_bt.batch && r < a.swa_bt.batch && m >= 0;
-        u.n_vis = u.ok ? entries_formed((long long)m + 1, a.kind_w, a.kind_s) : 0;
+        const uint32_t tokens = (uint32_t)m + 1u;  // entries_formed() by a shift: the stride is a power of two
+        u.n_vis = u.ok && tokens >= (uint32_t)a.kind_w ? (int)((tokens - a.kind_w) >> (__ffs(a.kind_s) - 1)) + 1 : 0;
         u.n_comp = a.topk ? a.k : u.n_vis;
         u.wlo = max(0, m - a.window + 1);
         u.n_keys = u.ok ? u.n_comp + (m - u.wlo + 1) : 0;
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         u.first = (ROWS ? 0 : split * a.cps) + crank;
         u.step = csize;
         u.end = ROWS ? n_tiles : min(n_tiles, (split + 1) * a.cps);
-        u.tiles = u.end > u.first ? (u.end - u.first + csize - 1) / csize : 1;
+        u.tiles = u.end > u.first ? (u.end - u.first + csize - 1) >> (__ffs(csize) - 1) : 1;
         return u;
     };
     auto load_q = [&](int unit, int odd) {  // by one warp: one 64-dim box per lane
@@ -465,6 +466,14 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         const int main_shift = __ffs(a.main.rows_per_block) - 1;  // 64 or 2 rows a block; the window's 256
         int g = 0;
         for (int unit = unit0, ord = 0; unit < units && ok; unit += unit_step, ++ord) {
+            const int32_t* const row_topk = a.topk + (long long)row_of(unit) * a.k;
+            int entry[3];  // top-k indices of the next two tiles' keys (-1: none); the first ones before the position is here
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                const int kk = lane + 32 * e, t = (ROWS ? 0 : split * a.cps) + crank + (kk < kFp4Keys ? 0 : csize);
+                const int j = t * kFp4Keys + kk % kFp4Keys;
+                entry[e] = load_int_if(row_topk + j, a.topk && j < a.k);
+            }
             const Unit u = make_unit(unit, r0, m0);
             if (unit + unit_step < units) {  // the next unit's, in flight meanwhile
                 const int next = row_of(unit + unit_step);
@@ -472,18 +481,11 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                 m0 = load_int_if(a.q_pos + next, true);
             }
             if (!u.ok && lane == 0 && crank == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
-            const int32_t* const row_topk = a.topk + (long long)u.row * a.k;
             auto key_index = [&](int i, int e) -> int {  // of the row, -1: none
                 const int kk = lane + 32 * e, t = i + kk / kFp4Keys;
                 const int tile = u.first + u.step * t, j = tile * kFp4Keys + kk % kFp4Keys;
                 return tile < u.end && j < u.n_keys ? j : -1;
             };
-            int entry[3];  // top-k indices of the next two tiles' keys (-1: none)
-#pragma unroll
-            for (int e = 0; e < 3; ++e) {
-                const int j = key_index(0, e);
-                entry[e] = load_int_if(row_topk + max(j, 0), a.topk && j >= 0 && j < u.n_comp);
-            }
             for (int i = 0; i < u.tiles && ok; i += 2) {
                 const bool two = i + 1 < u.tiles;
                 if (g >= kFp4Entries) ok = entry_wait(kfree, g - kFp4Entries);
