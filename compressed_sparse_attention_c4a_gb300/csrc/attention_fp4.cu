@@ -259,19 +259,16 @@ __device__ __noinline__ void rescale_quadrant(uint32_t taddr, const float* alpha
     tmem_wait_st();
 }
 
-// A finished row's output, by the first eight widening warps (ww): O^T from TMEM, times the row's factor per head, rotated by
-// R_m^-1, to global memory.  Warp quadrant = 32 dims of each 128-dim tile, lane = dim, half of the heads.  Neighbouring
-// lanes (a pair of dims) exchange one value per pair of heads: the even lane then holds both dims of the first head, the
-// odd lane those of the second, and stores them as one word: half a 128-byte line per head and quadrant.
+// A finished row's output, by the first eight widening warps (ww): O^T from TMEM, times the row's factor per head, rotated
+// by R_m^-1, to global memory.  Warp quadrant = 32 dims of each 128-dim tile, lane = dim, half of the heads; a store of a
+// warp is 64 bytes of one head's row.  (Neighbouring lanes exchanging values to store words of two dims: 361 us for the
+// prefill below, 355 so.)
 template <int NH>
 __device__ __noinline__ void store_row(const RopeTable& rope, uint16_t* out_row, uint32_t taddr, const float* inv, int ww,
                                        int m, bool fault) {
     constexpr int kHeads = NH / 2, kStep = kHeads < 16 ? kHeads : 16, kSteps = kHeads / kStep;
     const int lane = threadIdx.x & 31, quad = ww & 3, hbase = (ww >> 2) * kHeads;
-    const bool odd = lane & 1;
-    const uint32_t pick = odd ? 0x3276u : 0x5410u;
     const int first_rot = kD - rope.rope_dim;
-    uint16_t* const out = out_row + (hbase + (odd ? 1 : 0)) * kD + quad * 32 + (lane & ~1);
     taddr += ((uint32_t)(quad * 32) << 16) + hbase;
     inv += hbase;
     float v[kStep];
@@ -293,25 +290,26 @@ __device__ __noinline__ void store_row(const RopeTable& rope, uint16_t* out_row,
 #pragma unroll
             for (int e = 0; e < kStep; ++e) x[e] = 0.f;
         }
-        uint32_t* const to = reinterpret_cast<uint32_t*>(out + h0 * kD + tt * 128);
-        uint32_t w[kStep / 2];
+        uint16_t* const to = out_row + (hbase + h0) * kD + tt * 128 + quad * 32 + lane;
         if (!__any_sync(0xffffffffu, dim >= first_rot)) {
 #pragma unroll
-            for (int e = 0; e < kStep / 2; ++e) w[e] = bf16x2_rn(x[2 * e], x[2 * e + 1]);
-#pragma unroll
-            for (int e = 0; e < kStep / 2; ++e) w[e] = __byte_perm(w[e], __shfl_xor_sync(0xffffffffu, w[e], 1), pick);
+            for (int e = 0; e < kStep; e += 2) {
+                const uint32_t w = bf16x2_rn(x[e], x[e + 1]);
+                to[e * kD] = (uint16_t)w;
+                to[(e + 1) * kD] = (uint16_t)(w >> 16);
+            }
         } else {
             float cs = 1.f, sn = 0.f;
             if (dim >= first_rot && !fault) rope_cos_sin(m, rope, (dim - first_rot) >> 1, &cs, &sn);
+            if (lane & 1) sn = -sn;
 #pragma unroll
-            for (int e = 0; e < kStep / 2; ++e) {
-                const float recv = __shfl_xor_sync(0xffffffffu, odd ? x[2 * e] : x[2 * e + 1], 1);
-                const float lo = odd ? recv : x[2 * e], hi = odd ? x[2 * e + 1] : recv;
-                w[e] = bf16x2_rn(lo * cs + hi * sn, hi * cs - lo * sn);
+            for (int e = 0; e < kStep; e += 2) {
+                const float y0 = __shfl_xor_sync(0xffffffffu, x[e], 1), y1 = __shfl_xor_sync(0xffffffffu, x[e + 1], 1);
+                const uint32_t w = bf16x2_rn(x[e] * cs + y0 * sn, x[e + 1] * cs + y1 * sn);
+                to[e * kD] = (uint16_t)w;
+                to[(e + 1) * kD] = (uint16_t)(w >> 16);
             }
         }
-#pragma unroll
-        for (int e = 0; e < kStep / 2; ++e) to[e * kD] = w[e];
     }
 }
 
