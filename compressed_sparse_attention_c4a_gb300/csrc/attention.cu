@@ -783,18 +783,18 @@ __global__ void __launch_bounds__(kClThreads, 1)
 }
 
 // Split plans, shared by the workspace query and the launch: one cluster of `cl` CTAs per (row, head group, split)
-// over sub-tiles of 32 keys (4-bit rows: tiles of 48): clusters of 4
+// over sub-tiles of 32 keys: clusters of 4
 // while four CTAs per row still fit on the GPU at once, then 2, then 1; a row splits further only when
 // its clusters leave SMs idle, and never below two sub-tiles per CTA.
 struct SplitPlan {
     int hg, hg_count, nsplit, cps, cl;
 };
 
-static SplitPlan plan_cluster(int rows, int heads, int max_keys, int tile_keys) {
+static SplitPlan plan_cluster(int rows, int heads, int max_keys) {
     SplitPlan p;
     p.hg = heads >= 64 ? 64 : heads;
     p.hg_count = heads / p.hg;
-    const int n_sub = max(1, (max_keys + tile_keys - 1) / tile_keys);
+    const int n_sub = max(1, (max_keys + kClKeys - 1) / kClKeys);
     const long long units = (long long)rows * p.hg_count;
     const long long sms = sm_count();
     int cl = units * 4 <= sms ? 4 : (units * 2 <= sms ? 2 : 1);
@@ -807,8 +807,38 @@ static SplitPlan plan_cluster(int rows, int heads, int max_keys, int tile_keys) 
     return p;
 }
 
+// 4-bit rows: clusters of 4 while one for each row and head group fits on the GPU at once, then of 2, then single CTAs (which
+// run on from row to row).  fp4_clusters() counts what fits: a cluster needs its SMs in one group of SMs, so there are 36
+// clusters of 4 on 152 SMs, and rows 37 and 38 would wait for the others (640 keys: 30 us; with clusters of 2, 22).  Splits:
+// the fewest of least cost, in units of a tile's time (3,000 cycles): the tiles a CTA takes one after another, one for
+// joining the parts in a second kernel, and a tenth of one for every part of 64 heads that is written and read there.
+// Measured, splits chosen against none (640 keys of 64 heads): 1 row 4 splits 13.0 us against 14.3, 4 rows 4 splits 13.2
+// against 14.9, 8 rows 2 splits 14.8 against 16.2, 12 rows none 15.8 against 16.3 with two; 1152 keys: 1 row 6 splits 13.6
+// against 18.6, 8 rows 3 splits 16.2 against 19.0.
+static SplitPlan plan_fp4(int rows, int heads, int max_keys) {
+    SplitPlan p;
+    p.hg = heads >= 64 ? 64 : heads;
+    p.hg_count = heads / p.hg;
+    const int n_tiles = max(1, (max_keys + kFp4Keys - 1) / kFp4Keys);
+    const long long units = (long long)rows * p.hg_count;
+    int cl = units <= fp4_clusters(4) ? 4 : (units <= fp4_clusters(2) ? 2 : 1);
+    while (cl > 1 && cl > n_tiles) cl >>= 1;
+    const int per = (n_tiles + cl - 1) / cl;  // tiles of a CTA without a split
+    const int most = (int)std::min<long long>(per, fp4_clusters(cl) / units);
+    int ns = 1;
+    long long least = 10ll * per + units * p.hg / 64;
+    for (int n = 2; n <= most; ++n) {
+        const long long cost = 10ll * ((per + n - 1) / n) + 10 + units * n * p.hg / 64;
+        if (cost < least) ns = n, least = cost;
+    }
+    p.cl = cl;
+    p.cps = (n_tiles + ns - 1) / ns;
+    p.nsplit = (n_tiles + p.cps - 1) / p.cps;
+    return p;
+}
+
 static SplitPlan plan_for(int rows, int heads, int max_keys, int dtype) {
-    return plan_cluster(rows, heads, max_keys, dtype == DSA_FP4_BLOCK ? kFp4Keys : kClKeys);
+    return dtype == DSA_FP4_BLOCK ? plan_fp4(rows, heads, max_keys) : plan_cluster(rows, heads, max_keys);
 }
 
 // Workspace: split partials [rows][nsplit][heads][512] + (m, l) [rows][nsplit][heads][2] when a row's keys

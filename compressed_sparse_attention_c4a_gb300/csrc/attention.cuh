@@ -410,6 +410,8 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
 
 // The kernel over DSA_FP4_BLOCK rows (attention_fp4.cu) for a plan of cl CTAs per cluster, heads per CTA hg.
 dsa_status_t launch_attn_fp4(const AttnArgs& a, int hg, int cl, cudaStream_t st);
+// Clusters of cl (1, 2 or 4) of its CTAs that the current device holds at once.
+int fp4_clusters(int cl);
 // Tensor maps of the query rows and of the output (attention.cu).
 bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, int box_rows);
 bool make_out_map(CUtensorMap* map, void* base, uint64_t rows, int box_rows, bool e4m3);

@@ -1022,6 +1022,34 @@ static dsa_status_t launch(AttnArgs a, int cl, cudaStream_t st) {
     return launch_status();
 }
 
+int fp4_clusters(int cl) {
+    int dev = 0;
+    if (cl == 1 || cudaGetDevice(&dev) != cudaSuccess) return sm_count() / cl;
+    static std::atomic<int> known[16][2];  // by device and cluster size; 0: not asked yet
+    std::atomic<int>* const seen = dev < 16 ? &known[dev][cl == 4] : nullptr;
+    if (seen && seen->load(std::memory_order_relaxed) > 0) return seen->load(std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(sm_count() / cl * cl));
+    cfg.blockDim = dim3(kFp4Threads<false>);
+    cfg.dynamicSmemBytes = Fp4Smem<64>::kAlloc;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(attn_fp4_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fp4Smem<64>::kAlloc) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, attn_fp4_kernel<64, false>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return sm_count() / cl;
+    }
+    if (seen) seen->store(n, std::memory_order_relaxed);
+    return n;
+}
+
 dsa_status_t launch_attn_fp4(const AttnArgs& a, int hg, int cl, cudaStream_t st) {
     switch (hg) {
         case 16: return launch<16>(a, cl, st);

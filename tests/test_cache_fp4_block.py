@@ -449,6 +449,8 @@ ATTN = {
     "one_entry": S("one_entry", cached=[700] * 3, new=[1] * 3, topk=1, window=1, seed=55, **F),
     "wide_window": S("wide_window", cached=[5000, 600], new=[1, 1], topk=64, window=1024, seed=56, **F),
     "many_rows": S("many_rows", cached=[300 + 7 * i for i in range(90)], new=[1] * 90, topk=63, heads=64, seed=57, **F),
+    "pairs": S("pairs", cached=[200 + 31 * i for i in range(40)], new=[1] * 40, topk=250, heads=64, seed=63, **F),
+    "many_splits": S("many_splits", cached=[4999, 4200], new=[1, 1], topk=1024, seed=64, **F),
     "dense": S("dense", kind="c128a", cached=[60000, 1279, 126, 127, 0], new=[1] * 5, idx_heads=0, topk=0, seed=58, **F),
     "dense_c4a": S("dense_c4a", kind="c4a", cached=[3001, 5], new=[1] * 2, topk=0, heads=16, seed=59, **F),
     "prefill": S("prefill", cached=[1037, 0], new=[130, 70], queries="all", topk=100, seed=60, **F),
