@@ -25,11 +25,12 @@ namespace dsa {
 // The tiles of a CTA form one stream, described by a ring of six entries: the keys' addresses, scales and mask, and whether
 // the tile is the first or last of its row or the last of all.
 //   warp 7      resolves: two tiles at a time, three keys a lane (top-k index -> block table -> row address, row scale);
-//   warps 8 on  widen: twelve warps own 4 keys of every tile (in the cluster kernel eight own 6).  The rows' bytes are copied into shared memory with cp.async, each
-//               half of the warp's share again as soon as it is converted, so a tile's copies have a whole tile's time;
-//               the codes become bf16 and are stored 128B-swizzled as [64-dim chunk][48 keys][128 B], the first 256 dims,
-//               then the others.  Many rows: between two half-tiles, when a row's last product is done, the first eight of
-//               these warps read its O^T from TMEM, rotate and store it;
+//   warps 8 on  widen: twelve warps own 4 keys of every tile (in the cluster kernel eight own 6).  The rows' bytes are copied
+//               into shared memory with cp.async, each half of the warp's share again as soon as it is converted, so a
+//               tile's copies have a whole tile's time; the codes become bf16 and are stored 128B-swizzled as
+//               [64-dim chunk][48 keys][128 B], the first 256 dims, then the others.  Many rows: between two half-tiles,
+//               when a row's last product is done, the first eight of these warps read its O^T from TMEM, rotate and
+//               store it;
 //   warps 4, 6  S = Q K^T (M = 64 heads, N = 48 keys) of even and odd tiles;
 //   warp 5      O^T += V^T P^T (four tiles of M = 128 dims, N = NH heads, K = 48 keys);
 //   warps 0-3   softmax: 16 heads a warp, a head's 48 logits over the 4 lanes of a quad (the 16-lane TMEM load spreads a
@@ -37,7 +38,7 @@ namespace dsa {
 // The widened keys are a ring of five half-tiles (48 keys x 256 dims): S starts on the first half, P V frees it first.  Two
 // S and two P buffers.
 //
-// What bounds it (2048 rows of 640 keys, 64 heads: 363 us, a tile in about 3,000 cycles): shared memory is busy for 2,070
+// What bounds it (2048 rows of 640 keys, 64 heads: 355 us, a tile in about 3,000 cycles): shared memory is busy for 2,070
 // of them (reads of S 896 and of P V 576, widened stores 384, P^T 48, the rows' copies and loads 216), the schedulers
 // issue in 61 % of theirs, the tensor cores work in 33 %; and a row's O^T is read out while its successor's products
 // wait, about 5,000 cycles a row.  What else was measured on the way, in us: one CTA a row 463; rows loaded straight into
@@ -45,7 +46,10 @@ namespace dsa {
 // loads wait for lines when they are issued); loops unrolled and waits inline 578 (the roles share the instruction caches);
 // matrix instructions with descriptors computed in ordinary registers 390 (77 cycles to issue one, 35 with uniform ones);
 // the rows fetched by a warp of its own, with bulk copies 509 (100 cycles a row), with cp.async 397; tiles of 32 keys 416;
-// a tile widened in one step instead of two 422; eight widening warps 367; all twelve storing a finished row 384.
+// a tile widened in one step instead of two 422; eight widening warps 367; all twelve storing a finished row 384 (this
+// kernel then spills); a finished row stored as soon as its product is done, at any half-tile, 375.
+// A decode row's 17 us (32 rows of 640 keys, clusters of 4): 2.2 until the first keys are widened (position, block table,
+// rows, one load after the other), 6 for four tiles, 3 for the last tile's chain, 6 for the merge across the cluster.
 constexpr int kFp4Ring = 5;                            // widened half-tiles
 constexpr int kFp4Half = kFp4Keys * (kD / 2) * 2;
 constexpr int kFp4Chunk = kFp4Keys * 128;              // bytes of a 64-dim chunk

@@ -11,9 +11,14 @@ namespace dsa {
 
 constexpr int kRowThreads = 256;  // 8 warps, a row each, or four in turn
 
+// What bounds both: HBM from about 30,000 rows on (1,316 or 1,324 bytes a row: 131,072 rows stored in 35.8 us, 4.8 TB/s, and
+// read in 35.5; 65,536 rows in 14.3 and 15.5), below that the chain of loads from the schedule to the row.  Storing takes
+// 200 instructions a row for a warp, reading 100.
+//
 // Rows per warp: four consecutive ones, whose addresses four lanes find side by side and whose loads are in flight
-// together, when there are enough rows for two blocks of such warps on every SM.  Measured, four against one: 131,072 rows
-// stored 38 against 47 us, 16,384 scattered rows read 5.0 against 5.6; 5,000 rows stored and read 6.6 against 5.9.
+// together, when there are enough rows for two blocks of such warps on every SM.  Measured, four against one, stored and
+// read: 131,072 rows 35.8 and 35.5 us against 38.0 and 44.3, 65,536 rows 14.3 and 15.5 against 18.4 and 18.6, 16,384 rows
+// 5.1 and 5.0 against 5.3 and 5.4; 8,192 rows level, 5,000 rows 2.9 and 3.6 against 2.5 and 3.4.
 static int rows_per_warp(long long n) { return n >= 2ll * 4 * 8 * sm_count() ? 4 : 1; }
 
 struct CacheWriteArgs {
