@@ -24,7 +24,9 @@ namespace dsa {
 //
 // The tiles of a CTA form one stream, described by a ring of six entries: the keys' addresses, scales and mask, and whether
 // the tile is the first or last of its row or the last of all.
-//   warp 7      resolves: two tiles at a time, three keys a lane (top-k index -> block table -> row address, row scale);
+//   warp 7      resolves: two tiles at a time, three keys a lane (top-k index -> block table -> row address, row scale); a
+//               tile without a key (the padding of a short top-k row) is left out: 1153 prefill rows of up to 333 entries,
+//               16 heads, 130 us with those tiles, 91 without;
 //   warps 8 on  widen: twelve warps own 4 keys of every tile (in the cluster kernel eight own 6).  The rows' bytes are copied
 //               into shared memory with cp.async, each half of the warp's share again as soon as it is converted, so a
 //               tile's copies have a whole tile's time; the codes become bf16 and are stored 128B-swizzled as
@@ -488,6 +490,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                 const int tile = u.first + u.step * t, j = tile * kFp4Keys + kk % kFp4Keys;
                 return tile < u.end && j < u.n_keys ? j : -1;
             };
+            bool first = true;
             for (int i = 0; i < u.tiles && ok; i += 2) {
                 const bool two = i + 1 < u.tiles;
                 if (g >= kFp4Entries) ok = entry_wait(kfree, g - kFp4Entries);
@@ -495,6 +498,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 int j[3], id[3], block[3], row[3];
+                uint64_t addr[3];
                 uint32_t valid[3], bad = !u.ok;
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
@@ -523,38 +527,45 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                     }
                     scale[e] = load_float_if(pool.scale + max(row[e], 0), row[e] >= 0);
                     valid[e] = __ballot_sync(0xffffffffu, row[e] >= 0);
-                    const int kk = lane + 32 * e, entry_at = (g + kk / kFp4Keys) % kFp4Entries;
-                    if (two || kk < kFp4Keys)
-                        s_addr[entry_at * kFp4Keys + kk % kFp4Keys] =
-                            row[e] < 0 ? 0ull : reinterpret_cast<uint64_t>(pool.data) + (uint64_t)row[e] * kFp4BlockRow;
+                    addr[e] = row[e] < 0 ? 0ull : reinterpret_cast<uint64_t>(pool.data) + (uint64_t)row[e] * kFp4BlockRow;
                 }
                 bad = __any_sync(0xffffffffu, bad != 0);
                 if (bad && u.ok && lane == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
-                if (lane < 2 && (lane == 0 || two)) {
-                    const int t = i + lane, at = (g + lane) % kFp4Entries;
-                    const uint64_t mask = lane == 0 ? (uint64_t)valid[0] | (uint64_t)(valid[1] & 0xffffu) << 32
-                                                    : (uint64_t)(valid[1] >> 16) | (uint64_t)valid[2] << 16;
-                    s_mask[at] = mask | (bad ? kFp4Fault : 0ull);
-                    const bool last = t + 1 == u.tiles;
-                    s_info[4 * at] = (t == 0 ? kFirst : 0) | (last ? kLast : 0) | (ord & 3) * kOdd |
-                                     (last && unit + unit_step >= units ? kFinal : 0);
-                    s_info[4 * at + 1] = unit;
-                    s_info[4 * at + 2] = u.m;
+                // a tile without a key is left out (the padding of a short top-k row), unless it is the last
+                const uint64_t mask0 = (uint64_t)valid[0] | (uint64_t)(valid[1] & 0xffffu) << 32;
+                const uint64_t mask1 = (uint64_t)(valid[1] >> 16) | (uint64_t)valid[2] << 16;
+                const bool put0 = mask0 || bad || i + 1 == u.tiles, put1 = two && (mask1 || bad || i + 2 == u.tiles);
+                const int at0 = g % kFp4Entries, at1 = (g + (put0 ? 1 : 0)) % kFp4Entries;
+                const bool mine = lane == 0 ? put0 : lane == 1 && put1;  // lanes 0 and 1 write a tile's entry
+                const int my_at = lane == 0 ? at0 : at1;
+                if (mine) {
+                    s_mask[my_at] = (lane == 0 ? mask0 : mask1) | (bad ? kFp4Fault : 0ull);
+                    const bool last = i + lane + 1 == u.tiles;
+                    s_info[4 * my_at] = (first && (lane == 0 || !put0) ? kFirst : 0) | (last ? kLast : 0) | (ord & 3) * kOdd |
+                                        (last && unit + unit_step >= units ? kFinal : 0);
+                    s_info[4 * my_at + 1] = unit;
+                    s_info[4 * my_at + 2] = u.m;
                 }
-                __syncwarp();
-                if (lane < 2 && (lane == 0 || two)) mbar_arrive(&rfull[(g + lane) % kFp4Entries]);
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
-                    const int kk = lane + 32 * e, at = (g + kk / kFp4Keys) % kFp4Entries, key = kk % kFp4Keys;
-                    if (two || kk < kFp4Keys) {
-                        float* k = s_ksc + at * 2 * kFp4Keys + key / 2 * 4 + (key & 1);
+                    const int kk = lane + 32 * e;
+                    if (kk < kFp4Keys ? put0 : put1) s_addr[(kk < kFp4Keys ? at0 : at1) * kFp4Keys + kk % kFp4Keys] = addr[e];
+                }
+                __syncwarp();
+                if (mine) mbar_arrive(&rfull[my_at]);
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const int kk = lane + 32 * e, key = kk % kFp4Keys;
+                    if (kk < kFp4Keys ? put0 : put1) {
+                        float* k = s_ksc + (kk < kFp4Keys ? at0 : at1) * 2 * kFp4Keys + key / 2 * 4 + (key & 1);
                         k[0] = scale[e];
                         k[2] = scale[e] * a.scale_log2;
                     }
                 }
                 __syncwarp();
-                if (lane < 2 && (lane == 0 || two)) mbar_arrive(&kfull[(g + lane) % kFp4Entries]);
-                g += two ? 2 : 1;
+                if (mine) mbar_arrive(&kfull[my_at]);
+                g += (put0 ? 1 : 0) + (put1 ? 1 : 0);
+                first = first && !put0 && !put1;
             }
         }
         if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
@@ -795,7 +806,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         // rescaled and exp2(s - m) <= 2^8.  l_run: the lane's share of the sum of the fp32 probabilities, two halves
         float m_run[2] = {-INFINITY, -INFINITY};
         uint64_t l_run[2] = {0ull, 0ull};
-        uint64_t seen = 0;  // the row's masks' fault bits
+        bool seen = false;  // a fault bit in one of the row's masks
         int rows = 0;
         auto wait_pv = [&](int g) { return wait_bar(&pvdone[(2 * g + 1) % kFp4Ring], ((2 * g + 1) / kFp4Ring) & 1); };
         // O^T times alpha per head, when a head's maximum moved in tile g: after the other warps' votes for the tile are
@@ -823,11 +834,11 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (tid == 0) DSA_TRACE(g, 4);
-            const int info = s_info[4 * at], unit = s_info[4 * at + 1], pos = s_info[4 * at + 2];
+            const int info = s_info[4 * at];
             if (info & kFirst) {
                 m_run[0] = m_run[1] = -INFINITY;
                 l_run[0] = l_run[1] = 0ull;
-                seen = 0;
+                seen = false;
             }
             float alpha[2] = {1.f, 1.f};
             bool resc = false;
@@ -836,7 +847,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
             tmem_ld_16x48_nowait(tS + b * 64 + lane_off, sv);
             const float4* k4 = reinterpret_cast<const float4*>(s_ksc + at * 2 * kFp4Keys) + c;
             const uint64_t vm = s_mask[at];
-            seen |= vm;
+            seen = seen || (vm & kFp4Fault);
             float m0[2];  // the logits are taken relative to m0: the running maximum, 0 before the first key
             uint64_t neg[2];
 #pragma unroll
@@ -924,13 +935,15 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
             fence_proxy_async_smem();  // P^T stores -> async proxy
             tc_fence_before();
             __syncwarp();
+            const int unit = s_info[4 * at + 1], pos = s_info[4 * at + 2];
+            __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&pfull[b]);
                 mbar_arrive(&kfree[at]);
             }
             if (tid == 0) DSA_TRACE(g, 5);
             if (info & kLast) {
-                const bool fault = seen & kFp4Fault;
+                const bool fault = seen;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int head = head0 + 8 * h;
@@ -978,7 +991,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                             s_own[2 * NH + head] = l;
                         }
                     }
-                    if (tid == 0 && (seen & kFp4Fault)) *s_fault = 1;
+                    if (tid == 0 && seen) *s_fault = 1;
                 }
                 break;
             }

@@ -877,3 +877,29 @@ def test_many_rows_of_one_or_two_tiles(heads, topk, window):
     torch.cuda.synchronize()
     assert int(status) == 0
     _check(out, lse, _expected(case))
+
+
+@gpu
+@pytest.mark.parametrize("nq,heads", [(3, 64), (40, 64), (500, 16)])
+def test_tiles_without_a_key_are_left_out(nq, heads):
+    """Top-k rows with runs of -1 as long as several tiles, at the front, in the middle, at the end and all along: the same
+    values as rows without the padding, whatever tiles are left."""
+    spec = S("gaps", cached=[3000 - i for i in range(nq)], new=[1] * nq, heads=heads, topk=600, window=40, seed=97, **F)
+    case = _attn_case(spec, "random", seed=7)
+    tk = case["topk"]
+    for j in range(nq):
+        cut = [(0, 200), (150, 430), (10, 600), (0, 600), (0, 0), (48, 96), (1, 599), (300, 600)][j % 8]
+        tk[j, cut[0]:cut[1]] = -1
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    _check(out, lse, _expected(case, range(0, nq, max(1, nq // 60))))
+    for j in (3 % nq, 2 % nq):      # an unmapped block whose only entry is alone in its tile
+        pick = int((tk[j] >= 0).nonzero()[0]) if (tk[j] >= 0).any() else 300
+        tk[j, pick] = 17
+        case["bt_main"][j, 17 // case["epb"]] = -1
+    out, lse, status, _ = _run(case, _on_gpu(case))
+    torch.cuda.synchronize()
+    assert int(status) == dsa.DSA_ERR_DEVICE_FAULT
+    for j in (3 % nq, 2 % nq):
+        assert not np64(out[j]).any() and np.isneginf(np64(lse[j])).all()
