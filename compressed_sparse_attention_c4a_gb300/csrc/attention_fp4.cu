@@ -24,9 +24,9 @@ namespace dsa {
 //
 // The tiles of a CTA form one stream, described by a ring of six entries: the keys' addresses, scales and mask, and whether
 // the tile is the first or last of its row or the last of all.
-//   warp 7      resolves: two tiles at a time, three keys a lane (top-k index -> block table -> row address, row scale); a
-//               tile without a key (the padding of a short top-k row) is left out: 1153 prefill rows of up to 333 entries,
-//               16 heads, 130 us with those tiles, 91 without;
+//   warp 7      resolves: two tiles at a time, three keys a lane (top-k index -> block table -> row address, row scale).  The
+//               -1 that a top-k row ends in are cut off (many rows), and a tile without a key is left out: 1153 prefill
+//               rows with lists of 333, mostly padding, 16 heads, 130 us with all tiles, 91 without empty ones, 66 so;
 //   warps 8 on  widen: twelve warps own 4 keys of every tile (in the cluster kernel eight own 6).  The rows' bytes are copied
 //               into shared memory with cp.async, each half of the warp's share again as soon as it is converted, so a
 //               tile's copies have a whole tile's time; the codes become bf16 and are stored 128B-swizzled as
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
     // Position, request, block tables and query rows: inputs that no kernel of the layer step writes, read while the
     // preceding kernel finishes.  Top-k indices, cache rows and every output come after the wait.
     auto row_of = [&](int unit) { return unit >> (a.hg_count - 1); };  // one head group a row, or two
-    auto make_unit = [&](int unit, int r, int m) {
+    auto make_unit = [&](int unit, int r, int m, int listed) {  // listed: top-k entries to look at
         Unit u;
         u.row = row_of(unit);
         u.hg = unit - u.row * a.hg_count;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         u.ok = r >= 0 && r < a.main_bt.batch && r < a.swa_bt.batch && m >= 0;
         const uint32_t tokens = (uint32_t)m + 1u;  // entries_formed() by a shift: the stride is a power of two
         u.n_vis = u.ok && tokens >= (uint32_t)a.kind_w ? (int)((tokens - a.kind_w) >> (__ffs(a.kind_s) - 1)) + 1 : 0;
-        u.n_comp = a.topk ? a.k : u.n_vis;
+        u.n_comp = a.topk ? listed : u.n_vis;
         u.wlo = max(0, m - a.window + 1);
         u.n_keys = u.ok ? u.n_comp + (m - u.wlo + 1) : 0;
         const int n_tiles = (u.n_keys + kFp4Keys - 1) / kFp4Keys;
@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         // ---- resolve: every unit's tiles, two at a time: key kk = lane + 32 e of the two tiles' 96 ---------------
         const int main_shift = __ffs(a.main.rows_per_block) - 1;  // 64 or 2 rows a block; the window's 256
         int g = 0;
+        int tail = ROWS ? load_int_if(a.topk + (long long)row_of(unit0) * a.k + a.k - 1, a.topk != nullptr) : 0;
         for (int unit = unit0, ord = 0; unit < units && ok; unit += unit_step, ++ord) {
             const int32_t* const row_topk = a.topk + (long long)row_of(unit) * a.k;
             int entry[3];  // top-k indices of the next two tiles' keys (-1: none); the first ones before the position is here
@@ -478,11 +479,28 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                 const int j = t * kFp4Keys + kk % kFp4Keys;
                 entry[e] = load_int_if(row_topk + j, a.topk && j < a.k);
             }
-            const Unit u = make_unit(unit, r0, m0);
+            int listed = a.k;
+            if (ROWS && a.topk && tail < 0) {  // the list without the -1 it ends in, looked through from its end
+                for (listed = a.k - 1; listed > 0;) {
+                    int v[8], top = -1;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const int j = listed - 1 - (32 * n + lane);
+                        v[n] = load_int_if(row_topk + max(j, 0), j >= 0);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) top = max(top, v[n] >= 0 ? listed - 1 - (32 * n + lane) : -1);
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    listed = top >= 0 ? top + 1 : max(listed - 256, 0);
+                    if (top >= 0) break;
+                }
+            }
+            const Unit u = make_unit(unit, r0, m0, listed);
             if (unit + unit_step < units) {  // the next unit's, in flight meanwhile
                 const int next = row_of(unit + unit_step);
                 r0 = a.q_req ? load_int_if(a.q_req + next, true) : next;
                 m0 = load_int_if(a.q_pos + next, true);
+                tail = ROWS ? load_int_if(a.topk + (long long)next * a.k + a.k - 1, a.topk != nullptr) : 0;
             }
             if (!u.ok && lane == 0 && crank == 0) report(a.status, DSA_ERR_DEVICE_FAULT);
             auto key_index = [&](int i, int e) -> int {  // of the row, -1: none
