@@ -66,7 +66,7 @@ typedef int32_t dsa_status_t;
                           with scale = the least power of two with amax <= 2688 * scale (at least 2^-126; 1 for a row of
                           zeros), block scale = e4m3(block amax / (6 * scale)), code = e2m1(x / (scale * block scale)),
                           each to nearest even and saturating; a row with an infinity or a NaN is stored with scale NaN
-                          and zero codes, and reads back as NaN */
+                          and zero codes, and reads back as NaN.  Block scales are finite and not negative */
 
 /* compressor kinds ([P1] §5.2, [P2] 机制二) */
 #define DSA_C4A 0   /* window 8 raw tokens, stride 4: 64 entries per block */
@@ -346,7 +346,9 @@ dsa_status_t dsa_attn_plan(int32_t nq, int32_t heads, int32_t max_keys, int32_t 
  * q          [batch][heads][512] bf16, already rotated at m;  q_pos [batch] int32
  * kind       DSA_C4A or DSA_C128A (visibility and rows_per_block of `main`)
  * topk       [batch][k] int32 logical entry ids (-1 = none) or NULL;  k host int <= 2048
- * main, swa  pools with dim 512, both bf16, both e4m3 or both DSA_FP4_BLOCK;  window: host int, 1..1024
+ * main, swa  pools with dim 512, both bf16, both e4m3 or both DSA_FP4_BLOCK (whose rows are widened to bf16 exactly; rows
+ *            whose largest value is below 2^-105 lose accuracy: a probability times such a row's scale leaves bf16's
+ *            normal range);  window: host int, 1..1024
  * sm_scale   host float (1/sqrt(512) in the layer)
  * out        [batch][heads][512] bf16;  lse [batch][heads] fp32 (natural log of the softmax
  *            denominator) or NULL
