@@ -848,7 +848,7 @@ static size_t workspace_bytes_for(int rows, const SplitPlan& p, int heads) {
     return (size_t)rows * p.nsplit * heads * (kD + 4) * sizeof(float);
 }
 
-// Workspace that covers every row format (bf16 and e4m3 rows share a plan) (the size query does not know the pool's format).
+// Workspace that covers every row format (the size query does not know the pool's; bf16 and e4m3 rows share a plan).
 static size_t workspace_bytes_any(int rows, int heads, int max_keys) {
     return std::max(workspace_bytes_for(rows, plan_for(rows, heads, max_keys, DSA_BF16), heads),
                     workspace_bytes_for(rows, plan_for(rows, heads, max_keys, DSA_FP4_BLOCK), heads));
@@ -1169,7 +1169,7 @@ extern "C" dsa_status_t dsa_sparse_attn_decode_static(int32_t batch, int32_t hea
     if (batch == 0) return DSA_OK;
     if (heads != 16 && heads != 32 && heads != 64 && heads != 128) return DSA_ERR_UNSUPPORTED;
     const int max_comp = topk ? k : main_bt->max_blocks * main->rows_per_block;
-    const size_t need = workspace_bytes_any(batch, heads, max_comp + window);
+    const size_t need = workspace_bytes_for(batch, plan_for(batch, heads, max_comp + window, main->dtype), heads);
     if (need > kStaticScratchBytes) return DSA_ERR_UNSUPPORTED;  // beyond the fixed scratch: use the workspace call
     int st = DSA_OK;
     void* scratch = need > 0 ? static_scratch(&st) : nullptr;
