@@ -71,21 +71,25 @@ constexpr int kOdd = 8, kOdd2 = 16;               // the two lowest bits of the 
 // block scale of up to 448 must stay below 2^128, so it is 2^118.
 constexpr int kFp4Shift = 8;
 
-// Bounded wait (2 s of %globaltimer).  Only the first try is inline: the kernel's roles run side by side and share the
-// instruction caches, and with every wait's loop, every tile loop unrolled and the rare paths inline the schedulers
-// mostly waited for instructions (3.9 cycles of it per issued instruction).
-__device__ __noinline__ bool wait_bar_slow(uint64_t* bar, uint32_t parity) {
-    const uint64_t t0 = global_ns();
-    do {
-#pragma unroll 1
-        for (int k = 0; k < 64; ++k)
-            if (mbar_try_wait(bar, parity)) return true;
-    } while (global_ns() - t0 <= kWaitLimitNs);
-    return false;
+// Bounded wait (2 s of %globaltimer, its low word).  Inline, but a few instructions: the kernel's roles run side by side and
+// share the instruction caches (with 64-bit times, every tile loop unrolled and the rare paths inline the schedulers mostly
+// waited for instructions, 3.9 cycles of it per issued instruction).  A call out of line here makes every value that is
+// live across a wait take a register that calls preserve: 357 us for the prefill below against 334.
+__device__ __forceinline__ uint32_t global_ns_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_bar_slow(bar, parity);
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = global_ns_lo();
+#pragma unroll 1
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while (global_ns_lo() - t0 <= (uint32_t)kWaitLimitNs);
+    return false;
 }
+static_assert(kWaitLimitNs < 0x80000000ull, "within the low word");
 
 template <int NH>
 struct Fp4Smem {
@@ -271,7 +275,7 @@ __device__ __noinline__ void rescale_quadrant(uint32_t taddr, const float* alpha
 // prefill below, 355 so.)
 template <int NH>
 __device__ __noinline__ void store_row(const RopeTable& rope, uint16_t* out_row, uint32_t taddr, const float* inv, int ww,
-                                       int m, bool fault) {
+                                       int m, bool fault, uint64_t* ofree) {
     constexpr int kHeads = NH / 2, kStep = kHeads < 16 ? kHeads : 16, kSteps = kHeads / kStep;
     const int lane = threadIdx.x & 31, quad = ww & 3, hbase = (ww >> 2) * kHeads;
     const int first_rot = kD - rope.rope_dim;
@@ -291,7 +295,13 @@ __device__ __noinline__ void store_row(const RopeTable& rope, uint16_t* out_row,
             const float4 f = *reinterpret_cast<const float4*>(inv + h0 + e);
             x[e] = v[e] * f.x, x[e + 1] = v[e + 1] * f.y, x[e + 2] = v[e + 2] * f.z, x[e + 3] = v[e + 3] * f.w;
         }
-        if (n + 1 < 4 * kSteps) tmem_ld_nowait<kStep>(taddr + (n + 1) / kSteps * NH + (n + 1) % kSteps * kStep, v);
+        if (n + 1 < 4 * kSteps) {
+            tmem_ld_nowait<kStep>(taddr + (n + 1) / kSteps * NH + (n + 1) % kSteps * kStep, v);
+        } else {  // all read: the next row's products may begin
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ofree);
+        }
         if (fault) {
 #pragma unroll
             for (int e = 0; e < kStep; ++e) x[e] = 0.f;
@@ -633,10 +643,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
             const int unit = s_orow[par * 4], row = row_of(unit);
             tc_fence_after();
             store_row<NH>(a.rope, a.out + ((long long)row * a.heads + (unit - row * a.hg_count) * NH) * kD, tO, s_inv + par * NH,
-                          ww, s_orow[par * 4 + 2], s_orow[par * 4 + 3]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ofree);  // the next row's products may begin
+                          ww, s_orow[par * 4 + 2], s_orow[par * 4 + 3], ofree);
             ++done;
         };
         int ends[3] = {0, 0, 0}, n_ends = 0;  // half-tiles after which the next rows' products are complete
