@@ -28,11 +28,10 @@ namespace dsa {
 //               -1 that a top-k row ends in are cut off (many rows), and a tile without a key is left out: 1153 prefill
 //               rows with lists of 333, mostly padding, 16 heads, 130 us with all tiles, 91 without empty ones, 66 so;
 //   warps 8 on  widen: twelve warps own 4 keys of every tile (in the cluster kernel eight own 6).  The rows' bytes are copied
-//               into shared memory with cp.async, each half of the warp's share again as soon as it is converted, so a
-//               tile's copies have a whole tile's time; the codes become bf16 and are stored 128B-swizzled as
-//               [64-dim chunk][48 keys][128 B], the first 256 dims, then the others.  Many rows: between two half-tiles,
-//               when a row's last product is done, the first eight of these warps read its O^T from TMEM, rotate and
-//               store it;
+//               into shared memory with cp.async, the next tile's as soon as this one's have been read into registers;
+//               the codes become bf16 and are stored 128B-swizzled as [64-dim chunk][48 keys][128 B], the first 256 dims,
+//               then the others.  Many rows: between two tiles, when a row's last product is done, the first eight of
+//               these warps read its O^T from TMEM, rotate and store it;
 //   warps 4, 6  S = Q K^T (M = 64 heads, N = 48 keys) of even and odd tiles;
 //   warp 5      O^T += V^T P^T (four tiles of M = 128 dims, N = NH heads, K = 48 keys);
 //   warps 0-3   softmax: 16 heads a warp, a head's 48 logits over the 4 lanes of a quad (the 16-lane TMEM load spreads a
@@ -40,17 +39,18 @@ namespace dsa {
 // The widened keys are a ring of five half-tiles (48 keys x 256 dims): S starts on the first half, P V frees it first.  Two
 // S and two P buffers.
 //
-// What bounds it (2048 rows of 640 keys, 64 heads: 355 us, a tile in about 3,000 cycles): shared memory is busy for 2,070
-// of them (reads of S 896 and of P V 576, widened stores 384, P^T 48, the rows' copies and loads 216), the schedulers
-// issue in 61 % of theirs, the tensor cores work in 33 %; and a row's O^T is read out while its successor's products
-// wait, about 5,000 cycles a row.  What else was measured on the way, in us: one CTA a row 463; rows loaded straight into
-// registers 446 (227 KB of shared memory leave the L1 cache about 220 lines, which the rows of one tile fill, and further
-// loads wait for lines when they are issued); loops unrolled and waits inline 578 (the roles share the instruction caches);
-// matrix instructions with descriptors computed in ordinary registers 390 (77 cycles to issue one, 35 with uniform ones);
-// the rows fetched by a warp of its own, with bulk copies 509 (100 cycles a row), with cp.async 397; tiles of 32 keys 416;
-// a tile widened in one step instead of two 422; eight widening warps 367; all twelve storing a finished row 384 (this
-// kernel then spills); a finished row stored as soon as its product is done, at any half-tile, 375.
-// A decode row's 17 us (32 rows of 640 keys, clusters of 4): 2.2 until the first keys are widened (position, block table,
+// What bounds it (2048 rows of 640 keys, 64 heads: 325 us, a tile in about 2,800 cycles): shared memory is busy for 2,070
+// of them by its bytes alone (reads of S 896 and of P V 576, widened stores 384, P^T 48, the rows' copies and loads 216),
+// and a row's O^T is read out while its successor's products wait, about 5,000 cycles a row.  What else was measured on the
+// way, in us, each against the kernel of its time: one CTA a row 463 against 394; rows loaded straight into registers 446
+// (227 KB of shared memory leave the L1 cache about 220 lines, which the rows of one tile fill, and further loads wait for
+// lines when they are issued); loops unrolled and waits inline with 64-bit times 578 (the roles share the instruction
+// caches); matrix instructions with descriptors computed in ordinary registers 390 against 361 (77 cycles to issue one, 35
+// with uniform ones); the rows fetched by a warp of its own, with bulk copies 509 (100 cycles a row), with cp.async 397;
+// tiles of 32 keys 416; eight widening warps 367 against 363; all twelve storing a finished row 330 against 325; a finished
+// row stored as soon as its product is done, at any half-tile, 375 against 361; the copies in halves, each when its half
+// has been converted, 334 against 325.
+// A decode row's 16.5 us (32 rows of 640 keys, clusters of 4): 2.2 until the first keys are widened (position, block table,
 // rows, one load after the other), 6 for four tiles, 3 for the last tile's chain, 6 for the merge across the cluster.
 constexpr int kFp4Ring = 5;                            // widened half-tiles
 constexpr int kFp4Half = kFp4Keys * (kD / 2) * 2;
@@ -608,32 +608,30 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         const uint32_t raw_codes = raw + q * kFp4BlockRow + t * 8, raw_scale = raw + q * kFp4BlockRow + kD / 2 + t;
         const int hf = (t >> 2) & 1, p0 = 2 * (t & 3) + hf;
         const uint32_t dst0 = sK + (t >> 2) * kFp4Chunk;
-        // Copying, lanes 0-17: of a pair's row lane / 9, 16-byte piece lane % 9 of a half (8 of codes, one of 16 scales).
-        const int cr = lane >= 9 ? 1 : 0, cp = lane - 9 * cr;
-        const uint32_t cp_off = cp < 8 ? cp * 16 : kD / 2, cp_step = cp < 8 ? kD / 4 : 16;  // half 0, and to half 1
-        uint64_t src[kFp4Pairs];        // global address of the lane's piece (half 0) of the row of each pair
-        uint32_t src_bytes[kFp4Pairs];  // 16, or 0 to fill with zeros (a masked key)
-        auto aim = [&](int g) {         // at tile g's rows
+        // Copying: the warp's rows are kFp4PerWarp * 18 pieces of 16 bytes, contiguous in shared memory; a lane's are lane + 32 n.
+        constexpr int kPieces = kFp4PerWarp * 18, kCopies = (kPieces + 31) / 32;
+        uint64_t src[kCopies];        // global addresses of the lane's pieces
+        uint32_t src_bytes[kCopies];  // 16, or 0 to fill with zeros (a masked key)
+        auto aim = [&](int g) {       // at tile g's rows
 #pragma unroll
-            for (int u = 0; u < kFp4Pairs; ++u) {
-                const uint64_t at = s_addr[g % kFp4Entries * kFp4Keys + ww * kFp4PerWarp + 2 * u + cr];
-                src[u] = (at ? at : reinterpret_cast<uint64_t>(a.main.data)) + cp_off;
-                src_bytes[u] = at ? 16u : 0u;
+            for (int n = 0; n < kCopies; ++n) {
+                const int p = lane + 32 * n, r = p / 18;
+                const uint64_t at = s_addr[g % kFp4Entries * kFp4Keys + ww * kFp4PerWarp + min(r, kFp4PerWarp - 1)];
+                src[n] = (at ? at : reinterpret_cast<uint64_t>(a.main.data)) + (p - 18 * r) * 16;
+                src_bytes[n] = at ? 16u : 0u;
             }
         };
-        auto copy = [&](int h) {  // one group: a half of the warp's rows
-            if (lane < 18)
+        auto copy = [&]() {
 #pragma unroll
-                for (int u = 0; u < kFp4Pairs; ++u)
-                    cp_async16_nc(raw + (2 * u + cr) * kFp4BlockRow + cp_off + h * cp_step,
-                                  reinterpret_cast<const void*>(src[u] + h * cp_step), src_bytes[u]);
+            for (int n = 0; n < kCopies; ++n)
+                if (lane + 32 * n < kPieces)
+                    cp_async16_nc(raw + (lane + 32 * n) * 16, reinterpret_cast<const void*>(src[n]), src_bytes[n]);
             cp_async_commit();
         };
         ok = __all_sync(0xffffffffu, entry_wait(rfull, 0));
         if (ok) {
             aim(0);
-            copy(0);
-            copy(1);
+            copy();
         }
         int done = 0;  // rows stored
         auto output = [&]() {  // the next finished row, whose last product is known to be complete
@@ -655,13 +653,15 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
             const bool final = info & kFinal, last = info & kLast;
             if (final) {
 #pragma unroll
-                for (int u = 0; u < kFp4Pairs; ++u) src_bytes[u] = 0u;
+                for (int n = 0; n < kCopies; ++n) src_bytes[n] = 0u;
             } else {  // tile g + 1's rows, whose copies follow each part of tile g that has been converted
                 ok = __all_sync(0xffffffffu, entry_wait(rfull, g + 1));
                 if (!ok) break;
                 aim(g + 1);
             }
             if (ww == 0 && lane == 0) DSA_TRACE(g, 0);
+            uint2 code[2][kFp4Pairs];
+            uint32_t byte[2][kFp4Pairs];
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (lap > 0) ok = ok && wait_bar(&pvdone[slot], (lap - 1) & 1);
@@ -672,27 +672,32 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
                         ends[0] = ends[1], ends[1] = ends[2], --n_ends;
                     }
                 if (!ok) break;
-                cp_async_wait_group<1>();  // this half of tile g's rows, two groups ago
-                __syncwarp();
-                uint2 code[kFp4Pairs];
-                uint32_t byte[kFp4Pairs];
+                if (h == 0) {
+                    cp_async_wait_all();
+                    __syncwarp();
 #pragma unroll
-                for (int u = 0; u < kFp4Pairs; ++u) {
-                    code[u] = lds64(raw_codes + 2 * u * kFp4BlockRow + h * (kD / 4));
-                    byte[u] = lds8(raw_scale + 2 * u * kFp4BlockRow + h * 16);
+                    for (int u = 0; u < kFp4Pairs; ++u)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            code[n][u] = lds64(raw_codes + 2 * u * kFp4BlockRow + n * (kD / 4));
+                            byte[n][u] = lds8(raw_scale + 2 * u * kFp4BlockRow + n * 16);
+                        }
+                    __syncwarp();
+                    copy();  // tile g + 1's rows take their place
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kFp4Pairs; ++u) code[0][u] = code[1][u], byte[0][u] = byte[1][u];
                 }
-                __syncwarp();
-                copy(h);  // the same half of tile g + 1's
                 const uint32_t to = dst0 + slot * kFp4Half;
 #pragma unroll
                 for (int u = 0; u < kFp4Pairs; ++u) {
                     const int kk = ww * kFp4PerWarp + 2 * u + q;
-                    const uint32_t at = to + (kk >> 3) * 1024 + (kk & 7) * 128, s2 = block_scale_2p118(byte[u]);
+                    const uint32_t at = to + (kk >> 3) * 1024 + (kk & 7) * 128, s2 = block_scale_2p118(byte[0][u]);
                     const uint32_t piece = (p0 ^ (kk & 7)) << 4;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         uint32_t o[4];
-                        widen8((e != 0) != (hf != 0) ? code[u].y : code[u].x, s2, o);
+                        widen8((e != 0) != (hf != 0) ? code[0][u].y : code[0][u].x, s2, o);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (piece ^ (16u * e))), "r"(o[0]),
                                      "r"(o[1]), "r"(o[2]), "r"(o[3])
                                      : "memory");
