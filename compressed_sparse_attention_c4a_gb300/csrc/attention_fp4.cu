@@ -27,11 +27,10 @@ namespace dsa {
 //   warp 7      resolves: two tiles at a time, three keys a lane (top-k index -> block table -> row address, row scale).  The
 //               -1 that a top-k row ends in are cut off (many rows), and a tile without a key is left out: 1153 prefill
 //               rows with lists of 333, mostly padding, 16 heads, 130 us with all tiles, 91 without empty ones, 66 so;
-//   warps 8 on  widen: twelve warps own 4 keys of every tile (in the cluster kernel eight own 6).  The rows' bytes are copied
-//               into shared memory with cp.async, the next tile's as soon as this one's have been read into registers;
-//               the codes become bf16 and are stored 128B-swizzled as [64-dim chunk][48 keys][128 B], the first 256 dims,
-//               then the others.  Many rows: between two tiles, when a row's last product is done, the first eight of
-//               these warps read its O^T from TMEM, rotate and store it;
+//   warps 8-15  widen: each owns 6 keys of every tile.  The rows' bytes are copied into shared memory with cp.async, the next
+//               tile's as soon as this one's have been read into registers; the codes become bf16 and are stored
+//               128B-swizzled as [64-dim chunk][48 keys][128 B], the first 256 dims, then the others.  Many rows: between
+//               two tiles, when a row's last product is done, these warps read its O^T from TMEM, rotate and store it;
 //   warps 4, 6  S = Q K^T (M = 64 heads, N = 48 keys) of even and odd tiles;
 //   warp 5      O^T += V^T P^T (four tiles of M = 128 dims, N = NH heads, K = 48 keys);
 //   warps 0-3   softmax: 16 heads a warp, a head's 48 logits over the 4 lanes of a quad (the 16-lane TMEM load spreads a
@@ -39,7 +38,7 @@ namespace dsa {
 // The widened keys are a ring of five half-tiles (48 keys x 256 dims): S starts on the first half, P V frees it first.  Two
 // S and two P buffers.
 //
-// What bounds it (2048 rows of 640 keys, 64 heads: 325 us, a tile in about 2,800 cycles): shared memory is busy for 2,070
+// What bounds it (2048 rows of 640 keys, 64 heads: 317 us, a tile in about 2,700 cycles): shared memory is busy for 2,070
 // of them by its bytes alone (reads of S 896 and of P V 576, widened stores 384, P^T 48, the rows' copies and loads 216),
 // and a row's O^T is read out while its successor's products wait, about 5,000 cycles a row.  What else was measured on the
 // way, in us, each against the kernel of its time: one CTA a row 463 against 394; rows loaded straight into registers 446
@@ -47,20 +46,18 @@ namespace dsa {
 // lines when they are issued); loops unrolled and waits inline with 64-bit times 578 (the roles share the instruction
 // caches); matrix instructions with descriptors computed in ordinary registers 390 against 361 (77 cycles to issue one, 35
 // with uniform ones); the rows fetched by a warp of its own, with bulk copies 509 (100 cycles a row), with cp.async 397;
-// tiles of 32 keys 416; eight widening warps 367 against 363; all twelve storing a finished row 330 against 325; a finished
-// row stored as soon as its product is done, at any half-tile, 375 against 361; the copies in halves, each when its half
-// has been converted, 334 against 325.
+// tiles of 32 keys 416; a finished row stored as soon as its product is done, at any half-tile, 375 against 361; the copies
+// in halves, each when its half has been converted, 334 against 325; twelve widening warps of 4 keys 325 against 317.
 // A decode row's 16.5 us (32 rows of 640 keys, clusters of 4): 2.2 until the first keys are widened (position, block table,
 // rows, one load after the other), 6 for four tiles, 3 for the last tile's chain, 6 for the merge across the cluster.
 constexpr int kFp4Ring = 5;                            // widened half-tiles
 constexpr int kFp4Half = kFp4Keys * (kD / 2) * 2;
 constexpr int kFp4Chunk = kFp4Keys * 128;              // bytes of a 64-dim chunk
 constexpr int kFp4Entries = 6;                         // described tiles
-// Widening warps: three on each of the SM's four schedulers, or two in the cluster kernel (attn_finish takes 512 threads).
-template <bool ROWS>
-constexpr int kFp4Widen = ROWS ? 12 : 8;
-template <bool ROWS>
-constexpr int kFp4Threads = 256 + 32 * kFp4Widen<ROWS>;
+constexpr int kFp4Widen = 8;                           // widening warps, two on each of the SM's four schedulers
+constexpr int kFp4PerWarp = kFp4Keys / kFp4Widen;      // keys of a tile per widening warp
+constexpr int kFp4Pairs = kFp4PerWarp / 2;             // a warp converts two rows at a time
+static_assert(kFp4Widen * kFp4PerWarp == kFp4Keys && kFp4Pairs * 2 == kFp4PerWarp && 256 + 32 * kFp4Widen == kClThreads, "roles");
 constexpr int kFp4Groups = kFp4Keys / 8;               // groups of 8 keys (the softmax's columns)
 constexpr uint64_t kFp4AllValid = (1ull << kFp4Keys) - 1;
 constexpr uint64_t kFp4Fault = 1ull << 63;             // mask bit: a key of the tile hit a device fault
@@ -269,7 +266,7 @@ __device__ __noinline__ void rescale_quadrant(uint32_t taddr, const float* alpha
     tmem_wait_st();
 }
 
-// A finished row's output, by the first eight widening warps (ww): O^T from TMEM, times the row's factor per head, rotated
+// A finished row's output, by the widening warps (ww): O^T from TMEM, times the row's factor per head, rotated
 // by R_m^-1, to global memory.  Warp quadrant = 32 dims of each 128-dim tile, lane = dim, half of the heads; a store of a
 // warp is 64 bytes of one head's row.  (Neighbouring lanes exchanging values to store words of two dims: 361 us for the
 // prefill below, 355 so.)
@@ -339,12 +336,10 @@ struct Unit {
 };
 
 template <int NH, bool ROWS>
-__global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
+__global__ void __launch_bounds__(kClThreads, 1)
     attn_fp4_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
                     const __grid_constant__ AttnArgs a) {
     using L = Fp4Smem<NH>;
-    constexpr int kWiden = kFp4Widen<ROWS>, kFp4PerWarp = kFp4Keys / kWiden, kFp4Pairs = kFp4PerWarp / 2;
-    static_assert(kWiden * kFp4PerWarp == kFp4Keys && kFp4Pairs * 2 == kFp4PerWarp, "a warp converts two rows at a time");
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sQ = smem_u32(smem + L::kOffQ), sK = smem_u32(smem + L::kOffK), sP = smem_u32(smem + L::kOffP);
     uint64_t* s_addr = reinterpret_cast<uint64_t*>(smem + L::kOffAddr);
@@ -388,7 +383,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
     if (tid == 0) {
         DSA_STAMP(0);
         for (int b = 0; b < kFp4Ring; ++b) {
-            mbar_init(&full[b], kWiden);
+            mbar_init(&full[b], kFp4Widen);
             mbar_init(&pvdone[b], 1);
         }
         for (int b = 0; b < kFp4Entries; ++b) {
@@ -404,13 +399,13 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
         mbar_init(&qfull[1], 1);
         mbar_init(rdone, 4);
         mbar_init(ostat, 4);
-        mbar_init(ofree, 8);
+        mbar_init(ofree, kFp4Widen);
         for (int b = 0; b < 3; ++b) mbar_init(&xfull[b], 1);
         *s_fault = 0;
         fence_barrier_init();
     }
     if constexpr (NH < 64)  // the S product reads 64 query rows: rows NH.. are zero
-        for (int i = tid; i < 8 * (64 - NH) * 8; i += kFp4Threads<ROWS>) {
+        for (int i = tid; i < 8 * (64 - NH) * 8; i += kClThreads) {
             const int c = i / ((64 - NH) * 8), rr = NH + (i / 8) % (64 - NH), u = i % 8;
             *reinterpret_cast<uint4*>(smem + L::kOffQ + c * 8192 + rr * 128 + u * 16) = make_uint4(0, 0, 0, 0);
         }
@@ -710,7 +705,7 @@ __global__ void __launch_bounds__(kFp4Threads<ROWS>, 1)
             }
             if (ww == 0 && lane == 0) DSA_TRACE(g, 1);
             if constexpr (ROWS)
-                if (last && ww < 8) {
+                if (last) {
                     const int end = 2 * g + 1;
                     if (n_ends == 0) ends[0] = end;
                     else if (n_ends == 1) ends[1] = end;
@@ -1060,10 +1055,10 @@ static dsa_status_t launch(AttnArgs a, int cl, cudaStream_t st) {
         return DSA_ERR_CUDA;
     cudaError_t e;
     if (rows)
-        e = launch_pdl(kernel, dim3((unsigned)std::min<long long>(units, sm_count())), dim3(kFp4Threads<true>), L::kAlloc, st,
+        e = launch_pdl(kernel, dim3((unsigned)std::min<long long>(units, sm_count())), dim3(kClThreads), L::kAlloc, st,
                        qmap, omap, a);
     else
-        e = launch_pdl_cluster(kernel, dim3((unsigned)grid), dim3(kFp4Threads<false>), L::kAlloc, st, cl, qmap, omap, a);
+        e = launch_pdl_cluster(kernel, dim3((unsigned)grid), dim3(kClThreads), L::kAlloc, st, cl, qmap, omap, a);
     if (e == cudaSuccess && a.nsplit > 1) e = launch_attn_combine(a, st);
     if (e != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();
@@ -1077,7 +1072,7 @@ int fp4_clusters(int cl) {
     if (seen && seen->load(std::memory_order_relaxed) > 0) return seen->load(std::memory_order_relaxed);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(sm_count() / cl * cl));
-    cfg.blockDim = dim3(kFp4Threads<false>);
+    cfg.blockDim = dim3(kClThreads);
     cfg.dynamicSmemBytes = Fp4Smem<64>::kAlloc;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
