@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
             tc_fence_after();
             float sv[24];  // logits of head h in 4 e + 2 h, 4 e + 2 h + 1: keys 8 e + 2 c, + 1
             tmem_ld_16x48_nowait(tS + b * 64 + lane_off, sv);
-            const float4* k4 = reinterpret_cast<const float4*>(s_ksc + at * 2 * kFp4Keys) + c;
+            const float2* k2 = reinterpret_cast<const float2*>(s_ksc + at * 2 * kFp4Keys) + 2 * c;
             const uint64_t vm = s_mask[at];
             seen = seen || (vm & kFp4Fault);
             float m0[2];  // the logits are taken relative to m0: the running maximum, 0 before the first key
@@ -884,8 +884,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
             tmem_regs_after_wait<24>(sv);
 #pragma unroll
             for (int e = 0; e < kFp4Groups; ++e) {
-                const float4 k = k4[4 * e];
-                const uint64_t kl = pack_f32x2(k.z, k.w);
+                const float2 k = k2[8 * e + 1];
+                const uint64_t kl = pack_f32x2(k.x, k.y);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     unpack_f32x2(fma_f32x2(pack_f32x2(sv[4 * e + 2 * h], sv[4 * e + 2 * h + 1]), kl, neg[h]),
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
             const uint32_t prow = sP + b * L::kP + head0 * 128 + 4 * c;
 #pragma unroll
             for (int e = 0; e < kFp4Groups; ++e) {
-                const float4 k = k4[4 * e];
+                const float2 k = k2[8 * e];
                 const uint64_t ks = pack_f32x2(k.x, k.y);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
