@@ -435,9 +435,11 @@ __global__ void __launch_bounds__(kClThreads, 1)
         u.wlo = max(0, m - a.window + 1);
         u.n_keys = u.ok ? u.n_comp + (m - u.wlo + 1) : 0;
         const int n_tiles = (u.n_keys + kFp4Keys - 1) / kFp4Keys;
-        u.first = (ROWS ? 0 : split * a.cps) + crank;
+        u.first = split * a.cps + crank;
         u.step = csize;
-        u.end = ROWS ? n_tiles : min(n_tiles, (split + 1) * a.cps);
+        // never more tiles than planned: without a top-k list the position alone sets n_keys, and one beyond the block table
+        // (2^31 - 1: 11 million tiles) has its first unmapped key, a device fault, among the planned tiles
+        u.end = min(n_tiles, (split + 1) * a.cps);
         u.tiles = u.end > u.first ? (u.end - u.first + csize - 1) >> (__ffs(csize) - 1) : 1;
         return u;
     };
