@@ -790,11 +790,13 @@ struct SplitPlan {
     int hg, hg_count, nsplit, cps, cl;
 };
 
+static int tiles_of(int keys, int per_tile) { return keys > 0 ? (keys - 1) / per_tile + 1 : 1; }
+
 static SplitPlan plan_cluster(int rows, int heads, int max_keys) {
     SplitPlan p;
     p.hg = heads >= 64 ? 64 : heads;
     p.hg_count = heads / p.hg;
-    const int n_sub = max(1, (max_keys + kClKeys - 1) / kClKeys);
+    const int n_sub = tiles_of(max_keys, kClKeys);
     const long long units = (long long)rows * p.hg_count;
     const long long sms = sm_count();
     int cl = units * 4 <= sms ? 4 : (units * 2 <= sms ? 2 : 1);
@@ -819,7 +821,7 @@ static SplitPlan plan_fp4(int rows, int heads, int max_keys) {
     SplitPlan p;
     p.hg = heads >= 64 ? 64 : heads;
     p.hg_count = heads / p.hg;
-    const int n_tiles = max(1, (max_keys + kFp4Keys - 1) / kFp4Keys);
+    const int n_tiles = tiles_of(max_keys, kFp4Keys);
     const long long units = (long long)rows * p.hg_count;
     int cl = units <= fp4_clusters(4) ? 4 : (units <= fp4_clusters(2) ? 2 : 1);
     while (cl > 1 && cl > n_tiles) cl >>= 1;
@@ -848,10 +850,29 @@ static size_t workspace_bytes_for(int rows, const SplitPlan& p, int heads) {
     return (size_t)rows * p.nsplit * heads * (kD + 4) * sizeof(float);
 }
 
-// Workspace that covers every row format (the size query does not know the pool's; bf16 and e4m3 rows share a plan).
+// The plan with the most splits that a call of at most max_keys keys can have: a plan's splits rise and fall with the key
+// count (4-bit rows, one row of 64 heads: 19 for 3,648 keys, 11 for 4,224).  From the full length down, until no shorter one
+// can have more than the most seen: splits are at most the clusters that fit and the tiles of a cluster's CTA.
+static SplitPlan widest_plan(int rows, int heads, int max_keys, int dtype) {
+    const int per_tile = dtype == DSA_FP4_BLOCK ? kFp4Keys : kClKeys;
+    const int n_tiles = tiles_of(max_keys, per_tile);
+    SplitPlan widest = plan_for(rows, heads, max_keys, dtype);
+    const int cl = widest.cl;
+    const long long fit = (dtype == DSA_FP4_BLOCK ? fp4_clusters(cl) : sm_count() / cl) / ((long long)rows * widest.hg_count);
+    auto consider = [&](int n) {
+        const SplitPlan p = plan_for(rows, heads, n * per_tile, dtype);
+        if (p.nsplit > widest.nsplit) widest = p;
+    };
+    for (int n = std::min(3, n_tiles - 1); n > 0; --n) consider(n);  // these may have smaller clusters
+    for (int n = n_tiles - 1; n > 3 && widest.nsplit < std::min<long long>(fit, (n + cl - 1) / cl); --n) consider(n);
+    return widest;
+}
+
+// Workspace that covers every row format (the size query does not know the pool's; bf16 and e4m3 rows share a plan) and
+// every length up to max_keys.
 static size_t workspace_bytes_any(int rows, int heads, int max_keys) {
-    return std::max(workspace_bytes_for(rows, plan_for(rows, heads, max_keys, DSA_BF16), heads),
-                    workspace_bytes_for(rows, plan_for(rows, heads, max_keys, DSA_FP4_BLOCK), heads));
+    return std::max(workspace_bytes_for(rows, widest_plan(rows, heads, max_keys, DSA_BF16), heads),
+                    workspace_bytes_for(rows, widest_plan(rows, heads, max_keys, DSA_FP4_BLOCK), heads));
 }
 
 // Tensor map of a [rows][512] bf16 matrix with boxes of 64 columns x box_rows rows, 128B-swizzled.

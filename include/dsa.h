@@ -316,7 +316,8 @@ dsa_status_t dsa_topk_plan(int32_t nq, int32_t ld, int32_t k, int32_t* plan);
  * Workspace (bytes) that dsa_sparse_attn_decode / _prefill need for nq query rows of
  * `heads` heads and at most `max_keys` keys per row (compressed + window) on the current
  * device, for every pool format: the fp32 partial outputs and (max, sums) of rows whose keys
- * are split over several groups of CTAs.  0 means the call needs none.
+ * are split over several groups of CTAs.  A size for max_keys also serves every call of nq rows
+ * whose k (or table) and window give fewer.  0 means that none of these calls needs one.
  */
 size_t dsa_attn_workspace_size(int32_t nq, int32_t heads, int32_t max_keys);
 

@@ -41,3 +41,35 @@ def test_positions_beyond_the_block_table_cost_no_more_than_the_table(rows, head
     for j in (0, rows - 1):
         assert not np64(out[j]).any() and np.isneginf(np64(lse[j])).all(), j
     _check(out, lse, _expected(case, range(1, rows - 1, max(1, rows // 12))))
+
+
+# ---- the workspace ------------------------------------------------------------------------------------------------------
+def _need(rows, heads, keys, fmt):
+    """Bytes of split partials that a call of exactly these sizes needs (its plan; 516 floats per row, split and head)."""
+    _, _, splits, _ = dsa.dsa_attn_plan(rows, heads, keys, fmt)
+    return rows * splits * heads * 516 * 4 if splits > 1 else 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4_block"])
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+def test_a_workspace_sized_for_more_keys_serves_fewer(fmt, heads):
+    """dsa_attn_workspace_size covers every call of at most max_keys keys, whatever the pool's format: the split counts of the
+    plans rise and fall with the key count (host arithmetic)."""
+    for rows in (1, 2, 3, 4, 7, 8, 12, 16, 19, 37, 77, 153):
+        most = 0
+        for keys in sorted(set(range(1, 9000, 61)) | set(range(48, 9000, 96)) | set(range(47, 2400, 48))):
+            most = max(most, _need(rows, heads, keys, fmt))
+            size = dsa.dsa_attn_workspace_size(rows, heads, keys)
+            assert size >= most, (rows, keys, size, most)
+    # no more than the largest need of any format up to there
+    for rows, keys in ((1, 700), (4, 1300), (19, 640), (200, 640)):
+        largest = max(_need(rows, heads, k, f) for k in range(1, keys + 1) for f in ("bf16", "fp8", "fp4_block"))
+        assert dsa.dsa_attn_workspace_size(rows, heads, keys) == largest
+
+
+def test_workspace_size_of_the_longest_lengths():
+    """Sizes near the largest int are answered at once and do not fall."""
+    for rows in (1, 5, 36, 1000):
+        size = dsa.dsa_attn_workspace_size(rows, 64, 8320)
+        for keys in (10 ** 6, 2 ** 31 - 2048, 2 ** 31 - 1):
+            assert dsa.dsa_attn_workspace_size(rows, 64, keys) >= size
