@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
         s_rc[2 * lane + 1] = sn;
     }
     if (warp == 4 && n_mine > 0) {  // the query rows, one 64-dim box per lane
-        if (lane == 0) mbar_expect_tx(qfull, NH * kD * 2);
+        const int never = row == a.stall_row && crank == csize - 1 ? 16 : 0;  // test hook: bytes that no copy brings
+        if (lane == 0) mbar_expect_tx(qfull, NH * kD * 2 + never);
         __syncwarp();
         if (lane < kD / 64) tma_load_2d(smem + L::kOffQ + lane * 8192, &qmap, lane * 64, row * a.heads + hg * NH, qfull);
         __syncwarp();
@@ -945,7 +946,7 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
                                 const dsa_block_table_t* swa_bt, int32_t window, float sm_scale,
                                 const dsa_rope_t* rope, void* out, float* lse, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, void* stream, uint8_t* out8 = nullptr,
-                                float* out_scale = nullptr, const FusedTopk* fz = nullptr) {
+                                float* out_scale = nullptr, const FusedTopk* fz = nullptr, int32_t stall_row = -1) {
     if (rows < 0) return DSA_ERR_INVALID_ARG;
     if (rows == 0) return DSA_OK;
     if (kind != DSA_C4A && kind != DSA_C128A) return DSA_ERR_INVALID_ARG;
@@ -1001,6 +1002,7 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
         a.ws_ml = a.ws_o + (size_t)rows * p.nsplit * heads * kD;
     }
 
+    a.stall_row = stall_row;
     a.status = dev_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool fp8 = main->dtype == DSA_FP8_E4M3, fp4 = main->dtype == DSA_FP4_BLOCK;
@@ -1109,6 +1111,20 @@ extern "C" dsa_status_t dsa_sparse_attn_prefill(int32_t nq, int32_t heads, const
     if (!q_req) return DSA_ERR_INVALID_ARG;
     return sparse_attn(nq, heads, q, q_pos, q_req, kind, topk, k, main, main_bt, swa, swa_bt, window, sm_scale, rope,
                        out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+// Test hook of the bounded waits: a normal launch in which one row's queries never count as loaded, so that every wait
+// that depends on them runs out, with no copy or product in flight by then.
+extern "C" dsa_status_t dsa_debug_sparse_attn_stalled(int32_t nq, int32_t heads, const void* q, const int32_t* q_pos,
+                                                      const int32_t* q_req, int32_t kind, const int32_t* topk, int32_t k,
+                                                      const dsa_pool_t* main, const dsa_block_table_t* main_bt,
+                                                      const dsa_pool_t* swa, const dsa_block_table_t* swa_bt,
+                                                      int32_t window, float sm_scale, const dsa_rope_t* rope, void* out,
+                                                      float* lse, void* workspace, size_t workspace_bytes,
+                                                      int32_t stall_row, int32_t* dev_status, void* stream) {
+    if (stall_row < 0 || stall_row >= nq) return DSA_ERR_INVALID_ARG;
+    return sparse_attn(nq, heads, q, q_pos, q_req, kind, topk, k, main, main_bt, swa, swa_bt, window, sm_scale, rope,
+                       out, lse, workspace, workspace_bytes, dev_status, stream, nullptr, nullptr, nullptr, stall_row);
 }
 
 // ---------------------------------------------------------------------------------------------

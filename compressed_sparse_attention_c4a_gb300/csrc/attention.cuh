@@ -37,6 +37,7 @@ struct AttnArgs {
     const int32_t* n_valid;                   // fused top-k: [rows] valid scores of a row
     int32_t* topk_out;                        // fused top-k: the selected entries [rows][k]
     int nans;                                 // a sum that is NaN makes the row NaN (4-bit rows), else it counts as empty
+    int stall_row;                            // test hook: this row's last CTAs never see their queries arrive (-1: none)
     int32_t* status;
 };
 
@@ -162,7 +163,8 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
     if (tid == 0) DSA_STAMP(17);
     if (csize > 1 && tid == 0)  // before any peer can push (pushes follow phase 1)
         for (int b = 0; b < (csize - 1) * tiles_per; ++b) mbar_arrive_expect_tx(&xfull[b], (uint32_t)L::kTile);
-    const float fo = *s_fault ? 1.f : 0.f;  // this CTA met a device fault: the whole row is written as zeros
+    // this CTA met a device fault, or a wait of its ran out: the whole row is written as zeros
+    const float fo = *s_fault || !all_ok ? 1.f : 0.f;
     for (int h = tid; h < NH; h += kClThreads) {
         const uint32_t dst = smem_u32(smem + L::stat(crank, h));
         const float mo = have ? s_own[h] : -INFINITY, lo = have ? s_own[NH + h] : 0.f,

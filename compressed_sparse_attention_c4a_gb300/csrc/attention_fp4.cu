@@ -105,7 +105,8 @@ struct Fp4Smem {
     static constexpr int kOffPinfo = kOffVote + 32;                 // int [2]: flags of the tile in a P^T buffer
     static constexpr int kOffInv = kOffPinfo + 16;                  // float [2][NH]: output factor of a finished row
     static constexpr int kOffRow = kOffInv + 2 * NH * 4;            // int [2][4]: its unit, -, position, fault
-    static constexpr int kOffFault = kOffRow + 32;                  // int: a key of this CTA hit a device fault
+    // int: a key of this CTA hit a device fault; many rows: the fewest rows that a widening warp whose waits ran out has stored
+    static constexpr int kOffFault = kOffRow + 32;
     static constexpr int kOffRope = kOffFault + 16;                 // float [32][2]: cos, sin of each pair's angle at m
     static constexpr int kBars = 2 * kFp4Ring + 3 * kFp4Entries + 13;
     static constexpr int kOffBar = kOffRope + 256;                  // kBars mbarriers, TMEM address
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
         mbar_init(ostat, 4);
         mbar_init(ofree, kFp4Widen);
         for (int b = 0; b < 3; ++b) mbar_init(&xfull[b], 1);
-        *s_fault = 0;
+        *s_fault = ROWS ? 0x7fffffff : 0;
         fence_barrier_init();
     }
     if constexpr (NH < 64)  // the S product reads 64 query rows: rows NH.. are zero
@@ -445,7 +446,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
     };
     auto load_q = [&](int unit, int odd) {  // by one warp: one 64-dim box per lane
         const int row = row_of(unit);
-        if (lane == 0) mbar_expect_tx(&qfull[odd], NH * kD * 2);
+        const int never = row == a.stall_row && crank == csize - 1 ? 16 : 0;  // test hook: bytes that no copy brings
+        if (lane == 0) mbar_expect_tx(&qfull[odd], NH * kD * 2 + never);
         __syncwarp();
         if (lane < kD / 64)
             tma_load_2d(smem + L::kOffQ + lane * 8192, &qmap, lane * 64, row * a.heads + (unit - row * a.hg_count) * NH,
@@ -723,7 +725,10 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 ends[0] = ends[1], ends[1] = ends[2], --n_ends;
             }
         cp_async_wait_all();
-        if (!ok && lane == 0) report(a.status, DSA_ERR_TIMEOUT);
+        if (!ok && lane == 0) {
+            report(a.status, DSA_ERR_TIMEOUT);
+            if constexpr (ROWS) atomicMin(reinterpret_cast<int*>(smem + L::kOffFault), done);
+        }
     } else if (warp == 5) {
         // ---- O^T += V^T P^T, issued by one elected lane ------------------------------------------------------
         const uint32_t idesc_o = idesc_bf16(NH, 1, 128);
@@ -1028,9 +1033,18 @@ __global__ void __launch_bounds__(kClThreads, 1)
 
     if constexpr (ROWS) {
         tc_fence_before();
-        __syncthreads();
+        const bool all_ok = __syncthreads_and(ok);
         tc_fence_after();
         if (warp == 0) tmem_dealloc(tmem, L::kTmemCols);
+        if (!all_ok)  // a wait ran out: zeros for every row that some widening warp has not stored
+            for (long long unit = unit0 + (long long)*s_fault * unit_step; unit < units; unit += unit_step) {
+                const int row = row_of((int)unit);
+                const long long first = (long long)row * a.heads + ((int)unit - row * a.hg_count) * NH;
+                for (int i = tid; i < NH * kD / 8; i += kClThreads)
+                    reinterpret_cast<uint4*>(a.out + first * kD)[i] = make_uint4(0, 0, 0, 0);
+                if (a.lse)
+                    for (int h = tid; h < NH; h += kClThreads) a.lse[first + h] = -INFINITY;
+            }
     } else {
         const int row = row_of(unit0);
         attn_finish<NH, L, false, kFp4Shift, true>(a, &omap, smem, tmem, tO, row, split, unit0 - row * a.hg_count, crank,

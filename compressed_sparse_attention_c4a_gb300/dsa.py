@@ -27,7 +27,8 @@ EXPORTS = ["dsa_status_string", "dsa_compress", "dsa_index_scores", "dsa_topk", 
            "dsa_sparse_attn_decode", "dsa_sparse_attn_prefill", "dsa_gather_rows", "dsa_sparse_attn_decode_static",
            "dsa_attn_static_scratch_bytes", "dsa_attn_plan", "dsa_debug_index_scores_stalled", "dsa_index_topk",
            "dsa_index_topk_workspace_size", "dsa_index_scores_counted", "dsa_topk_counted", "dsa_sparse_attn_q8",
-           "dsa_compress_jobs", "dsa_topk_sparse_attn_decode", "dsa_cache_write", "dsa_cache_read"]
+           "dsa_compress_jobs", "dsa_topk_sparse_attn_decode", "dsa_cache_write", "dsa_cache_read",
+           "dsa_debug_sparse_attn_stalled"]
 
 
 class DsaPool(ctypes.Structure):
@@ -92,6 +93,8 @@ for _name, _args in {
                                ctypes.c_size_t, _P, _P],
     "dsa_sparse_attn_prefill": [_I, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, ctypes.c_float, _P, _P, _P,
                                 _P, ctypes.c_size_t, _P, _P],
+    "dsa_debug_sparse_attn_stalled": [_I, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, ctypes.c_float, _P, _P, _P,
+                                      _P, ctypes.c_size_t, _I, _P, _P],
     "dsa_topk_sparse_attn_decode": [_I, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _I, ctypes.c_float, _P,
                                     _P, _P, _P, ctypes.c_size_t, _P, _P],
     "dsa_cache_write": [_I, _P, _P, _I, _P, _P, _P, _P, _P],
@@ -309,6 +312,20 @@ def dsa_sparse_attn_prefill(q, q_pos, q_req, kind, topk, k, main, main_bt, swa, 
                                         _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status),
                                         _stream(stream))
     _check("dsa_sparse_attn_prefill", code)
+
+
+def dsa_debug_sparse_attn_stalled(q, q_pos, q_req, kind, topk, k, main, main_bt, swa, swa_bt, window, sm_scale, rope_cfg, out,
+                                  stall_row, lse=None, workspace=None, dev_status=None, stream=None):
+    """Test hook: the attention (q_req None for decode rows) with one row's queries withheld, so that the bounded waits on
+    them expire (see include/dsa.h)."""
+    nq, H, _ = q.shape
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    code = _lib.dsa_debug_sparse_attn_stalled(nq, H, _ptr(q), _ptr(q_pos), _ptr(q_req), KIND.get(kind, kind), _ptr(topk),
+                                              int(k), ctypes.byref(main), ctypes.byref(main_bt), ctypes.byref(swa),
+                                              ctypes.byref(swa_bt), int(window), float(sm_scale), ctypes.byref(rope_cfg),
+                                              _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, int(stall_row),
+                                              _ptr(dev_status), _stream(stream))
+    _check("dsa_debug_sparse_attn_stalled", code)
 
 
 def dsa_sparse_attn_q8(q, q_pos, q_req, kind, topk, k, main, main_bt, swa, swa_bt, window, sm_scale, rope_cfg, out,

@@ -26,7 +26,8 @@
  *     DSA_ERR_DEVICE_FAULT a needed block is unmapped (-1) or outside the pool, a
  *                          position lies beyond its block table, or an index is out of
  *                          range; the affected row is written as zeros (scores: -inf)
- *     DSA_ERR_TIMEOUT      a bounded wait on an asynchronous copy or MMA expired
+ *     DSA_ERR_TIMEOUT      a bounded wait on an asynchronous copy or MMA expired; attention rows that it kept from being
+ *                          finished are written as zeros, lse -inf
  *   Kernels never trap or assert.
  * Paged caches ([P2] 设计 1; [P1] §2.2, §6.1).  A logical block always covers 256 raw
  *   token positions: 64 c4a entries, 2 c128a entries or 256 SWA tokens.  Compressed
@@ -451,6 +452,22 @@ dsa_status_t dsa_sparse_attn_decode_static(int32_t batch, int32_t heads, const v
 
 /* Size in bytes of the fixed scratch array that dsa_sparse_attn_decode_static uses (32 MiB). */
 size_t dsa_attn_static_scratch_bytes(void);
+
+/*
+ * dsa_debug_sparse_attn_stalled - test hook of the bounded waits in the attention calls; the pages have no counterpart.
+ * Launches the attention as dsa_sparse_attn_prefill would (q_req NULL: as dsa_sparse_attn_decode), except that the last CTA
+ * of each cluster that works on row stall_row never sees its query rows arrive: every wait that depends on them gives up
+ * after two seconds (of %globaltimer), the kernel records DSA_ERR_TIMEOUT and returns, with nothing in flight.  Row stall_row
+ * is written as zeros with lse -inf; over DSA_FP4_BLOCK rows so are the rows that the same CTA would have taken after it.
+ * 0 <= stall_row < nq (else DSA_ERR_INVALID_ARG).  Other arguments and checks as those calls.
+ */
+dsa_status_t dsa_debug_sparse_attn_stalled(int32_t nq, int32_t heads, const void* q, const int32_t* q_pos,
+                                           const int32_t* q_req, int32_t kind, const int32_t* topk, int32_t k,
+                                           const dsa_pool_t* main, const dsa_block_table_t* main_bt,
+                                           const dsa_pool_t* swa, const dsa_block_table_t* swa_bt, int32_t window,
+                                           float sm_scale, const dsa_rope_t* rope, void* out, float* lse,
+                                           void* workspace, size_t workspace_bytes, int32_t stall_row,
+                                           int32_t* dev_status, void* stream);
 
 /*
  * dsa_cache_write - store rows in a paged cache, in the pool's format.  [P1] §2.2 (logical rows through a request's

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from compressed_sparse_attention_c4a_gb300 import dsa
-from test_cache_fp4_block import D, F, S, _attn_case, _check, _expected, _on_gpu, _run
+from test_cache_fp4_block import D, F, S, SM, _attn_case, _check, _expected, _on_gpu, _pools, _run
 from _parity import np64
 
 gpu = pytest.mark.gpu
@@ -73,3 +73,50 @@ def test_workspace_size_of_the_longest_lengths():
         size = dsa.dsa_attn_workspace_size(rows, 64, 8320)
         for keys in (10 ** 6, 2 ** 31 - 2048, 2 ** 31 - 1):
             assert dsa.dsa_attn_workspace_size(rows, 64, keys) >= size
+
+
+# ---- waits that run out -------------------------------------------------------------------------------------------------
+def test_stalled_attention_refuses_a_row_outside_the_call():
+    import ctypes
+    P, f = ctypes.c_void_p, dsa._lib.dsa_debug_sparse_attn_stalled
+    bt, rope = dsa.DsaBlockTable(64, 2, 4), dsa.DsaRope(64, 10000.0)
+    main, swa = dsa.DsaPool(256, 512, 4, 64, 512, dsa.DSA_FP4_BLOCK), dsa.DsaPool(256, 512, 4, 256, 512, dsa.DSA_FP4_BLOCK)
+    for row in (-1, 2, 2 ** 31 - 1):
+        assert f(2, 64, P(16), P(16), None, 0, P(16), 8, ctypes.byref(main), ctypes.byref(bt), ctypes.byref(swa),
+                 ctypes.byref(bt), 128, 0.044, ctypes.byref(rope), P(16), None, None, 0, row, None, None) == \
+            dsa.DSA_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("fmt,rows,heads,topk", [("fp4_block", 400, 64, 150), ("fp4_block", 330, 16, 1), ("fp4_block", 3, 64, 200),
+                                                 ("fp4_block", 40, 64, 200), ("bf16", 3, 64, 500), ("bf16", 40, 64, 200),
+                                                 ("fp8", 200, 32, 100)])
+def test_rows_that_a_wait_kept_from_being_finished_are_zeros(fmt, rows, heads, topk):
+    """A row whose queries never arrive in its last CTAs: the waits run out after two seconds, the kernel returns and records
+    it, the row (of 4-bit rows taken one after another: and those that its CTA would have taken next) is zeros with lse -inf,
+    whole clusters and splits of keys included; every other row has the bits of a normal call, and so has the next call."""
+    spec = S("stalled", cached=[2500 + i for i in range(rows)], new=[1] * rows, heads=heads, topk=topk, window=100, seed=12,
+             main_dtype=fmt, swa_dtype=fmt)
+    case = _attn_case(spec, "random", seed=2)
+    dev = _on_gpu(case)
+    want, want_lse, status, ws = _run(case, dev)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and bool(torch.isfinite(want_lse).all())
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    _, cluster, splits, _ = dsa.dsa_attn_plan(rows, heads, topk + 100, fmt)
+    in_turn = fmt == "fp4_block" and cluster == 1 and splits == 1
+    stall = (sms + 3 if in_turn else rows // 2)
+    lost = list(range(stall, rows, sms)) if in_turn else [stall]
+    out, lse = torch.full_like(want, 7.0), torch.full_like(want_lse, 7.0)
+    main, bt, swa, sbt = _pools(case, dev)
+    dsa.dsa_debug_sparse_attn_stalled(dev["q"], dev["q_pos"], None, spec.kind, dev["topk"], topk, main, bt, swa, sbt, 100, SM,
+                                      dsa.rope(64), out, stall, lse, ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == dsa.DSA_ERR_TIMEOUT
+    keep = torch.ones(rows, dtype=torch.bool)
+    keep[lost] = False
+    assert not bool(out[lost].any()) and bool(torch.isneginf(lse[lost]).all())
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+    again, again_lse, status, _ = _run(case, dev)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and torch.equal(again, want) and torch.equal(again_lse, want_lse)
