@@ -946,7 +946,8 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
                                 const dsa_block_table_t* swa_bt, int32_t window, float sm_scale,
                                 const dsa_rope_t* rope, void* out, float* lse, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, void* stream, uint8_t* out8 = nullptr,
-                                float* out_scale = nullptr, const FusedTopk* fz = nullptr, int32_t stall_row = -1) {
+                                float* out_scale = nullptr, const FusedTopk* fz = nullptr, int32_t stall_row = -1,
+                                bool check_only = false) {
     if (rows < 0) return DSA_ERR_INVALID_ARG;
     if (rows == 0) return DSA_OK;
     if (kind != DSA_C4A && kind != DSA_C128A) return DSA_ERR_INVALID_ARG;
@@ -972,6 +973,7 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
     const SplitPlan p = plan_for(rows, heads, max_keys, main->dtype);
     const size_t need = workspace_bytes_for(rows, p, heads);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return DSA_ERR_INVALID_ARG;
+    if (check_only) return DSA_OK;
 
     AttnArgs a{};
     a.rows = rows;
@@ -1080,7 +1082,12 @@ extern "C" dsa_status_t dsa_topk_sparse_attn_decode(
     if (window < 1 || window > 1024) return DSA_ERR_INVALID_ARG;
     const SplitPlan p = plan_for(batch, heads, k + window, main->dtype);
     if (main->dtype == DSA_FP4_BLOCK || !fusable(p, heads, ld, k)) {  // two launches: the top-k, then the attention over its output
-        const dsa_status_t e = dsa_topk(batch, scores, ld, n_visible, k, topk_out, dev_status, stream);
+        // what the attention refuses is refused before the top-k has run
+        dsa_status_t e = sparse_attn(batch, heads, q, q_pos, nullptr, kind, topk_out, k, main, main_bt, swa, swa_bt, window,
+                                     sm_scale, rope, out, lse, workspace, workspace_bytes, dev_status, stream, nullptr,
+                                     nullptr, nullptr, -1, true);
+        if (e != DSA_OK) return e;
+        e = dsa_topk(batch, scores, ld, n_visible, k, topk_out, dev_status, stream);
         if (e != DSA_OK) return e;
         return sparse_attn(batch, heads, q, q_pos, nullptr, kind, topk_out, k, main, main_bt, swa, swa_bt, window,
                            sm_scale, rope, out, lse, workspace, workspace_bytes, dev_status, stream);

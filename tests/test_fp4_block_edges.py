@@ -120,3 +120,27 @@ def test_rows_that_a_wait_kept_from_being_finished_are_zeros(fmt, rows, heads, t
     again, again_lse, status, _ = _run(case, dev)
     torch.cuda.synchronize()
     assert int(status) == 0 and torch.equal(again, want) and torch.equal(again_lse, want_lse)
+
+
+# ---- refusals ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not memory: only where no launch can follow")
+@pytest.mark.parametrize("dtype", [dsa.DSA_FP4_BLOCK, dsa.DSA_BF16])
+def test_topk_and_attention_in_one_call_refuse_before_anything_is_launched(dtype):
+    """Where the call is two launches, what the attention refuses is refused before the top-k runs: nothing is launched and no
+    memory is touched (without a GPU a launch would answer DSA_ERR_CUDA instead)."""
+    import ctypes
+    P, f = ctypes.c_void_p, dsa._lib.dsa_topk_sparse_attn_decode
+    bt, rope = dsa.DsaBlockTable(64, 2, 64), dsa.DsaRope(64, 10000.0)
+    pool = lambda epb, dim=512, d=dtype: dsa.DsaPool(256, 512, 4, epb, dim, d)  # noqa: E731
+    assert dsa.dsa_attn_plan(1, 16, 512 + 128, dtype)[2] > 1                    # needs a workspace
+
+    def call(main=pool(64), swa=pool(256), q=P(16), out=P(16), sm=0.044, ws=P(256), ws_bytes=1 << 30):
+        return f(1, 16, q, P(16), 0, P(16), 4096, P(16), 512, P(16), ctypes.byref(main), ctypes.byref(bt), ctypes.byref(swa),
+                 ctypes.byref(bt), 128, sm, ctypes.byref(rope), out, None, ws, ws_bytes, None, None)
+
+    INV, UNS = dsa.DSA_ERR_INVALID_ARG, dsa.DSA_ERR_UNSUPPORTED
+    assert call(ws=None, ws_bytes=0) == INV and call(ws_bytes=16) == INV and call(ws=P(16)) == INV
+    assert call(q=None) == INV and call(q=P(8)) == INV and call(out=None) == INV and call(sm=0.0) == INV
+    assert call(swa=pool(128)) == INV and call(main=pool(64, dim=128)) == UNS
+    other = dsa.DSA_FP8_E4M3
+    assert call(swa=pool(256, d=other)) == UNS
