@@ -150,7 +150,7 @@ def pool(data, rows_per_block, scale=None, fmt=None):
 
 def block_table(table):
     """A DsaBlockTable over an int32 [batch][max_blocks] tensor."""
-    return DsaBlockTable(table.data_ptr(), *table.shape)
+    return DsaBlockTable(table.data_ptr(), table.shape[0], table.shape[1])
 
 
 def rope(rope_dim=64, theta=10000.0):

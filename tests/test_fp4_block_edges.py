@@ -144,3 +144,12 @@ def test_topk_and_attention_in_one_call_refuse_before_anything_is_launched(dtype
     assert call(swa=pool(128)) == INV and call(main=pool(64, dim=128)) == UNS
     other = dsa.DSA_FP8_E4M3
     assert call(swa=pool(256, d=other)) == UNS
+
+
+def test_binding_block_table_takes_the_first_two_sizes():
+    """A table may carry a trailing dimension of one; one dimension alone is no table."""
+    t = torch.zeros((3, 5, 1), dtype=torch.int32)
+    bt = dsa.block_table(t)
+    assert (bt.batch, bt.max_blocks, bt.table) == (3, 5, t.data_ptr())
+    with pytest.raises(IndexError):
+        dsa.block_table(torch.zeros(5, dtype=torch.int32))
