@@ -36,6 +36,12 @@ __device__ __forceinline__ void fp4_block_row_scale(uint32_t amax_bits, float* s
     if (amax_bits >= 0x7f800000u) *s = __uint_as_float(0x7fc00000u), *inv_s = 0.f;
 }
 
+// Eight codes with every zero as code 0, whatever its sign: 7 added to a code's magnitude carries into the sign's place
+// unless the magnitude is 0.
+__device__ __forceinline__ uint32_t fp4_plain_zeros(uint32_t c) {
+    return c & (((c & 0x77777777u) + 0x77777777u) | 0x77777777u);
+}
+
 // One block: its e4m3 scale (returned) and 16 codes (element 2j in the low nibble).  v / (s bs) is a reciprocal and one
 // correction step, which gives the quotient itself wherever that is representable (the borders are).
 __device__ __forceinline__ uint8_t fp4_block_codes(const float (&v)[kFp4Block], float block_amax, float inv_s,
@@ -57,6 +63,7 @@ __device__ __forceinline__ uint8_t fp4_block_codes(const float (&v)[kFp4Block], 
         }
         c[k / 4] |= (uint32_t)float2_to_e2m1x2(q[0], q[1]) << (8 * (k % 4));
     }
+    c[0] = fp4_plain_zeros(c[0]), c[1] = fp4_plain_zeros(c[1]);
     return bs8;
 }
 
@@ -105,6 +112,7 @@ __device__ __forceinline__ uint8_t fp4_block_codes_bf16(uint32_t (&u)[kFp4Block 
         c[k / 4] |= (uint32_t)float2_to_e2m1x2(__uint_as_float((uint32_t)t), __uint_as_float((uint32_t)(t >> 32)))
                     << (8 * (k % 4));
     }
+    c[0] = fp4_plain_zeros(c[0]), c[1] = fp4_plain_zeros(c[1]);
     return bs8;
 }
 

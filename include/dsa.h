@@ -66,8 +66,9 @@ typedef int32_t dsa_status_t;
                           fp32 scale per row: value_d = scale * e4m3(block d / 16) * e2m1(code_d).  Rows are quantised
                           with scale = the least power of two with amax <= 2688 * scale (at least 2^-126; 1 for a row of
                           zeros), block scale = e4m3(block amax / (6 * scale)), code = e2m1(x / (scale * block scale)),
-                          each to nearest even and saturating; a row with an infinity or a NaN is stored with scale NaN
-                          and zero codes, and reads back as NaN.  Block scales are finite and not negative */
+                          each to nearest even and saturating, a zero without a sign; a row with an infinity or a NaN
+                          is stored with scale NaN and zero codes, and reads back as NaN.  Block scales are finite and
+                          not negative */
 
 /* compressor kinds ([P1] §5.2, [P2] 机制二) */
 #define DSA_C4A 0   /* window 8 raw tokens, stride 4: 64 entries per block */

@@ -218,7 +218,8 @@ def fp4_block_quantize_rows(v):
     bs_codes = e4m3_encode(np.max(np.abs(blocks), axis=-1) / E2M1_MAX)
     bs = e4m3_decode(bs_codes)[..., None]
     q = np.divide(blocks, bs, out=np.zeros_like(blocks), where=bs > 0)
-    packed = fp4_pack(e2m1_encode(q).reshape(v.shape))
+    codes = e2m1_encode(q).reshape(v.shape)
+    packed = fp4_pack(np.where(codes == 8, 0, codes))  # a zero has no sign
     return np.concatenate([packed, bs_codes.astype(np.uint8)], axis=-1), s
 
 

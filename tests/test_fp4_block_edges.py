@@ -7,7 +7,10 @@ import pytest
 import torch
 
 from compressed_sparse_attention_c4a_gb300 import dsa
-from test_cache_fp4_block import D, F, S, SM, _attn_case, _check, _expected, _on_gpu, _pools, _run
+from compressed_sparse_attention_c4a_gb300 import synth
+from oracle import codecs
+from test_cache_fp4_block import (D, F, S, SM, _attn_case, _awkward_rows, _check, _expected, _on_gpu, _paged, _pools, _run,
+                                  _schedule)
 from _parity import np64
 
 gpu = pytest.mark.gpu
@@ -153,3 +156,54 @@ def test_binding_block_table_takes_the_first_two_sizes():
     assert (bt.batch, bt.max_blocks, bt.table) == (3, 5, t.data_ptr())
     with pytest.raises(IndexError):
         dsa.block_table(torch.zeros(5, dtype=torch.int32))
+
+
+# ---- the sign of a zero ---------------------------------------------------------------------------------------------------
+def _rows_around_zero(n, seed):
+    """bf16 rows with negative values that round to zero, negative zeros, and blocks whose scale rounds to zero."""
+    x = _awkward_rows(n, seed).float()
+    x[:, ::5] = -x[:, ::5].abs() * 2.0 ** -9
+    x[:, 1::7] = -0.0
+    x[:, 3::11] = -x[:, 3::11].abs() * 2.0 ** -24
+    x[1::2, 64:96] = -2.0 ** -120
+    return x.to(torch.bfloat16)
+
+
+def test_oracle_writes_zero_codes_without_a_sign():
+    data, _ = codecs.fp4_block_quantize_rows(np64(_rows_around_zero(24, 4)))
+    assert not ((data[:, :256] & 15) == 8).any() and not ((data[:, :256] >> 4) == 8).any()
+
+
+@gpu
+@pytest.mark.parametrize("n", [40, 10500])
+def test_stored_bytes_are_the_oracles_zero_codes_included(n):
+    """A row a warp and four rows a warp: every byte and scale equal the oracle's, where a code of magnitude zero is 0."""
+    x = _rows_around_zero(n, 6)
+    bt, blocks = _paged([n], [0], 64, 2)
+    gd, gs = torch.full((blocks * 64, 288), 17, dtype=torch.uint8, device="cuda"), torch.zeros(blocks * 64, device="cuda")
+    cu, start = _schedule([n], [0])
+    table = bt.cuda()
+    dsa.dsa_cache_write(cu.cuda(), start.cuda(), x.cuda(), dsa.pool(gd, 64, gs, fmt="fp4_block"), dsa.block_table(table))
+    torch.cuda.synchronize()
+    rows = (bt[0].long()[:, None] * 64 + torch.arange(64)).flatten()[:n].numpy()
+    want, ws = codecs.fp4_block_quantize_rows(np64(x))
+    assert np.array_equal(gd.cpu().numpy()[rows], want) and np.array_equal(np64(gs)[rows], ws)
+
+
+@gpu
+def test_compressor_stores_zero_codes_without_a_sign():
+    from compressed_sparse_attention_c4a_gb300.step import LayerStep
+    spec = S("zeros", cached=[1000, 6, 0], new=[1, 1, 40], queries="all", idx_heads=0, topk=0, seed=42, **F)
+    case = synth.make_case(spec, "cpu")
+    case["x_new"][:, ::3] = -case["x_new"][:, ::3].abs() * 2.0 ** -12
+    for k in ("main_data", "swa_data"):
+        case[k].zero_()                                     # what is not written holds no sign
+    dev = _on_gpu(case)
+    step = LayerStep(dev)
+    step.compress_main()
+    torch.cuda.synchronize()
+    assert int(step.status) == 0
+    for k in ("main_data", "swa_data"):
+        codes = dev[k].cpu().numpy()[:, :256]
+        assert (codes >> 4 > 8).any() and ((codes & 15) == 0).any()
+        assert not ((codes & 15) == 8).any() and not ((codes >> 4) == 8).any()
