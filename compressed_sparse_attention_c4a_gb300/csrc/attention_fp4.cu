@@ -327,6 +327,18 @@ __device__ __noinline__ void store_row(const RopeTable& rope, uint16_t* out_row,
     }
 }
 
+// Zeros for the rows of a CTA from its row number `done` on, lse -inf (a wait ran out).
+template <int NH>
+__device__ __noinline__ void zero_rows(const AttnArgs& a, int unit0, int unit_step, int units, int done) {
+    for (long long unit = unit0 + (long long)done * unit_step; unit < units; unit += unit_step) {
+        const long long first = unit * NH;  // a row's head groups follow one another
+        for (int i = threadIdx.x; i < NH * kD / 8; i += kClThreads)
+            reinterpret_cast<uint4*>(a.out + first * kD)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int h = threadIdx.x; h < NH; h += kClThreads) a.lse[first + h] = -INFINITY;
+    }
+}
+
 // The unit (query row, head group) that a CTA works on and its share of the row's tiles.
 struct Unit {
     int row, hg, r, m;
@@ -1036,15 +1048,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
         const bool all_ok = __syncthreads_and(ok);
         tc_fence_after();
         if (warp == 0) tmem_dealloc(tmem, L::kTmemCols);
-        if (!all_ok)  // a wait ran out: zeros for every row that some widening warp has not stored
-            for (long long unit = unit0 + (long long)*s_fault * unit_step; unit < units; unit += unit_step) {
-                const int row = row_of((int)unit);
-                const long long first = (long long)row * a.heads + ((int)unit - row * a.hg_count) * NH;
-                for (int i = tid; i < NH * kD / 8; i += kClThreads)
-                    reinterpret_cast<uint4*>(a.out + first * kD)[i] = make_uint4(0, 0, 0, 0);
-                if (a.lse)
-                    for (int h = tid; h < NH; h += kClThreads) a.lse[first + h] = -INFINITY;
-            }
+        if (!all_ok) zero_rows<NH>(a, unit0, unit_step, units, *s_fault);
     } else {
         const int row = row_of(unit0);
         attn_finish<NH, L, false, kFp4Shift, true>(a, &omap, smem, tmem, tO, row, split, unit0 - row * a.hg_count, crank,
