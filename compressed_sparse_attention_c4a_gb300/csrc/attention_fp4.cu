@@ -253,6 +253,14 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
+// The two bf16 values of a word added to two fp32 sums, without widening them first (widened by shifts 328 us for the prefill
+// below, 327 so; by a warp-level product with a matrix of ones 341).
+__device__ __forceinline__ void add_bf16x2(uint32_t w, float (&s)[2]) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+        : "+f"(s[0]), "+f"(s[1])
+        : "r"(w));
+}
+
 // O^T of the calling warp's quadrant times alpha per head (a rare step, kept out of the loops).
 template <int NH>
 __device__ __noinline__ void rescale_quadrant(uint32_t taddr, const float* alpha) {
@@ -847,9 +855,11 @@ __global__ void __launch_bounds__(kClThreads, 1)
         const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
         const int hr = lane >> 2, c = lane & 3, head0 = warp * 16 + hr;
         // m_run: the head's running maximum, lazy: it moves only when exceeded by more than 2^8, so O^T is rarely
-        // rescaled and exp2(s - m) <= 2^8.  l_run: the lane's share of the sum of the fp32 probabilities, two halves
+        // rescaled and exp2(s - m) <= 2^8.  l_run: the lane's share of the sum of the probabilities as rounded for P V (the
+        // output's normaliser: values that all keys share come out exactly), two halves; e_run: of the fp32 probabilities
+        // (the log-sum-exp).  The prefill below takes 327 us so, 318 with one sum of fp32 probabilities
         float m_run[2] = {-INFINITY, -INFINITY};
-        uint64_t l_run[2] = {0ull, 0ull};
+        uint64_t l_run[2] = {0ull, 0ull}, e_run[2] = {0ull, 0ull};
         bool seen = false;  // a fault bit in one of the row's masks
         int rows = 0;
         auto wait_pv = [&](int g) { return wait_bar(&pvdone[(2 * g + 1) % kFp4Ring], ((2 * g + 1) / kFp4Ring) & 1); };
@@ -881,7 +891,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
             const int info = s_info[4 * at];
             if (info & kFirst) {
                 m_run[0] = m_run[1] = -INFINITY;
-                l_run[0] = l_run[1] = 0ull;
+                l_run[0] = l_run[1] = e_run[0] = e_run[1] = 0ull;
                 seen = false;
             }
             float alpha[2] = {1.f, 1.f};
@@ -943,7 +953,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
                     }
                 }
             }
-            uint64_t sum[2] = {0ull, 0ull};
+            float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+            uint64_t esum[2] = {0ull, 0ull};
             const uint32_t prow = sP + b * L::kP + head0 * 128 + 4 * c;
 #pragma unroll
             for (int e = 0; e < kFp4Groups; ++e) {
@@ -952,8 +963,11 @@ __global__ void __launch_bounds__(kClThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint64_t p = pack_f32x2(ex2_sfu(sv[4 * e + 2 * h]), ex2_sfu(sv[4 * e + 2 * h + 1]));
-                    sum[h] = add_f32x2(sum[h], p);
-                    float p0, p1;  // the probability that multiplies the codes carries the row scale
+                    esum[h] = add_f32x2(esum[h], p);
+                    float p0, p1;
+                    unpack_f32x2(p, &p0, &p1);
+                    add_bf16x2(bf16x2_rn(p0, p1), sum[h]);
+                    // the probability that multiplies the codes carries the row scale: a power of two, so it rounds alike
                     unpack_f32x2(mul_f32x2(p, ks), &p0, &p1);
                     if (NH == 64 || head0 + 8 * h < NH)
                         asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + h * 1024 + ((e ^ (hr & 7)) << 4)),
@@ -962,7 +976,10 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 }
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) l_run[h] = fma_f32x2(l_run[h], pack_f32x2(alpha[h], alpha[h]), sum[h]);
+            for (int h = 0; h < 2; ++h) {
+                l_run[h] = fma_f32x2(l_run[h], pack_f32x2(alpha[h], alpha[h]), pack_f32x2(sum[h][0], sum[h][1]));
+                e_run[h] = fma_f32x2(e_run[h], pack_f32x2(alpha[h], alpha[h]), esum[h]);
+            }
             if (c == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -991,9 +1008,10 @@ __global__ void __launch_bounds__(kClThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int head = head0 + 8 * h;
-                    float l0, l1;
+                    float l0, l1, e0, e1;
                     unpack_f32x2(l_run[h], &l0, &l1);
-                    const float l = quad_sum(l0 + l1);
+                    unpack_f32x2(e_run[h], &e0, &e1);
+                    const float l = quad_sum(l0 + l1), e = quad_sum(e0 + e1);
                     if (c != 0 || (NH < 64 && head >= NH)) continue;
                     if constexpr (ROWS) {  // the output's factor, and the log-sum-exp
                         const bool some = !(l <= 0.f) && !fault;
@@ -1001,9 +1019,9 @@ __global__ void __launch_bounds__(kClThreads, 1)
                         const int row = row_of(unit);
                         if (a.lse)
                             a.lse[(long long)row * a.heads + (unit - row * a.hg_count) * NH + head] =
-                                some ? (m_run[h] + log2f(l)) / kLog2e : -INFINITY;
+                                some ? (m_run[h] + log2f(e)) / kLog2e : -INFINITY;
                     } else {  // read after the last product (their place is in the ring)
-                        l_run[h] = pack_f32x2(l, 0.f);
+                        l_run[h] = pack_f32x2(l, e);
                     }
                 }
                 if constexpr (ROWS) {
@@ -1025,14 +1043,14 @@ __global__ void __launch_bounds__(kClThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int head = head0 + 8 * h;
-                        float l, l1;
-                        unpack_f32x2(l_run[h], &l, &l1);
+                        float l, e;
+                        unpack_f32x2(l_run[h], &l, &e);
                         if (c == 0 && (NH == 64 || head < NH)) {
                             // a NaN among masked or absent maxima only: give the partial a weight, so that the NaN
                             // reaches the row
                             s_own[head] = m_run[h] == -INFINITY && l != l ? 0.f : m_run[h];
                             s_own[NH + head] = l;
-                            s_own[2 * NH + head] = l;
+                            s_own[2 * NH + head] = e;
                         }
                     }
                     if (tid == 0 && seen) *s_fault = 1;

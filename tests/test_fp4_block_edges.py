@@ -207,3 +207,52 @@ def test_compressor_stores_zero_codes_without_a_sign():
         codes = dev[k].cpu().numpy()[:, :256]
         assert (codes >> 4 > 8).any() and ((codes & 15) == 0).any()
         assert not ((codes & 15) == 8).any() and not ((codes >> 4) == 8).any()
+
+
+# ---- the normaliser ---------------------------------------------------------------------------------------------------------
+def _one_value_case(rows, heads):
+    """Every key holds 1 in dims 0 .. 255; one entry, in a row's second tile, also holds 1 in dim 256, the only dim of the
+    queries that is not zero: its logit is up to 7.9 powers of two above the others', within the lazy maximum's margin."""
+    spec = S("one_value", cached=[1000] * rows, new=[1] * rows, heads=heads, topk=64, window=1, seed=3, **F)
+    case = _attn_case(spec, "random", seed=1)
+    for k in ("main", "swa"):
+        case[k + "_data"][:] = 0
+        case[k + "_data"][:, :128] = 0x22                   # two codes of 1
+        case[k + "_data"][:, 256:] = 0x38                   # block scales of 1
+        case[k + "_scale"][:] = 1.0
+    tk = torch.full((rows, 64), -1, dtype=torch.int32)
+    tk[:, 0], tk[:, 60] = 3, 200
+    for j in range(rows):
+        case["main_data"][int(case["bt_main"][j, 200 // 64]) * 64 + 200 % 64, 128] = 0x02
+    case["topk"] = tk
+    x = torch.linspace(0.1, 7.9, rows * heads)[torch.randperm(rows * heads, generator=torch.Generator().manual_seed(5))]
+    q = torch.zeros((rows, heads, D))
+    q[:, :, 256] = (x / (SM * np.log2(np.e))).view(rows, heads)
+    case["q"] = q.to(torch.bfloat16)
+    return case
+
+
+@gpu
+@pytest.mark.parametrize("rows,heads", [(160, 64), (330, 16)])
+def test_weights_add_up_to_one_whatever_their_rounding(rows, heads):
+    """Values that all keys share come out exactly: the probabilities are rounded to bf16 before they multiply the values, and
+    the normaliser sums them as rounded.  In fp32 the three weights, their sum, its reciprocal and the product are off by a few
+    2^-24, far less than 2^-9, half a bf16 step below 1.  (Summed before the rounding they differ by up to 2^-8.)  In e4m3 the
+    value is 448 times the block's scale.  The log-sum-exp is that of the probabilities before the rounding."""
+    case = _one_value_case(rows, heads)
+    dev = _on_gpu(case)
+    out, lse, status, ws = _run(case, dev)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert dsa.dsa_attn_plan(rows, heads, 65, "fp4_block")[1:3] == (1, 1)       # a row in one CTA: nothing is exchanged
+    assert bool((out[:, :, :256] == 1.0).all())
+    want = _expected(case, range(0, rows, 40))
+    _check(out, lse, want)
+    main, bt, swa, sbt = _pools(case, dev)
+    o8 = torch.zeros((rows, heads, D), dtype=torch.uint8, device="cuda")
+    s8 = torch.zeros((rows, heads, 4), device="cuda")
+    dsa.dsa_sparse_attn_q8(dev["q"], dev["q_pos"], dev["q_req"], "c4a", dev["topk"], 64, main, bt, swa, sbt, 1, SM,
+                           dsa.rope(64), o8, s8, lse, workspace=ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and bool((o8[:, :, :256] == 0x7E).all())            # 448
+    assert bool(((s8[:, :, :2] * 448.0 - 1.0).abs() <= 2.0 ** -20).all())
