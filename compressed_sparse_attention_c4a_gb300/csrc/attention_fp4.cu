@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
             for (int e = 0; e < 3; ++e) {
                 const int kk = lane + 32 * e, t = (ROWS ? 0 : split * a.cps) + crank + (kk < kFp4Keys ? 0 : csize);
                 const int j = t * kFp4Keys + kk % kFp4Keys;
-                entry[e] = load_int_if(row_topk + j, a.topk && j < a.k);
+                entry[e] = load_int_if(row_topk + j, a.topk && j < a.k && DSA_IDX_OK(j, a.k, a.status));
             }
             int listed = a.k;
             if (ROWS && a.topk && tail < 0) {  // the list without the -1 it ends in, looked through from its end
@@ -555,12 +555,14 @@ __global__ void __launch_bounds__(kClThreads, 1)
                     const dsa_block_table_t& bt = window ? a.swa_bt : a.main_bt;
                     const int lb = max(id[e], 0) >> (window ? 8 : main_shift);
                     block[e] = load_int_if(bt.table + (long long)u.r * bt.max_blocks + lb,
-                                           id[e] >= 0 && (window || id[e] < u.n_vis) && lb < bt.max_blocks);
+                                           id[e] >= 0 && (window || id[e] < u.n_vis) && lb < bt.max_blocks &&
+                                               DSA_IDX_OK((long long)u.r * bt.max_blocks + lb,
+                                                          (long long)bt.batch * bt.max_blocks, a.status));
                 }
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
                     const int jn = key_index(i + 2, e);
-                    entry[e] = load_int_if(row_topk + max(jn, 0), a.topk && jn >= 0 && jn < u.n_comp);
+                    entry[e] = load_int_if(row_topk + max(jn, 0), a.topk && jn >= 0 && jn < u.n_comp && DSA_IDX_OK(jn, a.k, a.status));
                 }
                 float scale[3];
 #pragma unroll
@@ -571,6 +573,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
                     if (id[e] >= 0) {
                         if (block[e] < 0 || block[e] >= pool.num_blocks) bad |= 2u;
                         else row[e] = (block[e] << (window ? 8 : main_shift)) + (id[e] & (window ? 255 : (1 << main_shift) - 1));
+                        if (row[e] >= 0 && !DSA_IDX_OK(row[e], (long long)pool.num_blocks * pool.rows_per_block, a.status))
+                            row[e] = -1;
                     }
                     scale[e] = load_float_if(pool.scale + max(row[e], 0), row[e] >= 0);
                     valid[e] = __ballot_sync(0xffffffffu, row[e] >= 0);
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 const int at0 = g % kFp4Entries, at1 = (g + (put0 ? 1 : 0)) % kFp4Entries;
                 const bool mine = lane == 0 ? put0 : lane == 1 && put1;  // lanes 0 and 1 write a tile's entry
                 const int my_at = lane == 0 ? at0 : at1;
-                if (mine) {
+                if (mine && DSA_IDX_OK(my_at, kFp4Entries, a.status)) {
                     s_mask[my_at] = (lane == 0 ? mask0 : mask1) | (bad ? kFp4Fault : 0ull);
                     const bool last = i + lane + 1 == u.tiles;
                     s_info[4 * my_at] = (first && (lane == 0 || !put0) ? kFirst : 0) | (last ? kLast : 0) | (ord & 3) * kOdd |
@@ -595,16 +599,17 @@ __global__ void __launch_bounds__(kClThreads, 1)
                 }
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
-                    const int kk = lane + 32 * e;
-                    if (kk < kFp4Keys ? put0 : put1) s_addr[(kk < kFp4Keys ? at0 : at1) * kFp4Keys + kk % kFp4Keys] = addr[e];
+                    const int kk = lane + 32 * e, slot = (kk < kFp4Keys ? at0 : at1) * kFp4Keys + kk % kFp4Keys;
+                    if ((kk < kFp4Keys ? put0 : put1) && DSA_IDX_OK(slot, kFp4Entries * kFp4Keys, a.status)) s_addr[slot] = addr[e];
                 }
                 __syncwarp();
                 if (mine) mbar_arrive(&rfull[my_at]);
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
                     const int kk = lane + 32 * e, key = kk % kFp4Keys;
-                    if (kk < kFp4Keys ? put0 : put1) {
-                        float* k = s_ksc + (kk < kFp4Keys ? at0 : at1) * 2 * kFp4Keys + key / 2 * 4 + (key & 1);
+                    const int slot = (kk < kFp4Keys ? at0 : at1) * 2 * kFp4Keys + key / 2 * 4 + (key & 1);
+                    if ((kk < kFp4Keys ? put0 : put1) && DSA_IDX_OK(slot + 2, kFp4Entries * 2 * kFp4Keys, a.status)) {
+                        float* k = s_ksc + slot;
                         k[0] = scale[e];
                         k[2] = scale[e] * a.scale_log2;
                     }
@@ -635,7 +640,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
 #pragma unroll
             for (int n = 0; n < kCopies; ++n) {
                 const int p = lane + 32 * n, r = p / 18;
-                const uint64_t at = s_addr[g % kFp4Entries * kFp4Keys + ww * kFp4PerWarp + min(r, kFp4PerWarp - 1)];
+                const int key = g % kFp4Entries * kFp4Keys + ww * kFp4PerWarp + min(r, kFp4PerWarp - 1);
+                const uint64_t at = DSA_IDX_OK(key, kFp4Entries * kFp4Keys, a.status) ? s_addr[key] : 0ull;
                 src[n] = (at ? at : reinterpret_cast<uint64_t>(a.main.data)) + (p - 18 * r) * 16;
                 src_bytes[n] = at ? 16u : 0u;
             }
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(kClThreads, 1)
         auto copy = [&]() {
 #pragma unroll
             for (int n = 0; n < kCopies; ++n)
-                if (lane + 32 * n < kPieces)
+                if (lane + 32 * n < kPieces && DSA_IDX_OK(ww * kPieces + lane + 32 * n, kFp4Keys * 18, a.status))
                     cp_async16_nc(raw + (lane + 32 * n) * 16, reinterpret_cast<const void*>(src[n]), src_bytes[n]);
             cp_async_commit();
         };
@@ -717,9 +723,10 @@ __global__ void __launch_bounds__(kClThreads, 1)
                     for (int e = 0; e < 2; ++e) {
                         uint32_t o[4];
                         widen8((e != 0) != (hf != 0) ? code[0][u].y : code[0][u].x, s2, o);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (piece ^ (16u * e))), "r"(o[0]),
-                                     "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                     : "memory");
+                        if (DSA_IDX_OK(at + (piece ^ (16u * e)) - sK, kFp4Ring * kFp4Half - 15, a.status))
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (piece ^ (16u * e))), "r"(o[0]),
+                                         "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                         : "memory");
                     }
                 }
                 fence_proxy_async_smem();  // the bf16 rows -> visible to the tensor core (async proxy)
@@ -969,7 +976,8 @@ __global__ void __launch_bounds__(kClThreads, 1)
                     add_bf16x2(bf16x2_rn(p0, p1), sum[h]);
                     // the probability that multiplies the codes carries the row scale: a power of two, so it rounds alike
                     unpack_f32x2(mul_f32x2(p, ks), &p0, &p1);
-                    if (NH == 64 || head0 + 8 * h < NH)
+                    if ((NH == 64 || head0 + 8 * h < NH) &&
+                        DSA_IDX_OK(prow + h * 1024 + ((e ^ (hr & 7)) << 4) - sP, 2 * L::kP - 3, a.status))
                         asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + h * 1024 + ((e ^ (hr & 7)) << 4)),
                                      "r"(bf16x2_rn(p0, p1))
                                      : "memory");

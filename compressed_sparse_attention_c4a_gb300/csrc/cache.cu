@@ -55,7 +55,10 @@ __device__ __forceinline__ long long pool_row(const dsa_block_table_t& bt, int r
     return (long long)pb * pool.rows_per_block + (row - lb * (uint32_t)pool.rows_per_block);
 }
 
-// A warp takes R consecutive rows.  BLOCK: a pool of DSA_FP4_BLOCK, else any other.  The schedule and the block table are read before waiting for the preceding kernel.
+__device__ __forceinline__ long long pool_rows(const dsa_pool_t& p) { return (long long)p.num_blocks * p.rows_per_block; }
+
+// A warp takes R consecutive rows.  BLOCK: a pool of DSA_FP4_BLOCK, else any other.  The schedule and the block table are
+// read before waiting for the preceding kernel.
 template <int DIM, int R, bool BLOCK>
 __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(CacheWriteArgs a) {
     constexpr int E = DIM / 32;
@@ -76,7 +79,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(CacheWriteArgs
         }
         if (lane < live) {
             const long long row = (long long)__ldg(a.start_row + r) + (j0 + lane - __ldg(a.cu_new + r));
-            if (row >= 0) prow = pool_row(a.bt, r, (uint32_t)row, a.pool);
+            if (row >= 0 && DSA_IDX_OK(r, a.batch, a.status)) prow = pool_row(a.bt, r, (uint32_t)row, a.pool);
+            if (prow >= 0 && !DSA_IDX_OK(prow, pool_rows(a.pool), a.status)) prow = -1;
         }
     }
     pdl_wait();
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_write_kernel(CacheWriteArgs
     uint32_t u[R][E / 2];
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        if (i < live) load_bf16_words<E>(a.x + (j0 + i) * DIM, lane, u[i], a.wide);
+        if (i < live && DSA_IDX_OK(j0 + i, a.n, a.status)) load_bf16_words<E>(a.x + (j0 + i) * DIM, lane, u[i], a.wide);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const long long to = __shfl_sync(0xffffffffu, prow, i);
@@ -200,6 +204,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(CacheReadArgs a
         const int id = __ldg(a.ids + j0 + lane), r = __ldg(a.req + j0 + lane);
         if (id >= 0 && r >= 0 && r < a.bt.batch)
             prow = pool_row(a.bt, r, (uint32_t)id, a.pool);
+        if (prow >= 0 && !DSA_IDX_OK(prow, pool_rows(a.pool), a.status)) prow = -1;
         if (prow < 0 && id != -1) report(a.status, DSA_ERR_DEVICE_FAULT);
     }
     StoredRow<E> row[R];
