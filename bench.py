@@ -22,6 +22,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -38,7 +39,8 @@ METRIC = "c4a DSA decode query-tokens/s per layer"
 UNIT = "query-tokens/s"
 COPIES = 4
 KERNEL_SOURCES = {"index_kernel": "index_scores.cu", "attn_kernel": "attention.cu", "topk_kernel": "topk.cu",
-                  "compress_kernel": "compress.cu"}
+                  "compress_kernel": "compress.cu", "attn_fp4_kernel": "attention_fp4.cu", "cache_write_kernel": "cache.cu",
+                  "cache_read_kernel": "cache.cu"}
 
 
 def parse():
@@ -199,12 +201,24 @@ def peaks():
 
 
 def kernel_source_digest(kernel):
-    """sha256 (16 hex digits) of a kernel's source file followed by the headers every kernel includes, so that a
-    change in shared device code also marks the kernel's ncu summary as stale."""
+    """sha256 (16 hex digits) of a kernel's source file followed by the headers every kernel includes and every further
+    header of csrc that it includes, directly or through another, so that a change in shared device code also marks the
+    kernel's ncu summary as stale."""
     csrc = os.path.join(ROOT, "compressed_sparse_attention_c4a_gb300", "csrc")
+
+    def text(name):
+        return open(os.path.join(csrc, name), "rb").read()
+
+    names, todo = [KERNEL_SOURCES[kernel], "common.cuh", "topk_cluster.cuh"], [KERNEL_SOURCES[kernel]]
+    further = set()
+    while todo:
+        for inc in re.findall(r'^#include "([^"]+\.cuh)"', text(todo.pop()).decode(), re.M):
+            if inc not in names and inc not in further:
+                further.add(inc)
+                todo.append(inc)
     h = hashlib.sha256()
-    for name in (KERNEL_SOURCES[kernel], "common.cuh", "topk_cluster.cuh"):
-        h.update(open(os.path.join(csrc, name), "rb").read())
+    for name in names + sorted(further):
+        h.update(text(name))
     return h.hexdigest()[:16]
 
 
