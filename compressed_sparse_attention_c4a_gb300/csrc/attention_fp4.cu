@@ -1128,10 +1128,11 @@ int fp4_clusters(int cl) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
+    const bool clean = cudaPeekAtLastError() == cudaSuccess;
     if (cudaFuncSetAttribute(attn_fp4_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fp4Smem<64>::kAlloc) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, attn_fp4_kernel<64, false>, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
+        if (clean) cudaGetLastError();  // this question's own error, not one that the caller has not seen yet
         return sm_count() / cl;
     }
     if (seen) seen->store(n, std::memory_order_relaxed);
