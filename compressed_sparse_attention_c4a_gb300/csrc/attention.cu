@@ -783,10 +783,9 @@ __global__ void __launch_bounds__(kClThreads, 1)
     attn_finish<NH, L, FUSED>(a, &omap, smem, tmem, tO, row, split, hg, crank, csize, n_mine, ok);
 }
 
-// Split plans, shared by the workspace query and the launch: one cluster of `cl` CTAs per (row, head group, split)
-// over sub-tiles of 32 keys: clusters of 4
-// while four CTAs per row still fit on the GPU at once, then 2, then 1; a row splits further only when
-// its clusters leave SMs idle, and never below two sub-tiles per CTA.
+// Split plans, shared by the workspace query and the launch: one cluster of `cl` CTAs per (row, head group, split) over
+// sub-tiles of 32 keys: clusters of 4 while four CTAs per row still fit on the GPU at once, then 2, then 1; a row splits
+// further only when its clusters leave SMs idle, and never below two sub-tiles per CTA.
 struct SplitPlan {
     int hg, hg_count, nsplit, cps, cl;
 };
@@ -817,7 +816,8 @@ static SplitPlan plan_cluster(int rows, int heads, int max_keys) {
 // joining the parts in a second kernel, and a tenth of one for every part of 64 heads that is written and read there.
 // Measured, splits chosen against none (640 keys of 64 heads): 1 row 4 splits 13.0 us against 14.3, 4 rows 4 splits 13.2
 // against 14.9, 8 rows 2 splits 14.8 against 16.2, 12 rows none 15.8 against 16.3 with two; 1152 keys: 1 row 6 splits 13.6
-// against 18.6, 8 rows 3 splits 16.2 against 19.0.
+// against 18.6, 8 rows 3 splits 16.2 against 19.0.  Whole rows go to clusters and no split waits for a free SM, so long rows
+// are dealt out unevenly between these sizes: 19 rows of 8,320 keys give the busiest CTA 44 tiles where an even share is 22.
 static SplitPlan plan_fp4(int rows, int heads, int max_keys) {
     SplitPlan p;
     p.hg = heads >= 64 ? 64 : heads;

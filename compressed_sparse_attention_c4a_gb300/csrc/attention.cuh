@@ -12,7 +12,7 @@ constexpr int kD = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
-    int rows, heads, hg_count, nsplit, cps;   // cps = 32-key sub-tiles per split
+    int rows, heads, hg_count, nsplit, cps;   // cps = the kernel's key tiles per split
     const uint16_t* q;
     const int32_t* q_pos;
     const int32_t* q_req;                     // NULL: row r belongs to request r
@@ -130,8 +130,9 @@ __device__ __forceinline__ void attn_finish(const AttnArgs& a, const CUtensorMap
     uint8_t* xout = smem + L::kOffQ;
     uint8_t* xin = smem + L::kOffQ + 3 * L::kTile;
     if (csize > 1) {
-        // 1. the tiles other CTAs own, unscaled (the owner applies this CTA's factor), staged as bf16; only
-        // this CTA's own accumulators are needed, so no CTA waits for another here
+        // 1. the tiles other CTAs own, unscaled (the owner applies this CTA's factor), staged as bf16 (half the bytes of
+        // fp32, in shared memory as between the CTAs, for 2^-8 of each partial: a rounding like the output's own); only this
+        // CTA's own accumulators are needed, so no CTA waits for another here
         float v[4][G];  // static register indices; the sent tiles' columns in flight together
         if (have) {
 #pragma unroll

@@ -7,6 +7,8 @@
 //
 // A code times its block scale has at most 6 significant bits, so the rows are widened to bf16 exactly and both products
 // run on bf16 tensor cores; the row scale multiplies the key's logit and its probability (a power of two: no rounding).
+// Rounded to fewer than 32 bits: a probability for P V (bf16, as the tensor core takes it; the normaliser sums the rounded
+// ones, so a row's weights add up to one), a CTA's partial output when a cluster merges (attn_finish), and the output.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -38,7 +40,7 @@ namespace dsa {
 // The widened keys are a ring of five half-tiles (48 keys x 256 dims): S starts on the first half, P V frees it first.  Two
 // S and two P buffers.
 //
-// What bounds it (2048 rows of 640 keys, 64 heads: 317 us, a tile in about 2,700 cycles): shared memory is busy for 2,070
+// What bounds it (2048 rows of 640 keys, 64 heads: 327 us, a tile in about 2,800 cycles): shared memory is busy for 2,120
 // of them by its bytes alone (reads of S 896 and of P V 576, widened stores 384, P^T 48, the rows' copies and loads 216),
 // and a row's O^T is read out while its successor's products wait, about 5,000 cycles a row.  What else was measured on the
 // way, in us, each against the kernel of its time: one CTA a row 463 against 394; rows loaded straight into registers 446
@@ -48,8 +50,10 @@ namespace dsa {
 // with uniform ones); the rows fetched by a warp of its own, with bulk copies 509 (100 cycles a row), with cp.async 397;
 // tiles of 32 keys 416; a finished row stored as soon as its product is done, at any half-tile, 375 against 361; the copies
 // in halves, each when its half has been converted, 334 against 325; twelve widening warps of 4 keys 325 against 317.
-// A decode row's 16.5 us (32 rows of 640 keys, clusters of 4): 2.2 until the first keys are widened (position, block table,
-// rows, one load after the other), 6 for four tiles, 3 for the last tile's chain, 6 for the merge across the cluster.
+// A decode row's 31,000 cycles (32 rows of 640 keys, clusters of 4: 16.3 us): 7,000 until the first tile is widened (position,
+// block table, rows, one load after the other), 13,000 for four tiles (widening, S, softmax, P V, one after the other), 11,000
+// for the merge across the cluster.  The same rows in bf16, which need no widening, take 14.0 us, one row of 16 heads 11.0
+// against 11.8; 16 rows of 8,320 keys 52.7 against 51.4, the prefill above 405 against 328.
 constexpr int kFp4Ring = 5;                            // widened half-tiles
 constexpr int kFp4Half = kFp4Keys * (kD / 2) * 2;
 constexpr int kFp4Chunk = kFp4Keys * 128;              // bytes of a 64-dim chunk

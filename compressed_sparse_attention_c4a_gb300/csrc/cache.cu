@@ -11,13 +11,16 @@ namespace dsa {
 
 constexpr int kRowThreads = 256;  // 8 warps, a row each, or four in turn
 
-// What bounds both: HBM from about 30,000 rows on (1,316 or 1,324 bytes a row: 131,072 rows stored in 35.8 us, 4.8 TB/s, and
-// read in 35.5; 65,536 rows in 14.3 and 15.5), below that the chain of loads from the schedule to the row.  Storing takes
-// 200 instructions a row for a warp, reading 100.
+// What bounds both, from about 30,000 rows on: the rows in flight.  A warp requests nothing of its next rows before its own are
+// stored, and its waits for HBM lead the stalls (131,072 rows, 1,316 or 1,324 bytes each: stored in 36.5 us, 4.7 TB/s, and read
+// in 35.7, with DRAM 50 and 39 % busy and the issue slots 57 and 51 %; 65,536 rows 20.3 and 20.1).  Below that the chain of loads
+// from the schedule to the row.  Storing takes 200 instructions a row for a warp, reading 100.  The other formats, 131,072 rows
+// of 512 stored and read: bf16 51.8 and 44.4 us (floor 40.1), e4m3 56.9 and 36.7 (30.1), e2m1 53.8 and 35.2 (25.1); their stores
+// divide every element by the row scale.
 //
 // Rows per warp: four consecutive ones, whose addresses four lanes find side by side and whose loads are in flight
-// together, when there are enough rows for two blocks of such warps on every SM.  Measured, four against one, stored and
-// read: 131,072 rows 35.8 and 35.5 us against 38.0 and 44.3, 65,536 rows 14.3 and 15.5 against 18.4 and 18.6, 16,384 rows
+// together, when there are enough rows for two blocks of such warps on every SM.  Measured over one input again and again
+// (up to 65,536 rows it stays in the L2), four against one, stored and read: 131,072 rows 35.8 and 35.5 us against 38.0 and 44.3, 65,536 rows 14.3 and 15.5 against 18.4 and 18.6, 16,384 rows
 // 5.1 and 5.0 against 5.3 and 5.4; 8,192 rows level, 5,000 rows 2.9 and 3.6 against 2.5 and 3.4.
 static int rows_per_warp(long long n) { return n >= 2ll * 4 * 8 * sm_count() ? 4 : 1; }
 

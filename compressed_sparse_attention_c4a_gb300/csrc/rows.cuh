@@ -43,7 +43,8 @@ __device__ __forceinline__ uint32_t fp4_plain_zeros(uint32_t c) {
 }
 
 // One block: its e4m3 scale (returned) and 16 codes (element 2j in the low nibble).  v / (s bs) is a reciprocal and one
-// correction step, which gives the quotient itself wherever that is representable (the borders are).
+// correction by the quotient's remainder (Markstein's), which gives the quotient itself wherever that is representable (the
+// borders are).
 __device__ __forceinline__ uint8_t fp4_block_codes(const float (&v)[kFp4Block], float block_amax, float inv_s,
                                                    uint32_t (&c)[2]) {
     const float a = inv_s == 0.f ? 0.f : block_amax * inv_s;
@@ -86,7 +87,7 @@ __device__ __forceinline__ uint8_t fp4_block_codes_bf16(uint32_t (&u)[kFp4Block 
 #pragma unroll
         for (int k = 0; k < kFp4Block / 2; ++k) u[k] = 0u;
     }
-    const float a0 = a * (1.f / 6.f);  // and a correction, which makes it the quotient
+    const float a0 = a * (1.f / 6.f);  // and a correction by the remainder, which makes it the quotient
     const uint8_t bs8 = float_to_e4m3(fmaf(fmaf(-a0, 6.f, a), 1.f / 6.f, a0));
     const __half_raw h = __nv_cvt_fp8_to_halfraw(bs8, __NV_E4M3);
     const float bs = __half2float(*reinterpret_cast<const __half*>(&h));

@@ -68,7 +68,9 @@ typedef int32_t dsa_status_t;
                           zeros), block scale = e4m3(block amax / (6 * scale)), code = e2m1(x / (scale * block scale)),
                           each to nearest even and saturating, a zero without a sign; a row with an infinity or a NaN
                           is stored with scale NaN and zero codes, and reads back as NaN.  Block scales are finite and
-                          not negative */
+                          not negative.  A value is exact in bf16 while it lies in bf16's range: where scale * block
+                          scale is below 2^-129 its lowest bits may lie below 2^-133, and the three largest bf16
+                          magnitudes (above 2016 * 2^117) may round up to 2112 * 2^117, an infinity */
 
 /* compressor kinds ([P1] §5.2, [P2] 机制二) */
 #define DSA_C4A 0   /* window 8 raw tokens, stride 4: 64 entries per block */
@@ -351,7 +353,10 @@ dsa_status_t dsa_attn_plan(int32_t nq, int32_t heads, int32_t max_keys, int32_t 
  * topk       [batch][k] int32 logical entry ids (-1 = none) or NULL;  k host int <= 2048
  * main, swa  pools with dim 512, both bf16, both e4m3 or both DSA_FP4_BLOCK (whose rows are widened to bf16 exactly; rows
  *            whose largest value is below 2^-105 lose accuracy: a probability times such a row's scale leaves bf16's
- *            normal range);  window: host int, 1..1024
+ *            normal range).  Fewer bytes are not always less time: over DSA_FP4_BLOCK rows a decode of few short rows is
+ *            slower than over bf16 (32 rows of 640 keys, 64 heads: 16.9 us against 14.0; one row of 16 heads 11.8 against
+ *            11.0), many or long rows faster (16 rows of 8,320 keys 51.4 against 52.7, 2,048 prefill rows of 640 keys 328
+ *            against 405);  window: host int, 1..1024
  * sm_scale   host float (1/sqrt(512) in the layer)
  * out        [batch][heads][512] bf16;  lse [batch][heads] fp32 (natural log of the softmax
  *            denominator) or NULL
@@ -416,6 +421,8 @@ dsa_status_t dsa_topk_sparse_attn_decode(int32_t batch, int32_t heads, const voi
  *     out_scale[row][h][b] = max_{d in block b} |o_hd| / 448,   out[row][h][d] = e4m3(o_hd / out_scale[row][h][b])
  * where o is the output dsa_sparse_attn_decode would store in bf16 (R_m^-1 already applied), rounded to nearest
  * even with saturation.
+ * Over DSA_FP4_BLOCK rows, many rows take longer than with bf16 output (2,048 prefill rows of 640 keys, 64 heads: 514 us
+ * against 328): a block's largest value is known only when its whole tile is, so each row is a CTA of its own.
  * out        [nq][heads][512] e4m3 bytes, 16-byte aligned;  out_scale [nq][heads][4] fp32, 16-byte aligned
  * Other arguments, results, workspace and errors as dsa_sparse_attn_decode / _prefill (a faulted row: zero codes,
  * scales 1, lse -inf).
@@ -493,8 +500,8 @@ dsa_status_t dsa_cache_write(int32_t batch, const int32_t* cu_new, const int32_t
 
 /*
  * dsa_cache_read - rows of a paged cache as bf16 values (the values the attention computes with): out[j] = the value
- * of logical row ids[j] of request req[j], rounded to nearest even (DSA_FP4_BLOCK and bf16 rows are exact).  The same row may be
- * read any number of times.
+ * of logical row ids[j] of request req[j], rounded to nearest even (bf16 rows are exact, DSA_FP4_BLOCK rows within the range
+ * given there).  The same row may be read any number of times.
  * n          host int, >= 0 (0 is a no-op);  req, ids [n] int32;  id -1 (as dsa_topk pads): a row of zeros
  * out        [n][dim] bf16, 16-byte aligned
  * pool, bt   any format, dim 64, 128 or 512 (DSA_FP4_BLOCK: 512)

@@ -256,3 +256,39 @@ def test_weights_add_up_to_one_whatever_their_rounding(rows, heads):
     torch.cuda.synchronize()
     assert int(status) == 0 and bool((o8[:, :, :256] == 0x7E).all())            # 448
     assert bool(((s8[:, :, :2] * 448.0 - 1.0).abs() <= 2.0 ** -20).all())
+
+
+# ---- the ends of the range ------------------------------------------------------------------------------------------------
+@gpu
+def test_values_at_the_ends_of_the_range_read_back_rounded():
+    """Rows of the smallest scales, whose values' lowest bits lie below bf16's smallest subnormal: rounded to nearest even, and
+    exact where scale times block scale is at least 2^-129.  Rows of bf16's largest magnitudes: 2016 * 2^117 and below come
+    back finite, above it as infinities (2112 * 2^117 is beyond fp32)."""
+    g = np.random.default_rng(8)
+    n = 64
+    codes = g.integers(0, 256, (n, 256)).astype(np.uint8)
+    codes[(codes & 15) == 8] &= 0xF0
+    bs = np.where(g.random((n, 32)) < 0.5, g.integers(0, 16, (n, 32)), g.integers(0, 127, (n, 32))).astype(np.uint8)
+    data, scale = np.concatenate([codes, bs], 1), 2.0 ** g.integers(-126, -115, n)
+    bt = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    gd, gs = torch.tensor(data).cuda(), torch.tensor(scale, dtype=torch.float32).cuda()
+    ids = torch.arange(n, dtype=torch.int32, device="cuda")
+    out = torch.empty((n, D), dtype=torch.bfloat16, device="cuda")
+    pool = dsa.pool(gd, 64, gs, fmt="fp4_block")
+    dsa.dsa_cache_read(pool, dsa.block_table(bt), torch.zeros_like(ids), ids, out)
+    vals = codecs.fp4_block_dequantize_rows(data, scale)
+    assert torch.equal(out.cpu().float(), torch.tensor(vals).to(torch.float32).to(torch.bfloat16).float())
+    exact = np.repeat(scale[:, None] * codecs.e4m3_decode(bs) >= 2.0 ** -129, 16, axis=1)
+    assert exact.any() and not exact.all() and np.array_equal(np64(out)[exact], vals[exact])
+    assert not np.array_equal(np64(out), vals)
+    # the largest
+    tops = torch.tensor([0x7F7C, 0x7F7D, 0x7F7E, 0x7F7F], dtype=torch.int16).view(torch.bfloat16)   # 2016 2^117, then above
+    x = torch.zeros((4, D), dtype=torch.bfloat16)
+    x[:, 7] = tops
+    cu, start = _schedule([4], [0])
+    dsa.dsa_cache_write(cu.cuda(), start.cuda(), x.cuda(), pool, dsa.block_table(bt))
+    dsa.dsa_cache_read(pool, dsa.block_table(bt), torch.zeros_like(ids), ids, out)
+    got = out[:4].float().cpu()
+    assert float(got[0, 7]) == 1920 * 2.0 ** 117 and bool(torch.isinf(got[1:, 7]).all())
+    got[:, 7] = 0
+    assert not bool(got.any())
