@@ -34,3 +34,13 @@ def test_a_change_in_any_included_header_changes_the_digest(tmp_path, monkeypatc
             covered = n == src or n in reach(src, set()) or n in ("common.cuh", "topk_cluster.cuh")
             assert (bench.kernel_source_digest(k) != before[k]) == covered, (k, n)
         (root / CSRC / n).write_text(text[n])
+
+
+def test_every_kernel_summary_names_its_sources_digest():
+    """A summary without the line could never be told from a current one."""
+    folder = os.path.join(bench.ROOT, "profiles")
+    for name in sorted(os.listdir(folder)):
+        if any(name.startswith(k + "_") for k in bench.KERNEL_SOURCES):
+            lines = open(os.path.join(folder, name)).read().splitlines()
+            assert sum(line.startswith("source_sha256_16: ") for line in lines) == 1, name
+            assert sum(line.startswith("dram_bytes_per_launch: ") for line in lines) == 1, name
