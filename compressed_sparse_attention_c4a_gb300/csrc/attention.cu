@@ -783,6 +783,11 @@ __global__ void __launch_bounds__(kClThreads, 1)
     attn_finish<NH, L, FUSED>(a, &omap, smem, tmem, tO, row, split, hg, crank, csize, n_mine, ok);
 }
 
+// Entries under a block table, at most 2^30 (positions are 32-bit, so a request has fewer).
+static int table_entries(const dsa_block_table_t* bt, const dsa_pool_t* pool) {
+    return (int)std::min<long long>((long long)bt->max_blocks * pool->rows_per_block, 1ll << 30);
+}
+
 // Split plans, shared by the workspace query and the launch: one cluster of `cl` CTAs per (row, head group, split) over
 // sub-tiles of 32 keys: clusters of 4 while four CTAs per row still fit on the GPU at once, then 2, then 1; a row splits
 // further only when its clusters leave SMs idle, and never below two sub-tiles per CTA.
@@ -968,7 +973,7 @@ static dsa_status_t sparse_attn(int32_t rows, int32_t heads, const void* q, cons
         return DSA_ERR_INVALID_ARG;
     if (rope->rope_dim < 0 || rope->rope_dim > 64 || (rope->rope_dim & 1) || !(rope->theta > 0.0))
         return DSA_ERR_INVALID_ARG;
-    const int max_comp = topk ? k : main_bt->max_blocks * main->rows_per_block;
+    const int max_comp = topk ? k : table_entries(main_bt, main);
     const int max_keys = max_comp + window;
     const SplitPlan p = plan_for(rows, heads, max_keys, main->dtype);
     const size_t need = workspace_bytes_for(rows, p, heads);
@@ -1212,7 +1217,7 @@ extern "C" dsa_status_t dsa_sparse_attn_decode_static(int32_t batch, int32_t hea
     if (batch < 0 || !main || !main_bt || window < 1) return DSA_ERR_INVALID_ARG;
     if (batch == 0) return DSA_OK;
     if (heads != 16 && heads != 32 && heads != 64 && heads != 128) return DSA_ERR_UNSUPPORTED;
-    const int max_comp = topk ? k : main_bt->max_blocks * main->rows_per_block;
+    const int max_comp = topk ? k : table_entries(main_bt, main);
     const size_t need = workspace_bytes_for(batch, plan_for(batch, heads, max_comp + window, main->dtype), heads);
     if (need > kStaticScratchBytes) return DSA_ERR_UNSUPPORTED;  // beyond the fixed scratch: use the workspace call
     int st = DSA_OK;

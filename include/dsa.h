@@ -362,7 +362,7 @@ dsa_status_t dsa_attn_plan(int32_t nq, int32_t heads, int32_t max_keys, int32_t 
  *            denominator) or NULL
  * workspace  >= dsa_attn_workspace_size(batch, heads, max_keys) bytes, 256-byte aligned, or
  *            NULL when that size is 0; max_keys = (topk ? k : main_bt->max_blocks *
- *            main->rows_per_block) + window
+ *            main->rows_per_block, 2^30 at most) + window
  * Supported: dim 512, rope_dim <= 64.
  * Launched with programmatic dependent launch: q, q_pos (q_req) and both block tables are read before
  * waiting for the preceding kernel in the stream, so a preceding kernel that releases its dependents
@@ -493,7 +493,8 @@ dsa_status_t dsa_debug_sparse_attn_stalled(int32_t nq, int32_t heads, const void
  * A row whose logical row is unmapped or beyond the table is not written and raises DSA_ERR_DEVICE_FAULT; the others
  * are written.  Pool rows that no row of x maps to are left as they were.
  * Launched with programmatic dependent launch: cu_new, start_row and the block table are read before waiting for the
- * preceding kernel in the stream; x is read, and the pool written, only after it.
+ * preceding kernel in the stream, so a preceding kernel that releases its dependents early must not write them after
+ * releasing; x is read, and the pool written, only after the wait.
  */
 dsa_status_t dsa_cache_write(int32_t batch, const int32_t* cu_new, const int32_t* start_row, int32_t n, const void* x,
                              const dsa_pool_t* pool, const dsa_block_table_t* bt, int32_t* dev_status, void* stream);

@@ -292,3 +292,21 @@ def test_values_at_the_ends_of_the_range_read_back_rounded():
     assert float(got[0, 7]) == 1920 * 2.0 ** 117 and bool(torch.isinf(got[1:, 7]).all())
     got[:, 7] = 0
     assert not bool(got.any())
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not memory: only where no launch can follow")
+@pytest.mark.parametrize("dtype", [dsa.DSA_FP4_BLOCK, dsa.DSA_BF16])
+@pytest.mark.parametrize("max_blocks", [2 ** 25, 2 ** 26, 2 ** 31 - 1])
+def test_a_table_of_more_entries_than_an_int_holds_is_planned_as_a_long_one(dtype, max_blocks):
+    """Attention over every visible entry under a table of 2^31 entries or more: the plan is a long row's (its key splits need
+    a workspace, and without one the call is refused), not that of what is left of the product modulo 2^32, whose few tiles
+    would leave most keys out.  Without a GPU a launch would answer DSA_ERR_CUDA instead."""
+    import ctypes
+    P, rope = ctypes.c_void_p, dsa.DsaRope(64, 10000.0)
+    bt, swa_bt = dsa.DsaBlockTable(64, 2, max_blocks), dsa.DsaBlockTable(64, 2, 64)
+    main, swa = dsa.DsaPool(256, 512, 4, 64, 512, dtype), dsa.DsaPool(256, 512, 4, 256, 512, dtype)
+    assert dsa.dsa_attn_workspace_size(1, 64, 2 ** 30) > 0
+    got = dsa._lib.dsa_sparse_attn_decode(1, 64, P(16), P(16), 0, None, 0, ctypes.byref(main), ctypes.byref(bt),
+                                          ctypes.byref(swa), ctypes.byref(swa_bt), 128, 0.044, ctypes.byref(rope), P(16), None,
+                                          None, 0, None, None)
+    assert got == dsa.DSA_ERR_INVALID_ARG
