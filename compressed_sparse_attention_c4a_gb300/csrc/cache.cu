@@ -1,4 +1,5 @@
-// dsa_cache_write / dsa_cache_read: rows into a paged cache in its storage format, and back as values.
+// dsa_cache_write / dsa_cache_read: rows into a paged cache in its storage format, and back as values; dsa_cache_append:
+// rows normed and rotated by their positions on the way.
 //
 // [P1] "DeepSeek DSA、DeepSeek V4与vLLM Hybrid KV Cache详解" §2.2 (logical rows of a request through its block table),
 // [P2] "DeepSeek V4 稀疏注意力完全解剖" 设计 1 (256 raw positions per logical block) and 第三层 (prefill keeps the cache
@@ -237,6 +238,107 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(CacheReadArgs a
     }
 }
 
+// ---- dsa_cache_append ------------------------------------------------------------------------------------------------
+struct CacheAppendArgs {
+    int batch, n;
+    const int32_t* cu_new;
+    const int32_t* start_pos;
+    const uint16_t* x;
+    long long x_ld;
+    const float* gamma;
+    float eps;
+    RopeTable rope;
+    dsa_pool_t pool;
+    dsa_block_table_t bt;
+    int32_t* status;
+    bool wide;  // rows of x 32-byte aligned
+};
+
+// Rotates the pairs of the last rope_dim dims by R_pos.  A lane finds the angle of one pair, whatever lanes hold it: the
+// E / 2 pairs of a lane one after the other would leave the lanes without pairs idle (rows of 512: four lanes hold them all).
+template <int E>
+__device__ __forceinline__ void rotate_row(float (&v)[E], int lane, const RopeTable& rt, long long pos) {
+    const int pairs = rt.rope_dim / 2, first = E * 32 - rt.rope_dim;
+    float c = 1.f, s = 0.f;
+    if (lane < pairs) rope_cos_sin(pos, rt, lane, &c, &s);
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+        const int d = lane * E + k, j = (d - first) / 2;
+        const float cj = __shfl_sync(0xffffffffu, c, j & 31), sj = __shfl_sync(0xffffffffu, s, j & 31);
+        if (d >= first) {
+            const float x0 = v[k], x1 = v[k + 1];
+            v[k] = x0 * cj - x1 * sj;
+            v[k + 1] = x0 * sj + x1 * cj;
+        }
+    }
+}
+
+// A warp takes R consecutive rows, one after the other from the registers that their loads, in flight together, fill.
+template <int DIM, int R, bool NORM>
+__global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
+    constexpr int E = DIM / 32;
+    const int lane = threadIdx.x & 31;
+    const long long j0 = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * R;
+    const int total = min(a.n, __ldg(a.cu_new + a.batch));
+    const int live = (int)min((long long)R, total - j0);
+    long long prow = -1;  // lane i < live: of row j0 + i
+    long long pos = 0;
+    if (live > 0) {
+        int r = request_of(a.cu_new, a.batch, (int)j0, lane);
+        if constexpr (R > 1) {
+            const int last = request_of(a.cu_new, a.batch, (int)j0 + live - 1, lane);
+            for (int hi = last + 1; hi - r > 1;) {  // between the two
+                const int mid = (r + hi) / 2;
+                if (__ldg(a.cu_new + mid) <= j0 + lane) r = mid;
+                else hi = mid;
+            }
+        }
+        if (lane < live) {
+            const int start = __ldg(a.start_pos + r);
+            pos = (long long)start + (j0 + lane - __ldg(a.cu_new + r));
+            if (start >= 0 && pos >= 0 && DSA_IDX_OK(r, a.batch, a.status)) prow = pool_row(a.bt, r, (uint32_t)pos, a.pool);
+            if (prow >= 0 && !DSA_IDX_OK(prow, pool_rows(a.pool), a.status)) prow = -1;
+        }
+    }
+    float g[E];
+    if constexpr (NORM) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) g[k] = a.gamma ? __ldg(a.gamma + lane * E + k) : 1.f;
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (live <= 0) return;
+    if (lane < live && prow < 0) report(a.status, DSA_ERR_DEVICE_FAULT);
+    uint32_t u[R][E / 2];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < live && DSA_IDX_OK(j0 + i, a.n, a.status)) load_bf16_words<E>(a.x + (j0 + i) * a.x_ld, lane, u[i], a.wide);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const long long to = __shfl_sync(0xffffffffu, prow, i), at = __shfl_sync(0xffffffffu, pos, i);
+        if (i >= live || to < 0) continue;
+        float v[E];
+        bf16_words<E>(u[i], v);
+        if constexpr (NORM) {
+            float ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < E; ++k) ss = fmaf(v[k], v[k], ss);
+            const float rs = rsqrtf(warp_sum(ss) / (float)DIM + a.eps);
+#pragma unroll
+            for (int k = 0; k < E; ++k) v[k] *= rs * g[k];
+        }
+        rotate_row<E>(v, lane, a.rope, at);
+        store_row<E>(a.pool, to, lane, v);
+    }
+}
+
+template <int DIM, bool NORM>
+static cudaError_t launch_append(const CacheAppendArgs& a, cudaStream_t st) {
+    const bool four = rows_per_warp(a.n) == 4;
+    const dim3 grid((unsigned)((a.n + (four ? 31ll : 7ll)) / (four ? 32 : 8))), block(kRowThreads);
+    return launch_pdl(four ? cache_append_kernel<DIM, 4, NORM> : cache_append_kernel<DIM, 1, NORM>, grid, block, 0, st, a);
+}
+
 static dsa_status_t check_rows(const dsa_pool_t* pool, const dsa_block_table_t* bt) {
     if (!pool_ok(pool) || !bt || !bt->table || bt->max_blocks <= 0 || bt->batch <= 0) return DSA_ERR_INVALID_ARG;
     if (pool->dim != 64 && pool->dim != 128 && pool->dim != 512) return DSA_ERR_UNSUPPORTED;
@@ -287,6 +389,30 @@ extern "C" dsa_status_t dsa_cache_read(const dsa_pool_t* pool, const dsa_block_t
         pool->dim == 64    ? launch_pdl(four ? cache_read_kernel<64, 4> : cache_read_kernel<64, 1>, grid, block, 0, st, a)
         : pool->dim == 128 ? launch_pdl(four ? cache_read_kernel<128, 4> : cache_read_kernel<128, 1>, grid, block, 0, st, a)
                            : launch_pdl(four ? cache_read_kernel<512, 4> : cache_read_kernel<512, 1>, grid, block, 0, st, a);
+    if (err != cudaSuccess) return DSA_ERR_CUDA;
+    return launch_status();
+}
+
+extern "C" dsa_status_t dsa_cache_append(int32_t batch, const int32_t* cu_new, const int32_t* start_pos, int32_t n,
+                                         const void* x, int64_t x_ld, int32_t norm, const float* rms_gamma, float rms_eps,
+                                         const dsa_rope_t* rope, const dsa_pool_t* pool, const dsa_block_table_t* bt,
+                                         int32_t* dev_status, void* stream) {
+    if (batch < 0 || n < 0) return DSA_ERR_INVALID_ARG;
+    if (batch == 0 || n == 0) return DSA_OK;
+    const dsa_status_t e = check_rows(pool, bt);
+    if (e != DSA_OK) return e;
+    if (!cu_new || !start_pos || !x || !aligned(x, 16) || x_ld % 8 || x_ld < pool->dim || x_ld >= (1ll << 40) ||
+        bt->batch < batch || !rope || rope->rope_dim < 0 || rope->rope_dim > pool->dim || (rope->rope_dim & 1) ||
+        !(rope->theta > 0.0) || (norm && !(rms_eps > 0.f)) || !aligned(rms_gamma, 4))
+        return DSA_ERR_INVALID_ARG;
+    if (rope->rope_dim > 64) return DSA_ERR_UNSUPPORTED;  // the frequency table holds 32 pairs
+    const CacheAppendArgs a{batch,   n,    cu_new, start_pos,  static_cast<const uint16_t*>(x),
+                            x_ld,    rms_gamma, rms_eps, make_rope_table(rope->rope_dim, rope->theta),
+                            *pool,   *bt,  dev_status, aligned(x, 32) && x_ld % 16 == 0};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t err = pool->dim == 64    ? norm ? launch_append<64, true>(a, st) : launch_append<64, false>(a, st)
+                            : pool->dim == 128 ? norm ? launch_append<128, true>(a, st) : launch_append<128, false>(a, st)
+                                               : norm ? launch_append<512, true>(a, st) : launch_append<512, false>(a, st);
     if (err != cudaSuccess) return DSA_ERR_CUDA;
     return launch_status();
 }

@@ -18,7 +18,7 @@ if not os.path.exists(_PATH):
 _lib = ctypes.CDLL(_PATH)
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE_FAULT, DSA_ERR_TIMEOUT = range(6)
-DSA_BF16, DSA_FP8_E4M3, DSA_FP4_E2M1, DSA_FP4_BLOCK = 0, 1, 2, 3
+DSA_BF16, DSA_FP8_E4M3, DSA_FP4_E2M1, DSA_FP4_BLOCK, DSA_FP32 = 0, 1, 2, 3, 4
 DSA_C4A, DSA_C128A = 0, 1
 KIND = {"c4a": DSA_C4A, "c128a": DSA_C128A}
 ATTN_DTYPE = {"bf16": DSA_BF16, "fp8": DSA_FP8_E4M3, "fp4_block": DSA_FP4_BLOCK}
@@ -28,7 +28,8 @@ EXPORTS = ["dsa_status_string", "dsa_compress", "dsa_index_scores", "dsa_topk", 
            "dsa_attn_static_scratch_bytes", "dsa_attn_plan", "dsa_debug_index_scores_stalled", "dsa_index_topk",
            "dsa_index_topk_workspace_size", "dsa_index_scores_counted", "dsa_topk_counted", "dsa_sparse_attn_q8",
            "dsa_compress_jobs", "dsa_topk_sparse_attn_decode", "dsa_cache_write", "dsa_cache_read",
-           "dsa_debug_sparse_attn_stalled"]
+           "dsa_debug_sparse_attn_stalled", "dsa_cache_append", "dsa_norm_q8", "dsa_gemm_q8", "dsa_gemm_q8_plan",
+           "dsa_debug_gemm_q8_stalled"]
 
 
 class DsaPool(ctypes.Structure):
@@ -66,6 +67,7 @@ class DsaError(RuntimeError):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _lib.dsa_status_string.restype = ctypes.c_char_p
 _lib.dsa_status_string.argtypes = [_I]
 _lib.dsa_attn_workspace_size.restype = ctypes.c_size_t
@@ -76,6 +78,8 @@ _lib.dsa_attn_plan.restype = ctypes.c_int32
 _lib.dsa_attn_plan.argtypes = [_I, _I, _I, _I, _P]
 _lib.dsa_index_topk_workspace_size.restype = ctypes.c_size_t
 _lib.dsa_index_topk_workspace_size.argtypes = [_I]
+_lib.dsa_gemm_q8_plan.restype = ctypes.c_int32
+_lib.dsa_gemm_q8_plan.argtypes = [_I, _I, _I, _I, _P]
 _lib.dsa_topk_plan.restype = ctypes.c_int32
 _lib.dsa_topk_plan.argtypes = [_I, _I, _I, _P]
 for _name, _args in {
@@ -98,6 +102,10 @@ for _name, _args in {
     "dsa_topk_sparse_attn_decode": [_I, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _I, ctypes.c_float, _P,
                                     _P, _P, _P, ctypes.c_size_t, _P, _P],
     "dsa_cache_write": [_I, _P, _P, _I, _P, _P, _P, _P, _P],
+    "dsa_cache_append": [_I, _P, _P, _I, _P, _L, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P],
+    "dsa_norm_q8": [_I, _I, _P, _L, _P, _L, _P, ctypes.c_float, _P, _L, _P, _P, _P],
+    "dsa_gemm_q8": [_I, _I, _I, _I, _P, _L, _P, _L, _P, _P, _I, _P, _L, _P, _P, _P],
+    "dsa_debug_gemm_q8_stalled": [_I, _I, _I, _I, _P, _L, _P, _L, _P, _P, _I, _P, _L, _P, ctypes.c_uint64, _P, _P],
     "dsa_cache_read": [_P, _P, _I, _P, _P, _P, _P, _P],
     "dsa_gather_rows": [_P, _P, _I, _P, _P, _P, _P, _P, _P],
     "dsa_sparse_attn_q8": [_I, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, ctypes.c_float, _P, _P, _P, _P, _P,
@@ -122,6 +130,22 @@ def _stream(stream):
 def _check(fn, code):
     if code != DSA_OK:
         raise DsaError(fn, code)
+
+
+def _want(fn, ok):
+    """What the C call cannot see (types, strides, devices of the tensors) is refused as it refuses an argument."""
+    if not ok:
+        raise DsaError(fn, DSA_ERR_INVALID_ARG)
+
+
+def _dense(t, *shape):
+    return tuple(t.shape) == shape and t.is_contiguous()
+
+
+def _here(*tensors):
+    """Every tensor (or None) on the current CUDA device, whose stream the call takes."""
+    dev = torch.cuda.current_device()
+    return all(t is None or t.get_device() == dev for t in tensors)
 
 
 def dsa_status_string(code):
@@ -354,6 +378,105 @@ def dsa_cache_read(pool_, bt, req, ids, out, dev_status=None, stream=None):
     code = _lib.dsa_cache_read(ctypes.byref(pool_), ctypes.byref(bt), ids.numel(), _ptr(req), _ptr(ids), _ptr(out),
                                _ptr(dev_status), _stream(stream))
     _check("dsa_cache_read", code)
+
+
+def dsa_cache_append(cu_new, start_pos, x, rope_cfg, pool_, bt, norm=False, rms_gamma=None, rms_eps=1e-6,
+                     dev_status=None, stream=None):
+    """Rows of x (bf16 [n][dim], rows any stride apart; request r's at cu_new[r] .. cu_new[r + 1]) normed where `norm`
+    says so, rotated by their positions start_pos[r] + 0, 1, .. and stored at those logical rows, in the pool's format
+    (see include/dsa.h)."""
+    fn = "dsa_cache_append"
+    _want(fn, x.dim() == 2 and x.dtype == torch.bfloat16 and x.shape[1] == pool_.dim and (x.numel() == 0 or x.stride(1) == 1))
+    _want(fn, cu_new.dtype == torch.int32 and start_pos.dtype == torch.int32 and _dense(start_pos, start_pos.numel())
+          and _dense(cu_new, start_pos.numel() + 1))
+    _want(fn, rms_gamma is None or (rms_gamma.dtype == torch.float32 and _dense(rms_gamma, pool_.dim)))
+    _want(fn, _here(cu_new, start_pos, x, rms_gamma, dev_status))
+    ld = x.stride(0) if x.shape[0] > 1 else pool_.dim
+    code = _lib.dsa_cache_append(start_pos.numel(), _ptr(cu_new), _ptr(start_pos), x.shape[0], _ptr(x), ld,
+                                 1 if norm else 0, _ptr(rms_gamma), float(rms_eps), ctypes.byref(rope_cfg),
+                                 ctypes.byref(pool_), ctypes.byref(bt), _ptr(dev_status), _stream(stream))
+    _check(fn, code)
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def dsa_norm_q8(x, gamma, eps, out, out_scale, residual=None, sum_out=None, stream=None):
+    """out, out_scale (uint8 [n][dim], fp32 [n][ceil(dim / 128)]) = the 8-bit rows of gamma * h / sqrt(mean(h^2) + eps),
+    h = x + residual; sum_out = h in bf16 (it may be x or residual).  x, residual, sum_out: bf16 [n][dim], rows any stride
+    apart; gamma None: ones (see include/dsa.h)."""
+    fn = "dsa_norm_q8"
+    _want(fn, x.dim() == 2)
+    n, dim = x.shape
+    for t in (x, residual, sum_out):
+        _want(fn, t is None or (tuple(t.shape) == (n, dim) and t.dtype == torch.bfloat16
+                                and (t.numel() == 0 or t.stride(1) == 1)))
+    _want(fn, gamma is None or (gamma.dtype == torch.float32 and _dense(gamma, dim)))
+    _want(fn, out.element_size() == 1 and _dense(out, n, dim))
+    _want(fn, out_scale.dtype == torch.float32 and _dense(out_scale, n, -(-dim // 128)))
+    _want(fn, _here(x, residual, sum_out, gamma, out, out_scale))
+    code = _lib.dsa_norm_q8(n, dim, _ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
+                            _ptr(gamma), float(eps), _ptr(sum_out), 0 if sum_out is None else _row_stride(sum_out), _ptr(out),
+                            _ptr(out_scale), _stream(stream))
+    _check(fn, code)
+
+
+def _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale, dev_status):
+    """The C arguments of a product: a [m][k] or [m][groups][k] (rows any stride apart), w [n][k] or [groups][n][k]."""
+    if a.dim() == 2:
+        a, out = a.unsqueeze(1), out.unsqueeze(1)
+        a_scale = a_scale.unsqueeze(1)
+        out_scale = None if out_scale is None else out_scale.unsqueeze(1)
+    if w.dim() == 2:
+        w, w_scale = w.unsqueeze(0), w_scale.unsqueeze(0)
+    _want(fn, a.dim() == 3 and w.dim() == 3 and out.dim() == 3 and a_scale.dim() == 3)
+    m, groups, k = a.shape
+    n = w.shape[1]
+    nkb, nnb = -(-k // 128), -(-n // 128)
+
+    def rows(t, cols):  # [m][groups][cols], the last two dense
+        return (tuple(t.shape) == (m, groups, cols)
+                and (t.numel() == 0 or ((cols == 1 or t.stride(2) == 1) and (groups == 1 or t.stride(1) == cols))))
+
+    def ld(t, cols):
+        return t.stride(0) if m > 1 else groups * cols
+
+    _want(fn, a.element_size() == 1 and w.element_size() == 1 and rows(a, k) and _dense(w, groups, n, k))
+    _want(fn, a_scale.dtype == torch.float32 and rows(a_scale, nkb))
+    _want(fn, w_scale.dtype == torch.float32 and _dense(w_scale, groups, nnb, nkb))
+    fmt = {torch.float32: DSA_FP32, torch.bfloat16: DSA_BF16, torch.uint8: DSA_FP8_E4M3,
+           torch.float8_e4m3fn: DSA_FP8_E4M3}.get(out.dtype)
+    _want(fn, fmt is not None and rows(out, n))
+    _want(fn, fmt != DSA_FP8_E4M3 or (out_scale is not None and out_scale.dtype == torch.float32
+                                      and _dense(out_scale, m, groups, nnb)))
+    _want(fn, _here(a, a_scale, w, w_scale, out, out_scale, dev_status))
+    return [m, n, k, groups, _ptr(a), ld(a, k), _ptr(a_scale), ld(a_scale, nkb), _ptr(w), _ptr(w_scale), fmt, _ptr(out),
+            ld(out, n), _ptr(out_scale) if fmt == DSA_FP8_E4M3 else None]
+
+
+def dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale=None, dev_status=None, stream=None):
+    """out[i][g] = w[g] a[i][g] for 8-bit rows a (uint8 [m][groups][k], a_scale fp32 [m][groups][ceil(k / 128)]) and weights
+    w (uint8 [groups][n][k], w_scale fp32 [groups][ceil(n / 128)][ceil(k / 128)]), into out [m][groups][n] in fp32, bf16 or
+    (uint8, with out_scale [m][groups][ceil(n / 128)]) 8-bit rows.  One group: the dimension may be left out everywhere.
+    (See include/dsa.h.)"""
+    args = _gemm_q8_args("dsa_gemm_q8", a, a_scale, w, w_scale, out, out_scale, dev_status)
+    _check("dsa_gemm_q8", _lib.dsa_gemm_q8(*args, _ptr(dev_status), _stream(stream)))
+
+
+def dsa_debug_gemm_q8_stalled(a, a_scale, w, w_scale, out, wait_limit_ns, out_scale=None, dev_status=None, stream=None):
+    """Test hook: the product's launch with every copy withheld, so that its bounded waits run out after ``wait_limit_ns``
+    (see include/dsa.h)."""
+    args = _gemm_q8_args("dsa_debug_gemm_q8_stalled", a, a_scale, w, w_scale, out, out_scale, dev_status)
+    _check("dsa_debug_gemm_q8_stalled", _lib.dsa_debug_gemm_q8_stalled(*args, int(wait_limit_ns), _ptr(dev_status),
+                                                                       _stream(stream)))
+
+
+def dsa_gemm_q8_plan(m, n, k, groups=1):
+    """(outputs of a tile, rows of a tile, CTAs that share it) of the product."""
+    plan = (ctypes.c_int32 * 3)()
+    _check("dsa_gemm_q8_plan", _lib.dsa_gemm_q8_plan(int(m), int(n), int(k), int(groups), plan))
+    return tuple(int(v) for v in plan)
 
 
 def dsa_gather_rows(pool_, bt, req, ids, out, out_scale=None, dev_status=None, stream=None):

@@ -72,6 +72,8 @@ typedef int32_t dsa_status_t;
                           scale is below 2^-129 its lowest bits may lie below 2^-133, and the three largest bf16
                           magnitudes (above 2016 * 2^117) may round up to 2112 * 2^117, an infinity */
 
+#define DSA_FP32 4 /* fp32 values (outputs of dsa_gemm_q8 only; no pool has them) */
+
 /* compressor kinds ([P1] §5.2, [P2] 机制二) */
 #define DSA_C4A 0   /* window 8 raw tokens, stride 4: 64 entries per block */
 #define DSA_C128A 1 /* window 128, stride 128: 2 entries per block */
@@ -511,6 +513,109 @@ dsa_status_t dsa_cache_write(int32_t batch, const int32_t* cu_new, const int32_t
  */
 dsa_status_t dsa_cache_read(const dsa_pool_t* pool, const dsa_block_table_t* bt, int32_t n, const int32_t* req,
                             const int32_t* ids, void* out, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_cache_append - new rows normed, rotated by their positions and stored in a paged cache, in one pass.  [P2] 融合点 3
+ * (the uncompressed keys: RoPE, then insert; the norm beside it), [P1] §2.2 (logical rows through a block table): the window
+ * rows of a layer whose raw rows come from a projection, with or without a compressor beside it.  Row j of x, of the request r with
+ * cu_new[r] <= j < cu_new[r+1], is the row of position p = start_pos[r] + j - cu_new[r]:
+ *     v = norm ? rms_gamma * x / sqrt(mean(x^2) + rms_eps) : x,    logical row p of request r = R_p v
+ * in the pool's format.  Without the norm the stored bytes are those of dsa_compress's window insert.
+ *
+ * batch      requests (host int, >= 0);  cu_new [batch + 1] int32, cu_new[0] = 0, non-decreasing
+ * start_pos  [batch] int32 >= 0
+ * n          host int: rows that x holds; rows of x from cu_new[batch] on are ignored.  batch or n 0 is a no-op
+ * x          n rows of dim bf16, x_ld elements apart (x_ld >= dim, a multiple of 8), 16-byte aligned
+ * norm       0 or 1;  rms_gamma [dim] fp32 or NULL (ones), rms_eps > 0: both ignored without the norm
+ * rope       rope_dim even, <= min(dim, 64) (0: no rotation)
+ * pool, bt   any format (as dsa_cache_write), dim 64, 128 or 512 (DSA_FP4_BLOCK: 512); pool->rows_per_block logical rows a
+ *            block (256: a window cache, one row per position);  bt->batch >= batch
+ * The rows a call writes must be distinct: two requests that map to one physical row race on it.  x must not overlap the pool.
+ * A row whose position is negative, unmapped or beyond the table is not written and raises DSA_ERR_DEVICE_FAULT; the others
+ * are written.  Pool rows that no row of x maps to are left as they were.
+ * Launched with programmatic dependent launch: cu_new, start_pos, rms_gamma and the block table are read before waiting for the
+ * preceding kernel in the stream, so a preceding kernel that releases its dependents early must not write them after
+ * releasing; x is read, and the pool written, only after the wait.
+ */
+dsa_status_t dsa_cache_append(int32_t batch, const int32_t* cu_new, const int32_t* start_pos, int32_t n, const void* x,
+                              int64_t x_ld, int32_t norm, const float* rms_gamma, float rms_eps, const dsa_rope_t* rope,
+                              const dsa_pool_t* pool, const dsa_block_table_t* bt, int32_t* dev_status, void* stream);
+
+/*
+ * 8-bit rows, as dsa_norm_q8 and dsa_gemm_q8 write them and dsa_gemm_q8 reads them: e4m3 codes and one fp32 scale for each
+ * block of 128 consecutive values (the last block of a row may be shorter),
+ *     scale_b = max(max |v| of the block / 448, 2^-126)  (1 for a block of zeros),    code_d = e4m3(v_d / scale_{d / 128}),
+ * rounded to nearest even.  A NaN keeps a NaN code and does not count in the maximum; a block with an infinity has an infinite
+ * scale, zero codes for its finite values and NaN codes for its infinities.  dsa_sparse_attn_q8's output is such rows of
+ * heads * 512 values.
+ */
+
+/*
+ * dsa_norm_q8 - the residual's addition, the RMS norm and the 8-bit rows that a projection reads, in one pass.  [P2] 融合点 1
+ * and 第四层 (the norm fused with its neighbours, intermediate data not read back), 融合点 2 (fp8 rows for the product that
+ * follows).  For each of n rows of dim values:
+ *     h = x + residual (h = x without one),   v = gamma * h / sqrt(mean(h^2) + eps),   out, out_scale = the 8-bit row of v
+ * in fp32 (h is not rounded before the norm); sum receives h rounded to bf16.
+ *
+ * n          rows (host int, >= 0; 0 is a no-op);  dim a multiple of 16, <= 16,384
+ * x, residual, sum   bf16, 16-byte aligned, rows *_ld elements apart (>= dim, a multiple of 8); residual and sum may be NULL
+ *            (their ld is ignored).  sum may be x or residual itself (with the same ld), and must not overlap them otherwise
+ * gamma      [dim] fp32, 16-byte aligned, or NULL (ones);  eps > 0
+ * out        [n][dim] e4m3 bytes, 16-byte aligned;  out_scale [n][ceil(dim / 128)] fp32
+ * A row that holds a NaN is NaN codes throughout; one that holds an infinity has NaN there and zeros elsewhere.
+ * Launched with programmatic dependent launch: gamma is read before waiting for the preceding kernel in the stream, x and
+ * residual only after it.
+ */
+dsa_status_t dsa_norm_q8(int32_t n, int32_t dim, const void* x, int64_t x_ld, const void* residual, int64_t residual_ld,
+                         const float* gamma, float eps, void* sum, int64_t sum_ld, uint8_t* out, float* out_scale,
+                         void* stream);
+
+/*
+ * dsa_gemm_q8 - the projections around the attention: products of 8-bit rows with 8-bit weights, scaled by blocks of 128, one
+ * matrix per group.  [P2] 全景图 (query and window projections before the attention, the output projection after it),
+ * 融合点 2 (the attention's fp8 output into a batched product).  For row i < m, group g < groups, output j < n:
+ *     out[i][g][j] = sum_kk a_scale[i][g][kk / 128] * w_scale[g][j / 128][kk / 128] * e4m3(a[i][g][kk]) * e4m3(w[g][j][kk])
+ * Sums in fp32: within a block of 128 on the tensor cores, each block's sum times its two scales (their product rounded to
+ * fp32) added in fp32.
+ *
+ * m          rows (host int, >= 0; 0 is a no-op);  n >= 1;  k a multiple of 16 (the last block may be shorter);  groups >= 1;
+ *            n * k < 2^40
+ * a          row i, group g at a + i * a_ld + g * k: e4m3 bytes, 16-byte aligned, a_ld >= groups * k a multiple of 16
+ * a_scale    row i, group g at a_scale + i * a_scale_ld + g * ceil(k / 128), fp32;  a_scale_ld >= groups * ceil(k / 128).
+ *            The rows of dsa_norm_q8 (groups 1), of dsa_sparse_attn_q8 (k = heads / groups * 512) or of another product
+ *            (k = its n, a multiple of 128) are such rows, with a_ld = groups * k and a_scale_ld = groups * ceil(k / 128)
+ * w          [groups][n][k] e4m3 bytes, 16-byte aligned;  w_scale [groups][ceil(n / 128)][ceil(k / 128)] fp32
+ * out_format DSA_FP32, DSA_BF16 or DSA_FP8_E4M3 (8-bit rows of n values for each row and group)
+ * out        row i, group g at element i * out_ld + g * n, out_ld >= groups * n, aligned to an element
+ * out_scale  [m][groups][ceil(n / 128)] fp32 (DSA_FP8_E4M3; else ignored)
+ * The result does not depend on timing: it is the same, bit for bit, whenever the same call is made again on a GPU of the same
+ * size.  An output that an expired bounded wait kept from being finished is 0 (DSA_ERR_TIMEOUT).
+ * Launched with programmatic dependent launch: w and w_scale are read before waiting for the preceding kernel in the stream,
+ * so a preceding kernel that releases its dependents early must not write them after releasing (no kernel of this library
+ * does); a and a_scale are read, and outputs written, only after the wait.  out and out_scale must not overlap an input.
+ */
+dsa_status_t dsa_gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, const uint8_t* a, int64_t a_ld,
+                         const float* a_scale, int64_t a_scale_ld, const uint8_t* w, const float* w_scale,
+                         int32_t out_format, void* out, int64_t out_ld, float* out_scale, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_gemm_q8_plan - how dsa_gemm_q8 splits the work for these sizes on the current device; host only, launches nothing.
+ * plan[0] = outputs of a tile, plan[1] = rows of a tile, plan[2] = CTAs of a cluster that share a tile (its blocks along k, or
+ * two halves of its outputs).  Returns DSA_ERR_INVALID_ARG / DSA_ERR_UNSUPPORTED as dsa_gemm_q8 would for these sizes (and
+ * DSA_ERR_INVALID_ARG for m = 0).
+ */
+dsa_status_t dsa_gemm_q8_plan(int32_t m, int32_t n, int32_t k, int32_t groups, int32_t* plan);
+
+/*
+ * dsa_debug_gemm_q8_stalled - test hook of the bounded waits in dsa_gemm_q8; the pages have no counterpart.  The launch that
+ * dsa_gemm_q8 would make, with every copy withheld: each wait for them gives up after wait_limit_ns nanoseconds (of
+ * %globaltimer), the kernel records DSA_ERR_TIMEOUT in dev_status, writes zeros and returns, with nothing in flight.
+ * wait_limit_ns: 1 .. 2e9 (else DSA_ERR_INVALID_ARG).  Other arguments and checks as dsa_gemm_q8.
+ */
+dsa_status_t dsa_debug_gemm_q8_stalled(int32_t m, int32_t n, int32_t k, int32_t groups, const uint8_t* a, int64_t a_ld,
+                                       const float* a_scale, int64_t a_scale_ld, const uint8_t* w, const float* w_scale,
+                                       int32_t out_format, void* out, int64_t out_ld, float* out_scale,
+                                       uint64_t wait_limit_ns, int32_t* dev_status, void* stream);
 
 /*
  * dsa_gather_rows - copy the stored bytes of n logical rows, exactly as the attention
