@@ -30,7 +30,7 @@ struct GemmArgs {
     long long out_ld;  // elements between rows
     float* out_scale;
     int format;
-    int vec;           // four consecutive outputs may be stored at once
+    int vec;           // 1: four consecutive outputs may be stored at once, 2: 16 bytes
     int splits;        // CTAs of a cluster that share a tile's blocks
     int tiles_n, tiles_m;
     int stages;
@@ -320,14 +320,340 @@ __global__ void __launch_bounds__(kFewThreads) gemm_q8_few_kernel(const __grid_c
     if (warp == 1) tmem_dealloc(tmem, NA * BN < 32 ? 32 : NA * BN);
 }
 
+// ---- many rows -------------------------------------------------------------------------------------------------------
+// Tile: 256 rows of a x 256 outputs, by a pair of CTAs whose tensor cores work as one (cta_group::2): each CTA copies its 128
+// rows of a and its 128 weight rows, the even one issues the products, and each has its rows' sums over all 256 outputs in its
+// TMEM, two accumulators of 256 columns in turn.  Pairs go from tile to tile; the products of the next tile's first two blocks
+// run while a tile is stored.
+//
+// Warp 0: copies; warp 1: products (even CTA); warps 2, 3 only fill the warpgroup; warps 4-11: sums, four for each half of the
+// outputs, a thread holding a row's 128 sums and reading one scale a block.
+constexpr int kWideThreads = 384;
+constexpr int kWideStages = 6;
+constexpr uint32_t kWideStage = 2 * 128 * 128;             // the CTA's rows of a, then its weight rows
+constexpr int kBandRows = 8;                               // row tiles that pass over the weights together
+constexpr int kWideSmem = 1024 + kWideStages * (int)kWideStage + 2 * kChunk * 256 * 4 + 512;
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives at the barrier in the pair's CTAs of `mask` once the products issued so far are complete.
+__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t mask = 3) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+// Only TMEM has been read before it, which has ended: no release at cluster scope, whose fence took most of the kernel's time.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Four bytes global -> shared, zero if !in; and the wait for all of the thread's but the last group.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// After tmem_wait_ld(): no use of the registers is scheduled before the wait.
+__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+// acc (two sums) += p (two products) * s (twice the same scale)
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t p0, uint32_t p1, uint64_t s) {
+    asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}" : "+l"(acc) : "r"(p0), "r"(p1), "l"(s));
+}
+
+struct WideTile {
+    int g, n0, m0;  // group, first output, first row
+};
+// Tile t: bands of kBandRows row tiles; within a band all outputs, the band's row tiles next to one another.
+__device__ __forceinline__ WideTile wide_tile(const GemmArgs& a, int t) {
+    const int per_group = a.tiles_m * a.tiles_n, g = t / per_group;
+    t -= g * per_group;
+    const int band = t / (kBandRows * a.tiles_n), first = band * kBandRows;
+    const int high = min(kBandRows, a.tiles_m - first);
+    t -= band * kBandRows * a.tiles_n;
+    return WideTile{g, (t / high) * 256, (first + t % high) * 256};
+}
+
+// 128 outputs of a row from a thread's sums, `left` of them within the matrix.
+__device__ __forceinline__ void store_half_row(const GemmArgs& a, long long row, int g, int j0, const float (&v)[128]) {
+    const int left = min(128, a.n - j0);
+    const long long at = row * a.out_ld + (long long)g * a.n + j0;
+    if (a.format == kOutQ8) {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 128; ++j) amax = fmaxf(amax, j < left ? fabsf(v[j]) : 0.f);
+        const float scale = block_scale8(amax);
+        const BlockQuotient q(scale);
+        a.out_scale[(row * a.groups + g) * a.nnb + j0 / 128] = scale;
+        uint8_t* to = static_cast<uint8_t*>(a.out) + at;
+#pragma unroll
+        for (int j = 0; j < 128; j += 16) {
+            uint32_t c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                c[e] = e4m3x4(q(v[j + 4 * e]), q(v[j + 4 * e + 1]), q(v[j + 4 * e + 2]), q(v[j + 4 * e + 3]));
+            if (a.vec == 2 && j + 16 <= left) {
+                *reinterpret_cast<uint4*>(to + j) = make_uint4(c[0], c[1], c[2], c[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (j + e < left) to[j + e] = (uint8_t)(c[e / 4] >> (8 * (e % 4)));
+            }
+        }
+    } else if (a.format == kOutBf16) {
+        uint16_t* to = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+        for (int j = 0; j < 128; j += 8) {
+            uint32_t c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = bf16x2(v[j + 2 * e], v[j + 2 * e + 1]);
+            if (a.vec == 2 && j + 8 <= left) {
+                *reinterpret_cast<uint4*>(to + j) = make_uint4(c[0], c[1], c[2], c[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (j + e < left) to[j + e] = (uint16_t)(c[e / 2] >> (16 * (e % 2)));
+            }
+        }
+    } else {
+        float* to = static_cast<float*>(a.out) + at;
+#pragma unroll
+        for (int j = 0; j < 128; j += 4) {
+            if (a.vec == 2 && j + 4 <= left) {
+                *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < left) to[j + e] = v[j + e];
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                       const __grid_constant__ CUtensorMap amap,
+                                                                       const __grid_constant__ GemmArgs a) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    float* scales = reinterpret_cast<float*>(base + kWideStages * kWideStage);  // [2][kChunk][256], a thread's own
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + 2 * kChunk * 256);      // the even CTA's: both CTAs' copies
+    uint64_t* empty = full + kWideStages;
+    uint64_t* acc_full = empty + kWideStages;
+    uint64_t* acc_empty = acc_full + 2;  // the even CTA's: both CTAs' warps
+    uint64_t* drained = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pairs = (int)(gridDim.x / 2), pair = (int)(blockIdx.x / 2);
+    const int tiles = a.groups * a.tiles_m * a.tiles_n;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWideStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 16);
+        }
+        mbar_init(drained, 1);
+        *stop = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 0 && lane == 0 && !a.withhold) {
+            int s = 0;
+            uint32_t ph = 1;
+            bool live = true;
+            for (int t = pair; t < tiles && live; t += pairs) {
+                const WideTile x = wide_tile(a, t);
+                const int row = x.m0 + 128 * (int)rank, feat = x.n0 + 128 * (int)rank;
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    if (!wait_or_stop(&empty[s], ph, stop, a)) {
+                        live = false;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(base) + s * kWideStage, bar = mapa_shared(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kWideStage);
+                    tma_load_3d_pair(st, &amap, kb * 128, x.g, row, bar);
+                    tma_load_3d_pair(st + 128 * 128, &wmap, kb * 128, feat, x.g, bar);
+                    if (++s == kWideStages) s = 0, ph ^= 1;
+                }
+            }
+            // every stage is read before the CTA ends (a stage never filled passes at once)
+            for (int i = 0; i < kWideStages && live; ++i) {
+                live = wait_or_stop(&empty[s], ph, stop, a);
+                if (++s == kWideStages) s = 0, ph ^= 1;
+            }
+        } else if (warp == 1 && rank == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(256, 256);
+            int s = 0, b = 0;
+            uint32_t ph = 0, aph = 1;
+            bool live = true;
+            for (int t = pair; t < tiles && live; t += pairs) {
+                for (int kb = 0; kb < a.nkb; ++kb) {
+                    const bool ok = wait_or_stop(&acc_empty[b], aph, stop, a) && wait_or_stop(&full[s], ph, stop, a);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        live = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(base) + s * kWideStage;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f8_pair_elect(tmem + b * 256, rows128_desc(st + ks * 32), rows128_desc(st + 128 * 128 + ks * 32),
+                                          idesc, ks > 0 ? 1u : 0u);
+                    mma_commit_pair_elect(&empty[s]);
+                    mma_commit_pair_elect(&acc_full[b]);
+                    if (++s == kWideStages) s = 0, ph ^= 1;
+                    b ^= 1;
+                    aph ^= b == 0 ? 1u : 0u;
+                }
+            }
+            mma_commit_pair_elect(drained, 1);
+            mbar_wait_bounded(drained, 0, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t8 = threadIdx.x - 128, half = (warp - 4) >> 2;
+        const int mine = 128 * (int)rank + 32 * (warp & 3) + lane;  // the thread's row of the tile
+        const uint32_t column = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
+        const uint32_t drained_to[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
+        // the row's scales, kChunk blocks ahead: into the thread's own places, so that only it waits for them
+        const uint32_t own = smem_u32(scales + t8);
+        int turn = 0;
+        const auto fetch = [&](int t, int kb) {
+            const WideTile x = wide_tile(a, t < tiles ? t : 0);
+            const int row = x.m0 + mine;
+            const float* sa = a.a_scale + (long long)(row < a.m ? row : 0) * a.a_scale_ld + (long long)x.g * a.nkb;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                const bool in = t < tiles && row < a.m && kb + i < a.nkb;
+                cp_async4(own + ((turn * kChunk + i) * 256) * 4, sa + (in ? kb + i : 0), in);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            turn ^= 1;
+        };
+        int b = 0;
+        uint32_t aph = 0;
+        bool live = true;
+        fetch(pair, 0);
+        for (int t = pair; t < tiles; t += pairs) {
+            const WideTile x = wide_tile(a, t);
+            const float* sw = a.w_scale + ((long long)x.g * a.nnb + min(x.n0 / 128 + half, a.nnb - 1)) * a.nkb;
+            uint64_t acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0ull;
+            for (int kb = 0; kb < a.nkb && live; ++kb) {
+                if (kb % kChunk == 0) {
+                    const bool more = kb + kChunk < a.nkb;
+                    fetch(more ? t : t + pairs, more ? kb + kChunk : 0);
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                }
+                const float ws = __ldg(sw + kb);
+                live = __all_sync(0xffffffffu, wait_or_stop(&acc_full[b], aph, stop, a));
+                if (!live) break;
+                tc_fence_after();
+                // `turn` is where the next fetch goes, which is where the last one but one went: the current scales
+                const float f = scales[(turn * kChunk + kb % kChunk) * 256 + t8] * ws;
+                uint64_t f2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[32];
+                    tmem_ld32_nowait(column + b * 256 + 32 * c, p);
+                    tmem_wait_ld();
+                    regs_after_wait(p);
+                    if (c == 3) {
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive_cluster(drained_to[b]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], p[2 * j], p[2 * j + 1], f2);
+                }
+                b ^= 1;
+                aph ^= b == 0 ? 1u : 0u;
+            }
+            const long long row = x.m0 + mine;
+            if (row < a.m && x.n0 + 128 * half < a.n) {
+                float v[128];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[j]));
+                    if (!live) v[2 * j] = v[2 * j + 1] = 0.f;  // a wait expired: this tile and the ones after it are zeros
+                }
+                store_half_row(a, row, x.g, x.n0 + 128 * half, v);
+            }
+        }
+    }
+    if (*stop) {  // copies that the other CTA asked for may still be on their way: they take microseconds
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 2000000ull) {}
+    }
+    tc_fence_before();
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
 // ---- host ----------------------------------------------------------------------------------------------------------
 struct GemmPlan {
+    int feat;    // outputs of a tile: 128, or 256 by a pair of CTAs
     int rows;    // rows of a in a tile
-    int splits;  // CTAs that share a tile's blocks of k
+    int splits;  // CTAs that share a tile: its blocks of k, or (a pair) its rows
 };
 
 static GemmPlan plan_gemm(int m, int n, int k, int groups) {
     GemmPlan p{};
+    p.feat = kFeat;
+    if ((long long)groups * ((m + 255) / 256) * ((n + 255) / 256) >= sm_count() / 2) return GemmPlan{256, 256, 2};
     p.rows = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
     const long long tiles = (long long)groups * row_blocks(n) * ((m + p.rows - 1) / p.rows);
     const int nkb = row_blocks(k);
@@ -367,6 +693,18 @@ static dsa_status_t launch_few(const CUtensorMap& wmap, const CUtensorMap& amap,
     return launch_status();
 }
 
+static dsa_status_t launch_wide(const CUtensorMap& wmap, const CUtensorMap& amap, GemmArgs a, cudaStream_t st) {
+    const long long tiles = (long long)a.groups * a.tiles_n * a.tiles_m;
+    if (tiles > 0x3fffffff) return DSA_ERR_UNSUPPORTED;
+    if (cudaFuncSetAttribute(gemm_q8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    const long long pairs = std::min<long long>(tiles, sm_count() / 2);
+    if (launch_pdl_cluster(gemm_q8_wide_kernel, dim3((unsigned)(2 * pairs)), dim3(kWideThreads), kWideSmem, st, 2, wmap, amap,
+                           a) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    return launch_status();
+}
+
 static dsa_status_t check_gemm(int32_t m, int32_t n, int32_t k, int32_t groups) {
     if (m < 0 || n <= 0 || k <= 0 || groups <= 0) return DSA_ERR_INVALID_ARG;
     if (k % 16 || (long long)n * k >= (1ll << 40) || n > 0x7fffff00 || k > 0x7fffff00 || m > 0x7fffff00)
@@ -396,14 +734,16 @@ static dsa_status_t gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, con
     args.m = m, args.n = n, args.k = k, args.groups = groups, args.nkb = nkb, args.nnb = nnb;
     args.a_scale = a_scale, args.a_scale_ld = a_scale_ld, args.w_scale = w_scale;
     args.out = out, args.out_ld = out_ld, args.out_scale = out_scale, args.format = out_format;
-    args.vec = aligned(out, 4 * size) && out_ld % 4 == 0 && (groups == 1 || n % 4 == 0);
-    args.splits = p.splits, args.tiles_n = nnb, args.tiles_m = (m + p.rows - 1) / p.rows;
+    args.vec = aligned(out, 4 * size) && out_ld % 4 == 0 && (groups == 1 || n % 4 == 0) ? 1 : 0;
+    if (args.vec && aligned(out, 16) && out_ld * size % 16 == 0 && (groups == 1 || (long long)n * size % 16 == 0)) args.vec = 2;
+    args.splits = p.splits, args.tiles_n = (n + p.feat - 1) / p.feat, args.tiles_m = (m + p.rows - 1) / p.rows;
     args.status = dev_status, args.wait_ns = wait_ns, args.withhold = withhold;
     CUtensorMap wmap, amap;
     if (!make_codes_map(&wmap, w, k, n, groups, k, (long long)n * k, kFeat, 1) ||
-        !make_codes_map(&amap, a, k, groups, m, k, a_ld, 1, p.rows))
+        !make_codes_map(&amap, a, k, groups, m, k, a_ld, 1, std::min(p.rows, 128)))
         return DSA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p.feat == 256) return launch_wide(wmap, amap, args, st);
     switch (p.rows) {
         case 16: return launch_few<16>(wmap, amap, args, st);
         case 32: return launch_few<32>(wmap, amap, args, st);
@@ -439,6 +779,6 @@ extern "C" dsa_status_t dsa_gemm_q8_plan(int32_t m, int32_t n, int32_t k, int32_
     const dsa_status_t e = check_gemm(m, n, k, groups);
     if (e != DSA_OK) return e;
     const GemmPlan p = plan_gemm(m, n, k, groups);
-    plan[0] = kFeat, plan[1] = p.rows, plan[2] = p.splits;
+    plan[0] = p.feat, plan[1] = p.rows, plan[2] = p.splits;
     return DSA_OK;
 }

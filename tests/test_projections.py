@@ -153,7 +153,10 @@ def new_out(m, groups, n, fmt):
 
 SHAPES = [(1, 1, 16, 1), (1, 520, 4096, 1), (3, 130, 144, 2), (16, 128, 128, 1), (17, 257, 272, 3), (32, 1024, 4096, 8),
           (33, 96, 1040, 1), (64, 384, 512, 1), (65, 1000, 1040, 1), (130, 300, 2064, 2), (300, 640, 384, 1),
-          (2, 4096, 8192, 1), (48, 512, 16400, 1), (127, 2, 48, 5), (5, 129, 1024, 1)]
+          (2, 4096, 8192, 1), (48, 512, 16400, 1), (127, 2, 48, 5), (5, 129, 1024, 1),
+          # tiles of 256 x 256 by pairs: one round of tiles and several, ends inside a tile, a half and a block
+          (2560, 2048, 144, 1), (5000, 1000, 400, 1), (700, 300, 272, 16), (19500, 130, 1168, 1), (513, 520, 16, 13),
+          (4100, 2900, 2064, 1)]
 
 
 @pytest.mark.parametrize("m,n,k,groups", SHAPES)
