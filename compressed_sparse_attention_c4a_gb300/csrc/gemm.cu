@@ -8,6 +8,7 @@
 // The inner sums run in kind::f8f6f4 (fp32 accumulation in TMEM), one accumulator per block of 128; the epilogue warps
 // read each, multiply by the two scales' product and add it to sums in fp32 registers.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "rows8.cuh"
@@ -25,6 +26,7 @@ struct GemmArgs {
     int nkb, nnb;      // blocks of 128 along k and n
     const float* a_scale;
     long long a_scale_ld;
+    int a_scale_vec;   // four consecutive scales of a row may be read at once, from multiples of four blocks on
     const float* w_scale;
     void* out;
     long long out_ld;  // elements between rows
@@ -51,6 +53,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ uint64_t rows128_desc(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
+// A descriptor like d with this low word (address, leading offset): an offset within shared memory carries nothing upwards.
+__device__ __forceinline__ uint64_t desc_lo(uint64_t d, uint32_t lo) { return (d & 0xffffffff00000000ull) | lo; }
 // kind::f8f6f4, D fp32, A and B e4m3 and K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
@@ -60,16 +64,15 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
 __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, const GemmArgs& a) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
-    for (;;) {
+#pragma unroll 1
+    do {
+#pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-        if (*stop) return false;
-        if (global_ns() - t0 > a.wait_ns) {
-            *stop = 1;
-            report(a.status, DSA_ERR_TIMEOUT);
-            return false;
-        }
-    }
+    } while (!*stop && global_ns() - t0 <= a.wait_ns);
+    if (!*stop) report(a.status, DSA_ERR_TIMEOUT);
+    *stop = 1;
+    return false;
 }
 
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
@@ -326,13 +329,15 @@ __global__ void __launch_bounds__(kFewThreads) gemm_q8_few_kernel(const __grid_c
 // TMEM, two accumulators of 256 columns in turn.  Pairs go from tile to tile; the products of the next tile's first two blocks
 // run while a tile is stored.
 //
-// Warp 0: copies; warp 1: products (even CTA); warps 2, 3 only fill the warpgroup; warps 4-11: sums, four for each half of the
-// outputs, a thread holding a row's 128 sums and reading one scale a block.
+// Warp 0: copies; warp 1: products (even CTA); warps 2, 3: the scales' products, kChunk blocks at a time; warps 4-11: sums, four
+// for each half of the outputs, a thread holding a row's 128 sums.
 constexpr int kWideThreads = 384;
-constexpr int kWideStages = 6;
+constexpr int kWideStages = 4;
+static_assert(kWideStages % 2 == 0, "a stage meets the same accumulator every round");
 constexpr uint32_t kWideStage = 2 * 128 * 128;             // the CTA's rows of a, then its weight rows
 constexpr int kBandRows = 8;                               // row tiles that pass over the weights together
-constexpr int kWideSmem = 1024 + kWideStages * (int)kWideStage + 2 * kChunk * 256 * 4 + 512;
+constexpr int kOutBytes = 2 * 4096;                        // a warp's outputs on their way
+constexpr int kWideSmem = 1024 + kWideStages * (int)kWideStage + 8 * kOutBytes + 2 * kChunk * 256 * 4 + 512;
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
@@ -363,10 +368,6 @@ __device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t ma
 // Only TMEM has been read before it, which has ended: no release at cluster scope, whose fence took most of the kernel's time.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Four bytes global -> shared, zero if !in; and the wait for all of the thread's but the last group.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -404,74 +405,101 @@ __device__ __forceinline__ WideTile wide_tile(const GemmArgs& a, int t) {
     return WideTile{g, (t / high) * 256, (first + t % high) * 256};
 }
 
-// 128 outputs of a row from a thread's sums, `left` of them within the matrix.
-__device__ __forceinline__ void store_half_row(const GemmArgs& a, long long row, int g, int j0, const float (&v)[128]) {
-    const int left = min(128, a.n - j0);
-    const long long at = row * a.out_ld + (long long)g * a.n + j0;
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// A warp's 32 rows of 128 outputs, a thread a row's.  Through shared memory, 128 bytes of each row at a time in the tensor
+// map's swizzle (eight lanes' 16 bytes lie in different banks), and from there by one bulk copy: stored by the threads
+// themselves, 32 lines an instruction, the outputs took a fifth of the kernel's time.  The copy leaves out what lies beyond
+// the matrix.  Where the output's alignment admits no tensor map, the threads store value by value.
+__device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap& omap, uint8_t* stage, long long row, int g,
+                                           int j0, int lane, const uint64_t (&acc)[64]) {
+    const int left = min(128, a.n - j0), row0 = (int)row - lane;
+    float r = 1.f, s = 0.f;  // an 8-bit row's quotients: see BlockQuotient
     if (a.format == kOutQ8) {
         float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < 128; ++j) amax = fmaxf(amax, j < left ? fabsf(v[j]) : 0.f);
+        for (int j = 0; j < 64; ++j) {
+            amax = fmaxf(amax, 2 * j < left ? fabsf(lo_of(acc[j])) : 0.f);
+            amax = fmaxf(amax, 2 * j + 1 < left ? fabsf(hi_of(acc[j])) : 0.f);
+        }
         const float scale = block_scale8(amax);
         const BlockQuotient q(scale);
-        a.out_scale[(row * a.groups + g) * a.nnb + j0 / 128] = scale;
-        uint8_t* to = static_cast<uint8_t*>(a.out) + at;
+        r = q.r, s = q.s;
+        if (row < a.m) a.out_scale[(row * a.groups + g) * a.nnb + j0 / 128] = scale;
+    }
+    const auto quotient = [&](float v) {
+        const float q = v * r;
+        return fmaf(fmaf(-q, s, v), r, q);
+    };
+    // word w of the row's outputs, of B bytes each
+    const auto word = [&](auto bytes, int w) -> uint32_t {
+        constexpr int B = decltype(bytes)::value;
+        if constexpr (B == 4) return (uint32_t)(acc[w / 2] >> (32 * (w % 2)));
+        else if constexpr (B == 2) return bf16x2(lo_of(acc[w]), hi_of(acc[w]));
+        else return e4m3x4(quotient(lo_of(acc[2 * w])), quotient(hi_of(acc[2 * w])), quotient(lo_of(acc[2 * w + 1])),
+                           quotient(hi_of(acc[2 * w + 1])));
+    };
+    const auto pieces = [&](auto bytes) {  // bytes an output
+        constexpr int B = decltype(bytes)::value, PER = 128 / B;  // outputs in 128 bytes
 #pragma unroll
-        for (int j = 0; j < 128; j += 16) {
-            uint32_t c[4];
+        for (int piece = 0; piece < B; ++piece) {
+            uint8_t* to = stage + (piece & 1) * 4096;
+            if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this half of the stage
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                c[e] = e4m3x4(q(v[j + 4 * e]), q(v[j + 4 * e + 1]), q(v[j + 4 * e + 2]), q(v[j + 4 * e + 3]));
-            if (a.vec == 2 && j + 16 <= left) {
-                *reinterpret_cast<uint4*>(to + j) = make_uint4(c[0], c[1], c[2], c[3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (j + e < left) to[j + e] = (uint8_t)(c[e / 4] >> (8 * (e % 4)));
+            for (int c = 0; c < 8; ++c) {
+                const int w = piece * 32 + c * 4;
+                *reinterpret_cast<uint4*>(to + lane * 128 + ((c ^ (lane & 7)) * 16)) =
+                    make_uint4(word(bytes, w), word(bytes, w + 1), word(bytes, w + 2), word(bytes, w + 3));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (piece * PER < left) tma_store_3d(&omap, j0 + piece * PER, g, row0, smem_u32(to));
+                bulk_commit();
             }
         }
-    } else if (a.format == kOutBf16) {
-        uint16_t* to = static_cast<uint16_t*>(a.out) + at;
+    };
+    if (a.vec == 2) {
+        if (a.format == kOutF32) pieces(std::integral_constant<int, 4>());
+        else if (a.format == kOutBf16) pieces(std::integral_constant<int, 2>());
+        else pieces(std::integral_constant<int, 1>());
+        return;
+    }
+    if (row >= a.m) return;
+    const long long at = row * a.out_ld + (long long)g * a.n + j0;
 #pragma unroll
-        for (int j = 0; j < 128; j += 8) {
-            uint32_t c[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = bf16x2(v[j + 2 * e], v[j + 2 * e + 1]);
-            if (a.vec == 2 && j + 8 <= left) {
-                *reinterpret_cast<uint4*>(to + j) = make_uint4(c[0], c[1], c[2], c[3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (j + e < left) to[j + e] = (uint16_t)(c[e / 2] >> (16 * (e % 2)));
-            }
-        }
-    } else {
-        float* to = static_cast<float*>(a.out) + at;
-#pragma unroll
-        for (int j = 0; j < 128; j += 4) {
-            if (a.vec == 2 && j + 4 <= left) {
-                *reinterpret_cast<float4*>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (j + e < left) to[j + e] = v[j + e];
-            }
-        }
+    for (int j = 0; j < 128; ++j) {
+        const float v = j % 2 ? hi_of(acc[j / 2]) : lo_of(acc[j / 2]);
+        if (j >= left) continue;
+        if (a.format == kOutF32) static_cast<float*>(a.out)[at + j] = v;
+        else if (a.format == kOutBf16) static_cast<uint16_t*>(a.out)[at + j] = float_to_bf16(v);
+        else static_cast<uint8_t*>(a.out)[at + j] = float_to_e4m3(quotient(v));
     }
 }
 
 __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                        const __grid_constant__ CUtensorMap amap,
+                                                                       const __grid_constant__ CUtensorMap omap,
                                                                        const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    float* scales = reinterpret_cast<float*>(base + kWideStages * kWideStage);  // [2][kChunk][256], a thread's own
+    uint8_t* stage_out = base + kWideStages * kWideStage;  // two pieces of 32 rows x 128 bytes for each warp of sums
+    float* scales = reinterpret_cast<float*>(stage_out + 8 * kOutBytes);  // [2][kChunk][half][128 rows]
     uint64_t* full = reinterpret_cast<uint64_t*>(scales + 2 * kChunk * 256);      // the even CTA's: both CTAs' copies
     uint64_t* empty = full + kWideStages;
     uint64_t* acc_full = empty + kWideStages;
     uint64_t* acc_empty = acc_full + 2;  // the even CTA's: both CTAs' warps
     uint64_t* drained = acc_empty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    uint64_t* sc_full = drained + 1;  // [2]: scales written
+    uint64_t* sc_empty = sc_full + 2; // [2]: and read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_empty + 2);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -487,6 +515,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 16);
+            mbar_init(&sc_full[i], 2);
+            mbar_init(&sc_empty[i], 8);
         }
         mbar_init(drained, 1);
         *stop = 0;
@@ -505,7 +535,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
     pdl_launch_dependents();
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0 && lane == 0 && !a.withhold) {
             int s = 0;
             uint32_t ph = 1;
@@ -531,106 +561,145 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
                 if (++s == kWideStages) s = 0, ph ^= 1;
             }
         } else if (warp == 1 && rank == 0) {
+            // Products need no tile: block after block, in a loop unrolled over the stages so that every address is a constant
+            // beside one uniform word.
             constexpr uint32_t idesc = idesc_e4m3(256, 256);
-            int s = 0, b = 0;
-            uint32_t ph = 0, aph = 1;
-            bool live = true;
-            for (int t = pair; t < tiles && live; t += pairs) {
-                for (int kb = 0; kb < a.nkb; ++kb) {
-                    const bool ok = wait_or_stop(&acc_empty[b], aph, stop, a) && wait_or_stop(&full[s], ph, stop, a);
+            const uint64_t desc = rows128_desc(smem_u32(base));
+            const uint32_t first = __shfl_sync(0xffffffffu, (uint32_t)desc, 0), d = __shfl_sync(0xffffffffu, tmem, 0);
+            long long left = (long long)((tiles - pair + pairs - 1) / pairs) * a.nkb;
+            for (uint32_t ph = 0; left > 0; ph ^= 1) {
+#pragma unroll
+                for (int s = 0; s < kWideStages; ++s) {
+                    if (left <= 0) break;
+                    // the accumulator's (round * kWideStages / 2 + s / 2)-th use; ph is the round's parity
+                    const uint32_t use = (kWideStages / 2 % 2 ? ph : 0u) + s / 2;
+                    const bool ok = wait_or_stop(&full[s], ph, stop, a) && wait_or_stop(&acc_empty[s & 1], (use & 1) ^ 1, stop, a);
                     if (!__all_sync(0xffffffffu, ok)) {
-                        live = false;
+                        left = 0;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(base) + s * kWideStage;
+                    const uint32_t lo = first + s * (kWideStage >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f8_pair_elect(tmem + b * 256, rows128_desc(st + ks * 32), rows128_desc(st + 128 * 128 + ks * 32),
+                        mma_f8_pair_elect(d + (s & 1) * 256, desc_lo(desc, lo + 2 * ks), desc_lo(desc, lo + (128 * 128 >> 4) + 2 * ks),
                                           idesc, ks > 0 ? 1u : 0u);
+                    mma_commit_pair_elect(&acc_full[s & 1]);
                     mma_commit_pair_elect(&empty[s]);
-                    mma_commit_pair_elect(&acc_full[b]);
-                    if (++s == kWideStages) s = 0, ph ^= 1;
-                    b ^= 1;
-                    aph ^= b == 0 ? 1u : 0u;
+                    --left;
                 }
             }
             mma_commit_pair_elect(drained, 1);
             mbar_wait_bounded(drained, 0, kWaitLimitNs);
+        } else if (warp >= 2) {
+            // Each lane two rows: their scales of kChunk blocks (32 bytes of each row), times those of the two halves' weights.
+            const int r0 = 64 * (warp - 2) + lane;
+            const bool vec = a.a_scale_vec != 0;
+            int c = 0;
+            uint32_t ph = 1;
+            bool live = true;
+            for (int t = pair; t < tiles && live; t += pairs) {
+                const WideTile x = wide_tile(a, t);
+                const float* sw = a.w_scale + ((long long)x.g * a.nnb + x.n0 / 128) * a.nkb;
+                const bool second = x.n0 / 128 + 1 < a.nnb;
+                for (int kb = 0; kb < a.nkb; kb += kChunk) {
+                    float s[2][kChunk];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = x.m0 + 128 * (int)rank + r0 + 32 * i;
+                        const float* sa = a.a_scale + (long long)row * a.a_scale_ld + (long long)x.g * a.nkb + kb;
+                        if (vec && row < a.m && kb + kChunk <= a.nkb) {
+                            const float4 u = *reinterpret_cast<const float4*>(sa), v = *reinterpret_cast<const float4*>(sa + 4);
+                            s[i][0] = u.x, s[i][1] = u.y, s[i][2] = u.z, s[i][3] = u.w;
+                            s[i][4] = v.x, s[i][5] = v.y, s[i][6] = v.z, s[i][7] = v.w;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < kChunk; ++j) s[i][j] = row < a.m && kb + j < a.nkb ? sa[j] : 0.f;
+                        }
+                    }
+                    float w0[kChunk], w1[kChunk];
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) {
+                        w0[j] = kb + j < a.nkb ? __ldg(sw + kb + j) : 0.f;
+                        w1[j] = second && kb + j < a.nkb ? __ldg(sw + a.nkb + kb + j) : 0.f;
+                    }
+                    live = __all_sync(0xffffffffu, wait_or_stop(&sc_empty[c], ph, stop, a));
+                    if (!live) break;
+                    float* to = scales + c * kChunk * 256 + r0;
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            to[j * 256 + 32 * i] = s[i][j] * w0[j];
+                            to[j * 256 + 128 + 32 * i] = s[i][j] * w1[j];
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[c]);
+                    c ^= 1;
+                    ph ^= c == 0 ? 1u : 0u;
+                }
+            }
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int t8 = threadIdx.x - 128, half = (warp - 4) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int half = (warp - 4) >> 2;
         const int mine = 128 * (int)rank + 32 * (warp & 3) + lane;  // the thread's row of the tile
         const uint32_t column = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
         const uint32_t drained_to[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
-        // the row's scales, kChunk blocks ahead: into the thread's own places, so that only it waits for them
-        const uint32_t own = smem_u32(scales + t8);
-        int turn = 0;
-        const auto fetch = [&](int t, int kb) {
-            const WideTile x = wide_tile(a, t < tiles ? t : 0);
-            const int row = x.m0 + mine;
-            const float* sa = a.a_scale + (long long)(row < a.m ? row : 0) * a.a_scale_ld + (long long)x.g * a.nkb;
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                const bool in = t < tiles && row < a.m && kb + i < a.nkb;
-                cp_async4(own + ((turn * kChunk + i) * 256) * 4, sa + (in ? kb + i : 0), in);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            turn ^= 1;
-        };
-        int b = 0;
-        uint32_t aph = 0;
+        int b = 0, c = 0;
+        uint32_t aph = 0, cph = 0;
         bool live = true;
-        fetch(pair, 0);
         for (int t = pair; t < tiles; t += pairs) {
             const WideTile x = wide_tile(a, t);
-            const float* sw = a.w_scale + ((long long)x.g * a.nnb + min(x.n0 / 128 + half, a.nnb - 1)) * a.nkb;
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0ull;
             for (int kb = 0; kb < a.nkb && live; ++kb) {
                 if (kb % kChunk == 0) {
-                    const bool more = kb + kChunk < a.nkb;
-                    fetch(more ? t : t + pairs, more ? kb + kChunk : 0);
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    live = __all_sync(0xffffffffu, wait_or_stop(&sc_full[c], cph, stop, a));
+                    if (!live) break;
                 }
-                const float ws = __ldg(sw + kb);
+                const float f = scales[(c * kChunk + kb % kChunk) * 256 + half * 128 + 32 * (warp & 3) + lane];
+                if (kb % kChunk == kChunk - 1 || kb == a.nkb - 1) {  // the chunk's last
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_empty[c]);
+                    c ^= 1;
+                    cph ^= c == 0 ? 1u : 0u;
+                }
                 live = __all_sync(0xffffffffu, wait_or_stop(&acc_full[b], aph, stop, a));
                 if (!live) break;
                 tc_fence_after();
-                // `turn` is where the next fetch goes, which is where the last one but one went: the current scales
-                const float f = scales[(turn * kChunk + kb % kChunk) * 256 + t8] * ws;
+                const uint32_t from = column + b * 256;
                 uint64_t f2;
                 asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
+                uint32_t p[2][32];
+                tmem_ld32_nowait(from, p[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[32];
-                    tmem_ld32_nowait(column + b * 256 + 32 * c, p);
+                for (int q = 0; q < 4; ++q) {
                     tmem_wait_ld();
-                    regs_after_wait(p);
-                    if (c == 3) {
+                    regs_after_wait(p[q & 1]);
+                    if (q < 3) {
+                        tmem_ld32_nowait(from + 32 * (q + 1), p[(q + 1) & 1]);
+                    } else {
                         tc_fence_before();
                         if (lane == 0) mbar_arrive_cluster(drained_to[b]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], p[2 * j], p[2 * j + 1], f2);
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 * q + j], p[q & 1][2 * j], p[q & 1][2 * j + 1], f2);
                 }
                 b ^= 1;
                 aph ^= b == 0 ? 1u : 0u;
             }
-            const long long row = x.m0 + mine;
-            if (row < a.m && x.n0 + 128 * half < a.n) {
-                float v[128];
+            if (!live) {  // a wait expired: this tile and the ones after it are zeros
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[j]));
-                    if (!live) v[2 * j] = v[2 * j + 1] = 0.f;  // a wait expired: this tile and the ones after it are zeros
-                }
-                store_half_row(a, row, x.g, x.n0 + 128 * half, v);
+                for (int j = 0; j < 64; ++j) acc[j] = 0ull;
             }
+            const int j0 = x.n0 + 128 * half;
+            if (j0 < a.n && x.m0 + 128 * (int)rank + 32 * (warp & 3) < a.m)
+                store_wide(a, omap, stage_out + (warp - 4) * kOutBytes, x.m0 + mine, x.g, j0, lane, acc);
         }
+        if (lane == 0) bulk_wait_all();
     }
     if (*stop) {  // copies that the other CTA asked for may still be on their way: they take microseconds
         const uint64_t t0 = global_ns();
@@ -694,13 +763,29 @@ static dsa_status_t launch_few(const CUtensorMap& wmap, const CUtensorMap& amap,
 }
 
 static dsa_status_t launch_wide(const CUtensorMap& wmap, const CUtensorMap& amap, GemmArgs a, cudaStream_t st) {
+    CUtensorMap omap = wmap;
+    if (a.vec == 2) {
+        auto fn = tensor_map_encoder();
+        const int size = a.format == kOutF32 ? 4 : a.format == kOutBf16 ? 2 : 1;
+        const cuuint64_t dim[3] = {(cuuint64_t)a.n, (cuuint64_t)a.groups, (cuuint64_t)a.m};
+        // one group: its stride is never used, but has to be a multiple of 16
+        const cuuint64_t stride[2] = {((cuuint64_t)a.n * size + 15) / 16 * 16, (cuuint64_t)a.out_ld * size};
+        const cuuint32_t box[3] = {(cuuint32_t)(128 / size), 1, 32}, one[3] = {1, 1, 1};
+        if (!fn || fn(&omap,
+                      a.format == kOutF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                      : a.format == kOutBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                      3, a.out, dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return DSA_ERR_CUDA;
+    }
     const long long tiles = (long long)a.groups * a.tiles_n * a.tiles_m;
     if (tiles > 0x3fffffff) return DSA_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(gemm_q8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess)
         return DSA_ERR_CUDA;
     const long long pairs = std::min<long long>(tiles, sm_count() / 2);
     if (launch_pdl_cluster(gemm_q8_wide_kernel, dim3((unsigned)(2 * pairs)), dim3(kWideThreads), kWideSmem, st, 2, wmap, amap,
-                           a) != cudaSuccess)
+                           omap, a) != cudaSuccess)
         return DSA_ERR_CUDA;
     return launch_status();
 }
@@ -732,7 +817,9 @@ static dsa_status_t gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, con
     const GemmPlan p = plan_gemm(m, n, k, groups);
     GemmArgs args{};
     args.m = m, args.n = n, args.k = k, args.groups = groups, args.nkb = nkb, args.nnb = nnb;
-    args.a_scale = a_scale, args.a_scale_ld = a_scale_ld, args.w_scale = w_scale;
+    args.a_scale = a_scale, args.a_scale_ld = a_scale_ld;
+    args.a_scale_vec = aligned(a_scale, 16) && a_scale_ld % 4 == 0 && (groups == 1 || nkb % 4 == 0);
+    args.w_scale = w_scale;
     args.out = out, args.out_ld = out_ld, args.out_scale = out_scale, args.format = out_format;
     args.vec = aligned(out, 4 * size) && out_ld % 4 == 0 && (groups == 1 || n % 4 == 0) ? 1 : 0;
     if (args.vec && aligned(out, 16) && out_ld * size % 16 == 0 && (groups == 1 || (long long)n * size % 16 == 0)) args.vec = 2;
