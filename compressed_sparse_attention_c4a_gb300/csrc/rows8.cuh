@@ -33,8 +33,11 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 
+// Two bf16 values in a word, the first in the low half, rounded to nearest even by one instruction.
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
-    return (uint32_t)float_to_bf16(a) | ((uint32_t)float_to_bf16(b) << 16);
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
 }
 
 }  // namespace dsa
