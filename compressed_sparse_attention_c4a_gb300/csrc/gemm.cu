@@ -17,7 +17,6 @@ namespace dsa {
 
 constexpr int kFeat = 128;       // weight rows of a tile (the MMA's M)
 constexpr int kChunk = 8;        // blocks of 128 whose scales are staged together
-constexpr int kFewThreads = 192; // warp 0: copies, warp 1: MMA, warps 2-5: sums
 
 enum { kOutF32 = DSA_FP32, kOutBf16 = DSA_BF16, kOutQ8 = DSA_FP8_E4M3 };
 
@@ -86,6 +85,29 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// After tmem_wait_ld(): no use of the registers is scheduled before the wait.
+__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+// acc (two sums) += p (two products) * s (twice the same scale)
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t p0, uint32_t p1, uint64_t s) {
+    asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}" : "+l"(acc) : "r"(p0), "r"(p1), "l"(s));
+}
+
 // Four consecutive outputs (features j0 + 4 lane ..) of row i, group g, by a warp that holds the 128 features of a block.
 __device__ __forceinline__ void store_block(const GemmArgs& a, int i, int g, int nb, int lane, float4 v) {
     const int j = nb * kFeat + 4 * lane, left = a.n - j;
@@ -131,13 +153,46 @@ template <int BN>
 __host__ __device__ constexpr int few_stage_bytes() { return kFeat * 128 + BN * 128; }
 template <int BN>
 __host__ __device__ constexpr int few_accumulators() { return BN >= 128 ? 2 : 4; }
+// warps of sums: 4 with all of a tile's rows each, or 8 with half of them
+template <int BN>
+__host__ __device__ constexpr int few_sum_warps() { return BN >= 64 ? 8 : 4; }
+template <int BN>
+__host__ __device__ constexpr int few_threads() { return 64 + 32 * few_sum_warps<BN>(); }
+
+// The sums of S CTAs for 8 / S rows j, j + step .. of the tile, every load in flight before the first is added (in rank order).
+// What is loaded is added, so no load from another CTA is left in flight.
+template <int S>
+__device__ __forceinline__ void join_rows(const GemmArgs& a, const float* part, int j, int step, int end, int row0, int g, int nb,
+                                          int lane, bool failed) {
+    constexpr int R = 8 / S;
+    float4 v[R][S];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int r = 0; r < S; ++r) {
+            if (j + i * step >= end) break;
+            const uint32_t at = smem_u32(part + (j + i * step) * 128 + 4 * lane);
+            v[i][r] = ld_cluster_v4(S > 1 ? mapa_shared(at, r) : at);
+        }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (j + i * step >= end) break;
+#pragma unroll
+        for (int r = 1; r < S; ++r)
+            v[i][0].x += v[i][r].x, v[i][0].y += v[i][r].y, v[i][0].z += v[i][r].z, v[i][0].w += v[i][r].w;
+        if (failed) v[i][0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        store_block(a, row0 + j + i * step, g, nb, lane, v[i][0]);
+    }
+}
 
 // Tile: 128 weight rows x BN rows of a.  The MMA's M is the weights' side, so that few rows of a cost few columns.  A tile's
 // blocks of 128 along k are shared by the CTAs of a cluster, whose sums are added in rank order.
+// Warp 0: copies, warp 1: products, the others: sums.
 template <int BN>
-__global__ void __launch_bounds__(kFewThreads) gemm_q8_few_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                                  const __grid_constant__ CUtensorMap amap, const GemmArgs a) {
-    constexpr int NA = few_accumulators<BN>();
+__global__ void __launch_bounds__(few_threads<BN>()) gemm_q8_few_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                        const __grid_constant__ CUtensorMap amap,
+                                                                        const __grid_constant__ GemmArgs a) {
+    constexpr int NA = few_accumulators<BN>(), EW = few_sum_warps<BN>(), COLS = BN * 4 / EW;  // rows of a for each warp of sums
     constexpr uint32_t kStage = few_stage_bytes<BN>();
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -158,7 +213,8 @@ __global__ void __launch_bounds__(kFewThreads) gemm_q8_few_kernel(const __grid_c
     tile /= a.tiles_m;
     const int nb = tile % a.tiles_n, g = tile / a.tiles_n;
     const int row0 = tm * BN;
-    const int kb0 = (int)((long long)a.nkb * rank / a.splits), kb1 = (int)((long long)a.nkb * (rank + 1) / a.splits);
+    const int count = (a.nkb - rank + a.splits - 1) / a.splits;  // blocks rank, rank + splits ..
+    const int ahead = min(a.stages, count);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -167,133 +223,150 @@ __global__ void __launch_bounds__(kFewThreads) gemm_q8_few_kernel(const __grid_c
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);
+            mbar_init(&acc_empty[i], EW);
         }
         mbar_init(drained, 1);
         *stop = 0;
         fence_barrier_init();
+        // The weights do not come from the preceding kernel: those of the first stages are requested before anything else.
+        if (!a.withhold)
+            for (int i = 0; i < ahead; ++i) {
+                mbar_arrive_expect_tx(&full[i], kStage);
+                tma_load_3d(smem_u32(base) + i * kStage, &wmap, (rank + i * a.splits) * 128, nb * kFeat, g, smem_u32(&full[i]));
+            }
     }
-    if (warp == 1) tmem_alloc(tmem_slot, NA * BN < 32 ? 32 : NA * BN);
+    if (warp == 1) tmem_alloc(tmem_slot, NA * BN);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0) {
-        // Copies.  The weights do not come from the preceding kernel: those of the first stages are requested before the wait.
+        pdl_wait();
         if (lane == 0 && !a.withhold) {
-            const int ahead = min(a.stages, kb1 - kb0);
-            for (int i = 0; i < ahead; ++i) {
-                const uint32_t st = smem_u32(base) + i * kStage;
-                mbar_arrive_expect_tx(&full[i], kStage);
-                tma_load_3d(st, &wmap, (kb0 + i) * 128, nb * kFeat, g, smem_u32(&full[i]));
-            }
-            pdl_wait();
             pdl_launch_dependents();
             for (int i = 0; i < ahead; ++i)
-                tma_load_3d(smem_u32(base) + i * kStage + kFeat * 128, &amap, (kb0 + i) * 128, g, row0, smem_u32(&full[i]));
-            int s = 0;
+                tma_load_3d(smem_u32(base) + i * kStage + kFeat * 128, &amap, (rank + i * a.splits) * 128, g, row0,
+                            smem_u32(&full[i]));
+            int s = 0, issued = ahead;
             uint32_t ph = 0;
-            int issued = ahead;
-            for (int kb = kb0 + ahead; kb < kb1; ++kb) {
+            for (int i = ahead; i < count; ++i) {
                 if (!wait_or_stop(&empty[s], ph, stop, a)) break;
                 const uint32_t st = smem_u32(base) + s * kStage;
+                const int x = (rank + i * a.splits) * 128;
                 mbar_arrive_expect_tx(&full[s], kStage);
-                tma_load_3d(st, &wmap, kb * 128, nb * kFeat, g, smem_u32(&full[s]));
-                tma_load_3d(st + kFeat * 128, &amap, kb * 128, g, row0, smem_u32(&full[s]));
+                tma_load_3d(st, &wmap, x, nb * kFeat, g, smem_u32(&full[s]));
+                tma_load_3d(st + kFeat * 128, &amap, x, g, row0, smem_u32(&full[s]));
                 ++issued;
                 if (++s == a.stages) s = 0, ph ^= 1;
             }
             // no copy is left in flight: the last fill of each stage has landed (an expired wait must not leave one behind)
             for (int i = max(0, issued - a.stages); i < issued; ++i)
                 mbar_wait_bounded(&full[i % a.stages], (uint32_t)(i / a.stages) & 1, kWaitLimitNs);
-        } else {
-            pdl_wait();
         }
     } else if (warp == 1) {
         pdl_wait();
         constexpr uint32_t idesc = idesc_e4m3(kFeat, BN);
+        const uint64_t desc = rows128_desc(smem_u32(base));
         int s = 0, b = 0;
         uint32_t ph = 0, aph = 1;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int i = 0; i < count; ++i) {
             const bool ok = wait_or_stop(&full[s], ph, stop, a) && wait_or_stop(&acc_empty[b], aph, stop, a);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            const uint32_t st = smem_u32(base) + s * kStage;
+            const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)desc + s * (kStage >> 4), 0);
+            const uint32_t d = __shfl_sync(0xffffffffu, tmem + b * BN, 0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_f8_elect(tmem + b * BN, rows128_desc(st + ks * 32), rows128_desc(st + kFeat * 128 + ks * 32), idesc,
-                             ks > 0 ? 1u : 0u);
-            mma_commit_elect(&empty[s]);
+                mma_f8_elect(d, desc_lo(desc, lo + 2 * ks), desc_lo(desc, lo + (kFeat * 128 >> 4) + 2 * ks), idesc, ks > 0 ? 1u : 0u);
             mma_commit_elect(&acc_full[b]);
+            mma_commit_elect(&empty[s]);
             if (++s == a.stages) s = 0, ph ^= 1;
             if (++b == NA) b = 0, aph ^= 1;
         }
         mma_commit_elect(drained);
         mbar_wait_bounded(drained, 0, kWaitLimitNs);
-        __syncwarp();
     } else {
         pdl_wait();
-        const int t = threadIdx.x - 64;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        float acc[BN];
+        const int t = threadIdx.x - 64, j0 = (warp - 2) / 4 * COLS;
+        const uint32_t column = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j0;
+        uint64_t acc[COLS / 2];
 #pragma unroll
-        for (int j = 0; j < BN; ++j) acc[j] = 0.f;
-        // the products of scales of block kb0 + chunk * 8 + e % 8 and row e / 8, e = t, t + 128 ..
-        constexpr int PER = BN * kChunk / 128;
+        for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
+        // the products of scales of the CTA's block chunk * 8 + e % 8 and row e / 8, e = t, t + 32 EW ..
+        constexpr int PER = BN * kChunk / (32 * EW);
         float next[PER];
         const float* sa = a.a_scale + (long long)g * a.nkb;
         const float* sw = a.w_scale + ((long long)g * a.nnb + nb) * a.nkb;
-        const auto fetch = [&](int kb) {
+        const auto fetch = [&](int i0) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int e = t + 128 * i, row = row0 + e / kChunk, b = kb + e % kChunk;
-                next[i] = row < a.m && b < kb1 ? sa[(long long)row * a.a_scale_ld + b] * __ldg(sw + b) : 0.f;
+                const int e = t + 32 * EW * i, row = row0 + e / kChunk, j = i0 + e % kChunk, kb = rank + j * a.splits;
+                next[i] = row < a.m && j < count ? sa[(long long)row * a.a_scale_ld + kb] * __ldg(sw + kb) : 0.f;
             }
         };
-        fetch(kb0);
+        fetch(0);
         int b = 0;
         uint32_t aph = 0;
         bool live = true;  // a warp whose wait expired still takes part in the barriers below
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const int c = (kb - kb0) % kChunk;
-            float* sc = scales + ((kb - kb0) / kChunk & 1) * kChunk * BN;
+        for (int j = 0; j < count; ++j) {
+            const int c = j % kChunk;
+            float* sc = scales + (j / kChunk & 1) * kChunk * BN;
             if (c == 0) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int e = t + 128 * i;
+                    const int e = t + 32 * EW * i;
                     sc[(e % kChunk) * BN + e / kChunk] = next[i];
                 }
-                named_bar_sync(1, 128);
-                fetch(kb + kChunk);
+                named_bar_sync(1, 32 * EW);
+                fetch(j + kChunk);
             }
             live = live && __all_sync(0xffffffffu, wait_or_stop(&acc_full[b], aph, stop, a));
             if (!live) continue;
             tc_fence_after();
-            const float4* s4 = reinterpret_cast<const float4*>(sc + c * BN);
-#pragma unroll
-            for (int j0 = 0; j0 < BN; j0 += 16) {
+            const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(sc + c * BN + j0);  // four rows' scales each
+            const uint32_t from = column + b * BN;
+            const auto done = [&]() {
+                tc_fence_before();
+                if (lane == 0) mbar_arrive(&acc_empty[b]);
+            };
+            if constexpr (COLS == 16) {
                 float p[16];
-                tmem_ld16(tmem + b * BN + lanes + j0, p);
-                if (j0 + 16 == BN) {
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive(&acc_empty[b]);
-                }
+                tmem_ld_nowait<16>(from, p);
+                tmem_wait_ld();
+                tmem_regs_after_wait<16>(p);
+                done();
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 f = s4[(j0 + j) / 4];
-                    acc[j0 + j] = fmaf(p[j], f.x, acc[j0 + j]);
-                    acc[j0 + j + 1] = fmaf(p[j + 1], f.y, acc[j0 + j + 1]);
-                    acc[j0 + j + 2] = fmaf(p[j + 2], f.z, acc[j0 + j + 2]);
-                    acc[j0 + j + 3] = fmaf(p[j + 3], f.w, acc[j0 + j + 3]);
+                for (int q = 0; q < 4; ++q) {
+                    const ulonglong2 f = s2[q];
+                    fma2(acc[2 * q], __float_as_uint(p[4 * q]), __float_as_uint(p[4 * q + 1]), f.x);
+                    fma2(acc[2 * q + 1], __float_as_uint(p[4 * q + 2]), __float_as_uint(p[4 * q + 3]), f.y);
+                }
+            } else {
+                uint32_t p[COLS / 32][32];
+#pragma unroll
+                for (int h = 0; h < COLS / 32; ++h) tmem_ld32_nowait(from + 32 * h, p[h]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < COLS / 32; ++h) regs_after_wait(p[h]);
+                done();
+#pragma unroll
+                for (int q = 0; q < COLS / 4; ++q) {
+                    const ulonglong2 f = s2[q];
+                    const uint32_t* v = p[q / 8] + 4 * (q % 8);
+                    fma2(acc[2 * q], v[0], v[1], f.x);
+                    fma2(acc[2 * q + 1], v[2], v[3], f.y);
                 }
             }
             if (++b == NA) b = 0, aph ^= 1;
         }
-        // the last accumulator was complete, so the stages have been read
-        const int feat = 32 * (warp & 3) + lane;
+        // every product has ended, so the stages are free
+        float* to = part + j0 * 128 + 32 * (warp & 3) + lane;
 #pragma unroll
-        for (int j = 0; j < BN; ++j) part[j * 128 + feat] = acc[j];
+        for (int j = 0; j < COLS / 2; ++j) {
+            to[2 * j * 128] = __uint_as_float((uint32_t)acc[j]);
+            to[(2 * j + 1) * 128] = __uint_as_float((uint32_t)(acc[j] >> 32));
+        }
     }
     __syncwarp();
     if (a.splits > 1) {
@@ -302,25 +375,23 @@ __global__ void __launch_bounds__(kFewThreads) gemm_q8_few_kernel(const __grid_c
     } else {
         __syncthreads();
     }
-    bool failed = false;
+    bool failed = false;  // a wait expired in one of the CTAs: zeros
     for (int r = 0; r < a.splits; ++r) failed |= ld_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(stop)), r)) != 0u;
-    for (int j = rank + a.splits * warp; j < BN && row0 + j < a.m; j += a.splits * (kFewThreads / 32)) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        const uint32_t at = smem_u32(part + j * 128 + 4 * lane);
-        for (int r = 0; r < a.splits; ++r) {
-            const float4 p = ld_cluster_v4(mapa_shared(at, r));
-            v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
-        }
-        if (failed) v = make_float4(0.f, 0.f, 0.f, 0.f);
-        store_block(a, row0 + j, g, nb, lane, v);
+    failed = __any_sync(0xffffffffu, failed);
+    const int end = min(BN, a.m - row0), step = a.splits * (few_threads<BN>() / 32);
+    for (int j = rank + a.splits * warp; j < end; j += 8 / a.splits * step) {
+        if (a.splits == 1) join_rows<1>(a, part, j, step, end, row0, g, nb, lane, failed);
+        else if (a.splits == 2) join_rows<2>(a, part, j, step, end, row0, g, nb, lane, failed);
+        else if (a.splits == 4) join_rows<4>(a, part, j, step, end, row0, g, nb, lane, failed);
+        else join_rows<8>(a, part, j, step, end, row0, g, nb, lane, failed);
     }
-    if (a.splits > 1) {  // the others may still read this CTA's sums
-        cluster_arrive();
+    // The others may still read this CTA's sums.  What a thread has read it has used, so nothing needs to be released (a
+    // release here waits for the outputs: 2 us).
+    if (a.splits > 1) {
+        cluster_arrive_relaxed();
         cluster_wait();
-    } else {
-        __syncthreads();
     }
-    if (warp == 1) tmem_dealloc(tmem, NA * BN < 32 ? 32 : NA * BN);
+    if (warp == 1) tmem_dealloc(tmem, NA * BN);
 }
 
 // ---- many rows -------------------------------------------------------------------------------------------------------
@@ -369,29 +440,6 @@ __device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t ma
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-// After tmem_wait_ld(): no use of the registers is scheduled before the wait.
-__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                     "+r"(r[i + 6]), "+r"(r[i + 7]));
-}
-// acc (two sums) += p (two products) * s (twice the same scale)
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t p0, uint32_t p1, uint64_t s) {
-    asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}" : "+l"(acc) : "r"(p0), "r"(p1), "l"(s));
-}
-
 struct WideTile {
     int g, n0, m0;  // group, first output, first row
 };
@@ -719,15 +767,18 @@ struct GemmPlan {
     int splits;  // CTAs that share a tile: its blocks of k, or (a pair) its rows
 };
 
+__host__ constexpr int few_ctas_per_sm(int rows);
+
 static GemmPlan plan_gemm(int m, int n, int k, int groups) {
     GemmPlan p{};
     p.feat = kFeat;
-    if ((long long)groups * ((m + 255) / 256) * ((n + 255) / 256) >= sm_count() / 2) return GemmPlan{256, 256, 2};
+    const long long sms = sm_count();
+    if (m > 128 && (long long)groups * ((m + 255) / 256) * ((n + 255) / 256) >= sms / 2) return GemmPlan{256, 256, 2};
     p.rows = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
     const long long tiles = (long long)groups * row_blocks(n) * ((m + p.rows - 1) / p.rows);
-    const int nkb = row_blocks(k);
+    const int nkb = row_blocks(k), most = p.rows >= 128 ? 4 : 8;
     p.splits = 1;
-    while (p.splits < 8 && tiles * p.splits * 2 <= 2ll * sm_count() && nkb >= 4 * p.splits) p.splits *= 2;
+    while (p.splits < most && tiles * p.splits * 2 <= few_ctas_per_sm(p.rows) * sms && nkb >= 4 * p.splits) p.splits *= 2;
     return p;
 }
 
@@ -744,20 +795,22 @@ static bool make_codes_map(CUtensorMap* map, const void* base, long long x, long
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// CTAs that an SM holds at once: registers allow one of 128 rows, shared memory and TMEM two of fewer.
+__host__ constexpr int few_ctas_per_sm(int rows) { return rows >= 128 ? 1 : 2; }
+
 template <int BN>
 static dsa_status_t launch_few(const CUtensorMap& wmap, const CUtensorMap& amap, GemmArgs a, cudaStream_t st) {
-    // two CTAs an SM where their accumulators and a few stages fit
     constexpr int extra = 1024 + 2 * kChunk * BN * 4 + 512;
-    constexpr int budget = BN <= 32 ? 228 * 1024 / 2 - 1024 : 227 * 1024;
-    a.stages = std::max(2, std::min(12, (budget - extra) / few_stage_bytes<BN>()));
+    constexpr int budget = few_ctas_per_sm(BN) == 2 ? 228 * 1024 / 2 - 1024 : 227 * 1024;
+    a.stages = std::min(12, (budget - extra) / few_stage_bytes<BN>());
     const int smem = extra + a.stages * few_stage_bytes<BN>();
-    static_assert(2 * few_stage_bytes<BN>() >= BN * 512 || BN == 128, "the sums fit into the stages");
+    static_assert((budget - extra) / few_stage_bytes<BN>() * few_stage_bytes<BN>() >= BN * 512, "the sums fit into the stages");
     if (cudaFuncSetAttribute(gemm_q8_few_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return DSA_ERR_CUDA;
     const long long grid = (long long)a.groups * a.tiles_n * a.tiles_m * a.splits;
     if (grid > 0x7fffffff) return DSA_ERR_UNSUPPORTED;
-    if (launch_pdl_cluster(gemm_q8_few_kernel<BN>, dim3((unsigned)grid), dim3(kFewThreads), smem, st, a.splits, wmap, amap,
-                           a) != cudaSuccess)
+    if (launch_pdl_cluster(gemm_q8_few_kernel<BN>, dim3((unsigned)grid), dim3(few_threads<BN>()), smem, st, a.splits, wmap,
+                           amap, a) != cudaSuccess)
         return DSA_ERR_CUDA;
     return launch_status();
 }
