@@ -151,48 +151,47 @@ __device__ __forceinline__ void store_block(const GemmArgs& a, int i, int g, int
 
 template <int BN>
 __host__ __device__ constexpr int few_stage_bytes() { return kFeat * 128 + BN * 128; }
-template <int BN>
-__host__ __device__ constexpr int few_accumulators() { return BN >= 128 ? 2 : 4; }
-// warps of sums: 4 with all of a tile's rows each, or 8 with half of them
-template <int BN>
-__host__ __device__ constexpr int few_sum_warps() { return BN >= 64 ? 8 : 4; }
-template <int BN>
-__host__ __device__ constexpr int few_threads() { return 64 + 32 * few_sum_warps<BN>(); }
+constexpr int kFewThreads = 192;
+constexpr int kFewAcc = 4;  // accumulators
 
-// The sums of S CTAs for 8 / S rows j, j + step .. of the tile, every load in flight before the first is added (in rank order).
-// What is loaded is added, so no load from another CTA is left in flight.
+// The sums of S CTAs for up to R = 4 / S rows j, j + step .. of the tile, four loads in flight before the first is added (in
+// rank order).  What is loaded is added, so no load from another CTA is left in flight.
 template <int S>
-__device__ __forceinline__ void join_rows(const GemmArgs& a, const float* part, int j, int step, int end, int row0, int g, int nb,
+__device__ __forceinline__ void join_rows(const GemmArgs& a, const float* part, int j, int step, int rows, int row0, int g, int nb,
                                           int lane, bool failed) {
-    constexpr int R = 8 / S;
-    float4 v[R][S];
+    constexpr int Q = S < 4 ? S : 4, R = 4 / Q;
+    const uint32_t at = smem_u32(part + j * 128 + 4 * lane);
+    float4 sum[R];
+#pragma unroll
+    for (int r0 = 0; r0 < S; r0 += Q) {
+        float4 v[R][Q];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int r = 0; r < Q; ++r)
+                if (i < rows) v[i][r] = ld_cluster_v4(mapa_shared(at + i * step * 512, r0 + r));
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i < rows)
+#pragma unroll
+                for (int r = 0; r < Q; ++r) {
+                    if (r0 + r == 0) sum[i] = v[i][r];
+                    else sum[i].x += v[i][r].x, sum[i].y += v[i][r].y, sum[i].z += v[i][r].z, sum[i].w += v[i][r].w;
+                }
+    }
 #pragma unroll
     for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int r = 0; r < S; ++r) {
-            if (j + i * step >= end) break;
-            const uint32_t at = smem_u32(part + (j + i * step) * 128 + 4 * lane);
-            v[i][r] = ld_cluster_v4(S > 1 ? mapa_shared(at, r) : at);
-        }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        if (j + i * step >= end) break;
-#pragma unroll
-        for (int r = 1; r < S; ++r)
-            v[i][0].x += v[i][r].x, v[i][0].y += v[i][r].y, v[i][0].z += v[i][r].z, v[i][0].w += v[i][r].w;
-        if (failed) v[i][0] = make_float4(0.f, 0.f, 0.f, 0.f);
-        store_block(a, row0 + j + i * step, g, nb, lane, v[i][0]);
-    }
+        if (i < rows) store_block(a, row0 + j + i * step, g, nb, lane, failed ? make_float4(0.f, 0.f, 0.f, 0.f) : sum[i]);
 }
 
 // Tile: 128 weight rows x BN rows of a.  The MMA's M is the weights' side, so that few rows of a cost few columns.  A tile's
 // blocks of 128 along k are shared by the CTAs of a cluster, whose sums are added in rank order.
-// Warp 0: copies, warp 1: products, the others: sums.
+// Warp 0: copies, warp 1: products, warps 2-5: sums, a thread a weight row's.
 template <int BN>
-__global__ void __launch_bounds__(few_threads<BN>()) gemm_q8_few_kernel(const __grid_constant__ CUtensorMap wmap,
+__global__ void __launch_bounds__(kFewThreads, 2) gemm_q8_few_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                         const __grid_constant__ CUtensorMap amap,
                                                                         const __grid_constant__ GemmArgs a) {
-    constexpr int NA = few_accumulators<BN>(), EW = few_sum_warps<BN>(), COLS = BN * 4 / EW;  // rows of a for each warp of sums
+    constexpr int NA = kFewAcc;
     constexpr uint32_t kStage = few_stage_bytes<BN>();
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(few_threads<BN>()) gemm_q8_few_kernel(const __
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], EW);
+            mbar_init(&acc_empty[i], 4);
         }
         mbar_init(drained, 1);
         *stop = 0;
@@ -288,20 +287,20 @@ __global__ void __launch_bounds__(few_threads<BN>()) gemm_q8_few_kernel(const __
         mbar_wait_bounded(drained, 0, kWaitLimitNs);
     } else {
         pdl_wait();
-        const int t = threadIdx.x - 64, j0 = (warp - 2) / 4 * COLS;
-        const uint32_t column = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j0;
-        uint64_t acc[COLS / 2];
+        const int t = threadIdx.x - 64;
+        const uint32_t column = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        uint64_t acc[BN / 2];
 #pragma unroll
-        for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
-        // the products of scales of the CTA's block chunk * 8 + e % 8 and row e / 8, e = t, t + 32 EW ..
-        constexpr int PER = BN * kChunk / (32 * EW);
+        for (int j = 0; j < BN / 2; ++j) acc[j] = 0ull;
+        // the products of scales of the CTA's block chunk * 8 + e % 8 and row e / 8, e = t, t + 128 ..
+        constexpr int PER = BN * kChunk / 128;
         float next[PER];
         const float* sa = a.a_scale + (long long)g * a.nkb;
         const float* sw = a.w_scale + ((long long)g * a.nnb + nb) * a.nkb;
         const auto fetch = [&](int i0) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int e = t + 32 * EW * i, row = row0 + e / kChunk, j = i0 + e % kChunk, kb = rank + j * a.splits;
+                const int e = t + 128 * i, row = row0 + e / kChunk, j = i0 + e % kChunk, kb = rank + j * a.splits;
                 next[i] = row < a.m && j < count ? sa[(long long)row * a.a_scale_ld + kb] * __ldg(sw + kb) : 0.f;
             }
         };
@@ -315,55 +314,37 @@ __global__ void __launch_bounds__(few_threads<BN>()) gemm_q8_few_kernel(const __
             if (c == 0) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int e = t + 32 * EW * i;
+                    const int e = t + 128 * i;
                     sc[(e % kChunk) * BN + e / kChunk] = next[i];
                 }
-                named_bar_sync(1, 32 * EW);
+                named_bar_sync(1, 128);
                 fetch(j + kChunk);
             }
             live = live && __all_sync(0xffffffffu, wait_or_stop(&acc_full[b], aph, stop, a));
             if (!live) continue;
             tc_fence_after();
-            const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(sc + c * BN + j0);  // four rows' scales each
+            const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(sc + c * BN);  // four rows' scales each
             const uint32_t from = column + b * BN;
-            const auto done = [&]() {
-                tc_fence_before();
-                if (lane == 0) mbar_arrive(&acc_empty[b]);
-            };
-            if constexpr (COLS == 16) {
-                float p[16];
-                tmem_ld_nowait<16>(from, p);
-                tmem_wait_ld();
-                tmem_regs_after_wait<16>(p);
-                done();
+            uint32_t p[BN];
+            if constexpr (BN == 16) tmem_ld_nowait<16>(from, reinterpret_cast<float(&)[16]>(p));
+            else tmem_ld32_nowait(from, p);
+            tmem_wait_ld();
+            if constexpr (BN == 16) tmem_regs_after_wait<16>(reinterpret_cast<float(&)[16]>(p));
+            else regs_after_wait(p);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&acc_empty[b]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const ulonglong2 f = s2[q];
-                    fma2(acc[2 * q], __float_as_uint(p[4 * q]), __float_as_uint(p[4 * q + 1]), f.x);
-                    fma2(acc[2 * q + 1], __float_as_uint(p[4 * q + 2]), __float_as_uint(p[4 * q + 3]), f.y);
-                }
-            } else {
-                uint32_t p[COLS / 32][32];
-#pragma unroll
-                for (int h = 0; h < COLS / 32; ++h) tmem_ld32_nowait(from + 32 * h, p[h]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int h = 0; h < COLS / 32; ++h) regs_after_wait(p[h]);
-                done();
-#pragma unroll
-                for (int q = 0; q < COLS / 4; ++q) {
-                    const ulonglong2 f = s2[q];
-                    const uint32_t* v = p[q / 8] + 4 * (q % 8);
-                    fma2(acc[2 * q], v[0], v[1], f.x);
-                    fma2(acc[2 * q + 1], v[2], v[3], f.y);
-                }
+            for (int q = 0; q < BN / 4; ++q) {
+                const ulonglong2 f = s2[q];
+                fma2(acc[2 * q], p[4 * q], p[4 * q + 1], f.x);
+                fma2(acc[2 * q + 1], p[4 * q + 2], p[4 * q + 3], f.y);
             }
             if (++b == NA) b = 0, aph ^= 1;
         }
         // every product has ended, so the stages are free
-        float* to = part + j0 * 128 + 32 * (warp & 3) + lane;
+        float* to = part + 32 * (warp & 3) + lane;
 #pragma unroll
-        for (int j = 0; j < COLS / 2; ++j) {
+        for (int j = 0; j < BN / 2; ++j) {
             to[2 * j * 128] = __uint_as_float((uint32_t)acc[j]);
             to[(2 * j + 1) * 128] = __uint_as_float((uint32_t)(acc[j] >> 32));
         }
@@ -378,12 +359,14 @@ __global__ void __launch_bounds__(few_threads<BN>()) gemm_q8_few_kernel(const __
     bool failed = false;  // a wait expired in one of the CTAs: zeros
     for (int r = 0; r < a.splits; ++r) failed |= ld_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(stop)), r)) != 0u;
     failed = __any_sync(0xffffffffu, failed);
-    const int end = min(BN, a.m - row0), step = a.splits * (few_threads<BN>() / 32);
-    for (int j = rank + a.splits * warp; j < end; j += 8 / a.splits * step) {
-        if (a.splits == 1) join_rows<1>(a, part, j, step, end, row0, g, nb, lane, failed);
-        else if (a.splits == 2) join_rows<2>(a, part, j, step, end, row0, g, nb, lane, failed);
-        else if (a.splits == 4) join_rows<4>(a, part, j, step, end, row0, g, nb, lane, failed);
-        else join_rows<8>(a, part, j, step, end, row0, g, nb, lane, failed);
+    const int end = min(BN, a.m - row0), step = a.splits * (kFewThreads / 32);
+    for (int j = rank + a.splits * warp; j < end;) {
+        const int rows = min((end - j + step - 1) / step, a.splits >= 4 ? 1 : 4 / a.splits);
+        if (a.splits == 1) join_rows<1>(a, part, j, step, rows, row0, g, nb, lane, failed);
+        else if (a.splits == 2) join_rows<2>(a, part, j, step, rows, row0, g, nb, lane, failed);
+        else if (a.splits == 4) join_rows<4>(a, part, j, step, rows, row0, g, nb, lane, failed);
+        else join_rows<8>(a, part, j, step, rows, row0, g, nb, lane, failed);
+        j += rows * step;
     }
     // The others may still read this CTA's sums.  What a thread has read it has used, so nothing needs to be released (a
     // release here waits for the outputs: 2 us).
@@ -767,19 +750,39 @@ struct GemmPlan {
     int splits;  // CTAs that share a tile: its blocks of k, or (a pair) its rows
 };
 
-__host__ constexpr int few_ctas_per_sm(int rows);
+constexpr int kFewCtasPerSm = 2;
 
+// The form with the least estimated time.  A round of CTAs takes a fixed time and one for each block of k; both were fitted to
+// in-graph times over cold weights on 152 SMs (us).  Outputs x k, rows: the best forms (rows of a tile x CTAs that share it),
+// and what they were taken for:
+//   4,096 x 4,096       1: 16x8 6.0, 16x4 6.1, 16x1 9.7;  64: 32x4 7.3, 32x2 8.5, pairs 16.7;  256: 32x1 13.5, pairs 17.7;
+//                       400: pairs 17.8, 32x1 25.6
+//   4,096 x 16,384      32: 32x8 14.2, 32x4 16.0;  64: 32x4 15.7, 32x2 21.1, pairs 53.6;  400: pairs 54.8, 32x1 83.0
+//   8 x 1,024 x 4,096   32: 32x4 9.1, 32x2 10.7;  100: 32x1 13.7, pairs 17.9;  160: pairs 18.3, 32x1 24.5
+//   32,768 x 4,096      32: 32x1 23.8, 32x2 27.5, 16x1 28.0;  64: 32x1 30.3, pairs 33.8;  100: pairs 35.0
+// The bytes of the weights bound every form; among those that they bound alike the one with the least work of its own is taken.
+// Tiles of 64 and 128 rows (one CTA an SM, a block 0.3 and 0.53 us) were best nowhere but at 160 to 256 rows of 4,096 x 16,384
+// (128x2 39.8 us, 32x1 42.6), and are not built.
 static GemmPlan plan_gemm(int m, int n, int k, int groups) {
-    GemmPlan p{};
-    p.feat = kFeat;
     const long long sms = sm_count();
-    if (m > 128 && (long long)groups * ((m + 255) / 256) * ((n + 255) / 256) >= sms / 2) return GemmPlan{256, 256, 2};
-    p.rows = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-    const long long tiles = (long long)groups * row_blocks(n) * ((m + p.rows - 1) / p.rows);
-    const int nkb = row_blocks(k), most = p.rows >= 128 ? 4 : 8;
-    p.splits = 1;
-    while (p.splits < most && tiles * p.splits * 2 <= few_ctas_per_sm(p.rows) * sms && nkb >= 4 * p.splits) p.splits *= 2;
-    return p;
+    const int nkb = row_blocks(k);
+    const double bytes_us = 3.5 + ((double)groups * n * k + (double)groups * m * k) / 6.0e6;
+    const long long wide_tiles = (long long)groups * ((m + 255ll) / 256) * ((n + 255ll) / 256);
+    const auto rounds = [](long long items, long long at_once) { return (double)((items + at_once - 1) / at_once); };
+    const auto cost = [&](double work) { return std::max(work, bytes_us) + 0.02 * work; };
+    GemmPlan best{256, 256, 2};
+    double least = cost(3.2 + rounds(wide_tiles, sms / 2) * (2.0 + 0.388 * nkb));
+    for (int rows = 16; rows <= 32; rows *= 2) {
+        const long long tiles = (long long)groups * row_blocks(n) * ((m + rows - 1ll) / rows);
+        for (int splits = 1; splits <= 8 && (splits == 1 || nkb >= 2 * splits); splits *= 2) {
+            // clusters of eight leave some SMs of a GPC out
+            const long long at_once = (splits == 8 ? sms * 27 / 32 : sms) * kFewCtasPerSm;
+            const double us = cost(rounds(tiles * splits, at_once) *
+                                   (4.5 + (splits > 1 ? 0.7 : 0.0) + (rows == 16 ? 0.16 : 0.235) * ((nkb + splits - 1) / splits)));
+            if (us < least) best = GemmPlan{kFeat, rows, splits}, least = us;
+        }
+    }
+    return best;
 }
 
 // Codes [z][y][x] (x contiguous) in boxes of 128 x values and `rows` of the dimension `box_dim`, one of the other.
@@ -795,13 +798,10 @@ static bool make_codes_map(CUtensorMap* map, const void* base, long long x, long
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs that an SM holds at once: registers allow one of 128 rows, shared memory and TMEM two of fewer.
-__host__ constexpr int few_ctas_per_sm(int rows) { return rows >= 128 ? 1 : 2; }
-
 template <int BN>
 static dsa_status_t launch_few(const CUtensorMap& wmap, const CUtensorMap& amap, GemmArgs a, cudaStream_t st) {
     constexpr int extra = 1024 + 2 * kChunk * BN * 4 + 512;
-    constexpr int budget = few_ctas_per_sm(BN) == 2 ? 228 * 1024 / 2 - 1024 : 227 * 1024;
+    constexpr int budget = 228 * 1024 / kFewCtasPerSm - 1024;
     a.stages = std::min(12, (budget - extra) / few_stage_bytes<BN>());
     const int smem = extra + a.stages * few_stage_bytes<BN>();
     static_assert((budget - extra) / few_stage_bytes<BN>() * few_stage_bytes<BN>() >= BN * 512, "the sums fit into the stages");
@@ -809,7 +809,7 @@ static dsa_status_t launch_few(const CUtensorMap& wmap, const CUtensorMap& amap,
         return DSA_ERR_CUDA;
     const long long grid = (long long)a.groups * a.tiles_n * a.tiles_m * a.splits;
     if (grid > 0x7fffffff) return DSA_ERR_UNSUPPORTED;
-    if (launch_pdl_cluster(gemm_q8_few_kernel<BN>, dim3((unsigned)grid), dim3(few_threads<BN>()), smem, st, a.splits, wmap,
+    if (launch_pdl_cluster(gemm_q8_few_kernel<BN>, dim3((unsigned)grid), dim3(kFewThreads), smem, st, a.splits, wmap,
                            amap, a) != cudaSuccess)
         return DSA_ERR_CUDA;
     return launch_status();
@@ -884,12 +884,7 @@ static dsa_status_t gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, con
         return DSA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (p.feat == 256) return launch_wide(wmap, amap, args, st);
-    switch (p.rows) {
-        case 16: return launch_few<16>(wmap, amap, args, st);
-        case 32: return launch_few<32>(wmap, amap, args, st);
-        case 64: return launch_few<64>(wmap, amap, args, st);
-        default: return launch_few<128>(wmap, amap, args, st);
-    }
+    return p.rows == 16 ? launch_few<16>(wmap, amap, args, st) : launch_few<32>(wmap, amap, args, st);
 }
 
 }  // namespace dsa

@@ -154,9 +154,17 @@ def new_out(m, groups, n, fmt):
 SHAPES = [(1, 1, 16, 1), (1, 520, 4096, 1), (3, 130, 144, 2), (16, 128, 128, 1), (17, 257, 272, 3), (32, 1024, 4096, 8),
           (33, 96, 1040, 1), (64, 384, 512, 1), (65, 1000, 1040, 1), (130, 300, 2064, 2), (300, 640, 384, 1),
           (2, 4096, 8192, 1), (48, 512, 16400, 1), (127, 2, 48, 5), (5, 129, 1024, 1),
+          # every number of CTAs that share a tile, of 16 and of 32 rows
+          (3, 2000, 2048, 8), (1, 64, 1040, 1), (1, 64, 2048, 1), (17, 4096, 128, 8), (20, 2000, 4096, 8), (17, 520, 1040, 8),
+          (31, 256, 2048, 8),
           # tiles of 256 x 256 by pairs: one round of tiles and several, ends inside a tile, a half and a block
           (2560, 2048, 144, 1), (5000, 1000, 400, 1), (700, 300, 272, 16), (19500, 130, 1168, 1), (513, 520, 16, 13),
           (4100, 2900, 2064, 1)]
+
+
+def test_gemm_shapes_reach_every_form():
+    plans = {dsa.dsa_gemm_q8_plan(*s) for s in SHAPES}
+    assert plans >= {(128, rows, share) for rows in (16, 32) for share in (1, 2, 4, 8)} | {(256, 256, 2)}
 
 
 @pytest.mark.parametrize("m,n,k,groups", SHAPES)
@@ -245,7 +253,7 @@ def test_gemm_two_calls_give_the_same_bits_and_streams():
         check_gemm(*d, o, None)
 
 
-@pytest.mark.parametrize("m,n,k", [(4, 256, 4096), (100, 200, 512), (1200, 1024, 1040)])
+@pytest.mark.parametrize("m,n,k", [(4, 256, 4096), (100, 200, 512), (2100, 2048, 1040)])
 def test_gemm_bounded_waits_expire_then_the_next_call_is_correct(m, n, k):
     g = gen(12)
     a, a_scale = rows8(g, m, 1, k)
