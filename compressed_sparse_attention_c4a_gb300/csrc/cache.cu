@@ -5,8 +5,11 @@
 // [P2] "DeepSeek V4 稀疏注意力完全解剖" 设计 1 (256 raw positions per logical block) and 第三层 (prefill keeps the cache
 // in bf16, decode quantises it row by row): the caches that a prefill hands over are stored row by row in the decode
 // format, and stored rows can be had back as bf16 values.
+#include <algorithm>
+
 #include "common.cuh"
 #include "rows.cuh"
+#include "rows8.cuh"
 
 namespace dsa {
 
@@ -273,7 +276,126 @@ __device__ __forceinline__ void rotate_row(float (&v)[E], int lane, const RopeTa
     }
 }
 
-// A warp takes R consecutive rows, one after the other from the registers that their loads, in flight together, fill.
+// The pool row (-1: none) and position of new row j0 + lane, for the `live` rows of a warp.
+template <int R>
+__device__ __forceinline__ void append_places(const CacheAppendArgs& a, long long j0, int live, int lane, long long* prow, long long* pos) {
+    *prow = -1, *pos = 0;
+    if (live <= 0) return;
+    int r = request_of(a.cu_new, a.batch, (int)j0, lane);
+    if constexpr (R > 1) {
+        const int last = request_of(a.cu_new, a.batch, (int)j0 + live - 1, lane);
+        for (int hi = last + 1; hi - r > 1;) {  // between the two
+            const int mid = (r + hi) / 2;
+            if (__ldg(a.cu_new + mid) <= j0 + lane) r = mid;
+            else hi = mid;
+        }
+    }
+    if (lane >= live) return;
+    const int start = __ldg(a.start_pos + r);
+    *pos = (long long)start + (j0 + lane - __ldg(a.cu_new + r));
+    if (start >= 0 && *pos >= 0 && DSA_IDX_OK(r, a.batch, a.status)) *prow = pool_row(a.bt, r, (uint32_t)*pos, a.pool);
+    if (*prow >= 0 && !DSA_IDX_OK(*prow, pool_rows(a.pool), a.status)) *prow = -1;
+}
+
+// Rows of 512 into bf16 or e4m3 pools.  Lane l holds dims 128 i + 4 l .. + 3, so that the 32 pairs of the rotation lie two to
+// a lane in sixteen lanes.
+template <int R, bool NORM, bool FP8>
+__global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __grid_constant__ CacheAppendArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int total = min(a.n, __ldg(a.cu_new + a.batch));
+    float g[16];
+    if constexpr (NORM) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float* src = a.gamma + 128 * i + 4 * lane;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g[4 * i + k] = a.gamma ? __ldg(src + k) : 1.f;
+        }
+    }
+    const int pairs = a.rope.rope_dim / 2;
+    const int p0 = 2 * lane - 64 + pairs;  // the first of the lane's two pairs among the rotated ones
+    bool waited = false;
+    for (long long j0 = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * R;; j0 += (long long)gridDim.x * (kRowThreads / 32) * R) {
+        const int live = (int)min((long long)R, total - j0);
+        long long prow, pos;
+        append_places<R>(a, j0, live, lane, &prow, &pos);
+        if (!waited) {
+            pdl_wait();
+            pdl_launch_dependents();
+            waited = true;
+        }
+        if (live <= 0) return;
+        if (lane < live && prow < 0) report(a.status, DSA_ERR_DEVICE_FAULT);
+        uint2 u[R][4];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i < live && DSA_IDX_OK(j0 + i, a.n, a.status)) {
+                const uint16_t* src = a.x + (j0 + i) * a.x_ld + 4 * lane;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) u[i][c] = *reinterpret_cast<const uint2*>(src + 128 * c);
+            }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const long long to = __shfl_sync(0xffffffffu, prow, i), at = __shfl_sync(0xffffffffu, pos, i);
+            if (i >= live || to < 0) continue;
+            float v[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                v[4 * c] = __uint_as_float(u[i][c].x << 16), v[4 * c + 1] = __uint_as_float(u[i][c].x & 0xffff0000u);
+                v[4 * c + 2] = __uint_as_float(u[i][c].y << 16), v[4 * c + 3] = __uint_as_float(u[i][c].y & 0xffff0000u);
+            }
+            if constexpr (NORM) {
+                float ss = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) ss = fmaf(v[k], v[k], ss);
+                const float rs = rsqrtf(warp_sum(ss) / 512.f + a.eps);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] *= rs * g[k];
+            }
+            if (pairs > 0) {
+                float c = 1.f, s = 0.f;
+                if (lane < pairs) rope_cos_sin(at, a.rope, lane, &c, &s);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float ck = __shfl_sync(0xffffffffu, c, (p0 + k) & 31), sk = __shfl_sync(0xffffffffu, s, (p0 + k) & 31);
+                    if (p0 + k >= 0) {
+                        const float x0 = v[12 + 2 * k], x1 = v[13 + 2 * k];
+                        v[12 + 2 * k] = x0 * ck - x1 * sk;
+                        v[13 + 2 * k] = x0 * sk + x1 * ck;
+                    }
+                }
+            }
+            if constexpr (!FP8) {
+                uint16_t* dst = static_cast<uint16_t*>(a.pool.data) + to * 512 + 4 * lane;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint2*>(dst + 128 * c) = make_uint2(bf16x2(v[4 * c], v[4 * c + 1]), bf16x2(v[4 * c + 2], v[4 * c + 3]));
+            } else {
+                float m = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(v[k]));
+                const float amax = __uint_as_float(warp_abs_max_bits(__float_as_uint(m)));  // (fmaxf passes over NaN)
+                const float scale = amax > 0.f ? amax / 448.f : 1.f;
+                if (scale < 0x1p-100f) {  // its reciprocal could leave fp32's range
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] /= scale;
+                } else {
+                    const BlockQuotient q(scale);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = q(v[k]);
+                }
+                uint8_t* dst = static_cast<uint8_t*>(a.pool.data) + to * 512 + 4 * lane;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint32_t*>(dst + 128 * c) = e4m3x4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                if (lane == 0) a.pool.scale[to] = scale;
+            }
+        }
+    }
+}
+
+// Any pool of rows of DIM.  A warp takes R consecutive rows, one after the other from the registers that their loads, in flight
+// together, fill.
 template <int DIM, int R, bool NORM>
 __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
     constexpr int E = DIM / 32;
@@ -281,25 +403,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
     const long long j0 = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * R;
     const int total = min(a.n, __ldg(a.cu_new + a.batch));
     const int live = (int)min((long long)R, total - j0);
-    long long prow = -1;  // lane i < live: of row j0 + i
-    long long pos = 0;
-    if (live > 0) {
-        int r = request_of(a.cu_new, a.batch, (int)j0, lane);
-        if constexpr (R > 1) {
-            const int last = request_of(a.cu_new, a.batch, (int)j0 + live - 1, lane);
-            for (int hi = last + 1; hi - r > 1;) {  // between the two
-                const int mid = (r + hi) / 2;
-                if (__ldg(a.cu_new + mid) <= j0 + lane) r = mid;
-                else hi = mid;
-            }
-        }
-        if (lane < live) {
-            const int start = __ldg(a.start_pos + r);
-            pos = (long long)start + (j0 + lane - __ldg(a.cu_new + r));
-            if (start >= 0 && pos >= 0 && DSA_IDX_OK(r, a.batch, a.status)) prow = pool_row(a.bt, r, (uint32_t)pos, a.pool);
-            if (prow >= 0 && !DSA_IDX_OK(prow, pool_rows(a.pool), a.status)) prow = -1;
-        }
-    }
+    long long prow, pos;
+    append_places<R>(a, j0, live, lane, &prow, &pos);
     float g[E];
     if constexpr (NORM) {
 #pragma unroll
@@ -335,8 +440,15 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
 template <int DIM, bool NORM>
 static cudaError_t launch_append(const CacheAppendArgs& a, cudaStream_t st) {
     const bool four = rows_per_warp(a.n) == 4;
-    const dim3 grid((unsigned)((a.n + (four ? 31ll : 7ll)) / (four ? 32 : 8))), block(kRowThreads);
-    return launch_pdl(four ? cache_append_kernel<DIM, 4, NORM> : cache_append_kernel<DIM, 1, NORM>, grid, block, 0, st, a);
+    const long long ctas = (a.n + (four ? 31ll : 7ll)) / (four ? 32 : 8);
+    const dim3 block(kRowThreads);
+    if (DIM == 512 && (a.pool.dtype == DSA_BF16 || a.pool.dtype == DSA_FP8_E4M3)) {
+        const bool fp8 = a.pool.dtype == DSA_FP8_E4M3;
+        const dim3 grid((unsigned)std::min<long long>(ctas, 8ll * sm_count()));
+        return fp8 ? launch_pdl(four ? cache_append_wide_kernel<4, NORM, true> : cache_append_wide_kernel<1, NORM, true>, grid, block, 0, st, a)
+                   : launch_pdl(four ? cache_append_wide_kernel<4, NORM, false> : cache_append_wide_kernel<1, NORM, false>, grid, block, 0, st, a);
+    }
+    return launch_pdl(four ? cache_append_kernel<DIM, 4, NORM> : cache_append_kernel<DIM, 1, NORM>, dim3((unsigned)ctas), block, 0, st, a);
 }
 
 static dsa_status_t check_rows(const dsa_pool_t* pool, const dsa_block_table_t* bt) {
