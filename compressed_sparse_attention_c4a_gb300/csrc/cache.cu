@@ -257,13 +257,21 @@ struct CacheAppendArgs {
     bool wide;  // rows of x 32-byte aligned
 };
 
+// The lane's frequency as a table's first, kept in registers: a kernel argument indexed by the lane is fetched lane by lane, and
+// the compiler would fetch it again for every row (131,072 rows: 71 us against 42).
+__device__ __forceinline__ void own_frequency(const RopeTable& all, int lane, RopeTable& own) {
+    own.f_hi[0] = all.f_hi[lane], own.f_lo[0] = all.f_lo[lane];
+    asm volatile("" : "+f"(own.f_hi[0]), "+f"(own.f_lo[0]));
+}
+
 // Rotates the pairs of the last rope_dim dims by R_pos.  A lane finds the angle of one pair, whatever lanes hold it: the
 // E / 2 pairs of a lane one after the other would leave the lanes without pairs idle (rows of 512: four lanes hold them all).
+// own: a table whose first frequency is the lane's.
 template <int E>
-__device__ __forceinline__ void rotate_row(float (&v)[E], int lane, const RopeTable& rt, long long pos) {
-    const int pairs = rt.rope_dim / 2, first = E * 32 - rt.rope_dim;
+__device__ __forceinline__ void rotate_row(float (&v)[E], int lane, const RopeTable& own, int rope_dim, long long pos) {
+    const int pairs = rope_dim / 2, first = E * 32 - rope_dim;
     float c = 1.f, s = 0.f;
-    if (lane < pairs) rope_cos_sin(pos, rt, lane, &c, &s);
+    if (lane < pairs) rope_cos_sin(pos, own, 0, &c, &s);
 #pragma unroll
     for (int k = 0; k < E; k += 2) {
         const int d = lane * E + k, j = (d - first) / 2;
@@ -276,121 +284,150 @@ __device__ __forceinline__ void rotate_row(float (&v)[E], int lane, const RopeTa
     }
 }
 
-// The pool row (-1: none) and position of new row j0 + lane, for the `live` rows of a warp.
-template <int R>
-__device__ __forceinline__ void append_places(const CacheAppendArgs& a, long long j0, int live, int lane, long long* prow, long long* pos) {
+// The pool row (-1: none) and position of new row j0 + lane * apart, for the `live` rows of a warp.
+__device__ __forceinline__ void append_places(const CacheAppendArgs& a, long long j0, long long apart, int live, int lane,
+                                              long long* prow, uint32_t* pos) {
     *prow = -1, *pos = 0;
     if (live <= 0) return;
     int r = request_of(a.cu_new, a.batch, (int)j0, lane);
-    if constexpr (R > 1) {
-        const int last = request_of(a.cu_new, a.batch, (int)j0 + live - 1, lane);
-        for (int hi = last + 1; hi - r > 1;) {  // between the two
+    const long long j = j0 + lane * apart;
+    if (lane >= live) return;
+    if (live > 1)
+        for (int hi = a.batch; hi - r > 1;) {
             const int mid = (r + hi) / 2;
-            if (__ldg(a.cu_new + mid) <= j0 + lane) r = mid;
+            if (__ldg(a.cu_new + mid) <= j) r = mid;
             else hi = mid;
         }
-    }
-    if (lane >= live) return;
     const int start = __ldg(a.start_pos + r);
-    *pos = (long long)start + (j0 + lane - __ldg(a.cu_new + r));
-    if (start >= 0 && *pos >= 0 && DSA_IDX_OK(r, a.batch, a.status)) *prow = pool_row(a.bt, r, (uint32_t)*pos, a.pool);
+    *pos = (uint32_t)start + (uint32_t)(j - __ldg(a.cu_new + r));  // below 2^32
+    if (start >= 0 && DSA_IDX_OK(r, a.batch, a.status)) *prow = pool_row(a.bt, r, *pos, a.pool);
     if (*prow >= 0 && !DSA_IDX_OK(*prow, pool_rows(a.pool), a.status)) *prow = -1;
 }
 
+constexpr int kAppendAhead = 2;  // rows of a warp on their way
+
 // Rows of 512 into bf16 or e4m3 pools.  Lane l holds dims 128 i + 4 l .. + 3, so that the 32 pairs of the rotation lie two to
-// a lane in sixteen lanes.
-template <int R, bool NORM, bool FP8>
+// a lane in sixteen lanes.  The warps take the rows in turn, two of a warp's on their way into shared memory while it works on
+// one; the places of a warp's next eight rows are found by eight lanes side by side.  131,072 rows normed into e4m3 (1,540 bytes
+// each) take 40.4 us, 5.0 TB/s: bound by the issue slots (70 % busy), of about 250 instructions a row.
+template <bool NORM, bool FP8>
 __global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __grid_constant__ CacheAppendArgs a) {
     const int lane = threadIdx.x & 31;
     const int total = min(a.n, __ldg(a.cu_new + a.batch));
-    float g[16];
+    uint64_t g[8];
     if constexpr (NORM) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float* src = a.gamma + 128 * i + 4 * lane;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) g[4 * i + k] = a.gamma ? __ldg(src + k) : 1.f;
+        for (int i = 0; i < 8; ++i) {
+            const float* src = a.gamma + 128 * (i / 2) + 4 * lane + 2 * (i % 2);
+            g[i] = a.gamma ? pair2(__ldg(src), __ldg(src + 1)) : pair2(1.f, 1.f);
         }
     }
     const int pairs = a.rope.rope_dim / 2;
+    RopeTable own;
+    own_frequency(a.rope, lane, own);
     const int p0 = 2 * lane - 64 + pairs;  // the first of the lane's two pairs among the rotated ones
-    bool waited = false;
-    for (long long j0 = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * R;; j0 += (long long)gridDim.x * (kRowThreads / 32) * R) {
-        const int live = (int)min((long long)R, total - j0);
-        long long prow, pos;
-        append_places<R>(a, j0, live, lane, &prow, &pos);
-        if (!waited) {
-            pdl_wait();
-            pdl_launch_dependents();
-            waited = true;
+    __shared__ alignas(16) uint4 ring[kRowThreads / 32][kAppendAhead][64];
+    uint4(*mine)[64] = ring[threadIdx.x >> 5];
+    const auto request = [&](long long j, int slot) {  // a group of copies, empty behind the last row
+        if (j < total && DSA_IDX_OK(j, a.n, a.status)) {
+            const uint16_t* src = a.x + j * a.x_ld + 8 * lane;
+            cp_async16_nc(smem_u32(&mine[slot][lane]), src, 16);
+            cp_async16_nc(smem_u32(&mine[slot][lane + 32]), src + 256, 16);
         }
-        if (live <= 0) return;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    constexpr int kTogether = 8;  // rows whose places are found together
+    const long long warps = (long long)gridDim.x * (kRowThreads / 32);
+    long long j0 = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5), prow;
+    const auto rows_from = [&](long long j) { return j < total ? (int)min((long long)kTogether, (total - 1 - j) / warps + 1) : 0; };
+    uint32_t pos;
+    int live = rows_from(j0);
+    append_places(a, j0, warps, live, lane, &prow, &pos);
+    pdl_wait();
+    pdl_launch_dependents();
+#pragma unroll
+    for (int i = 0; i < kAppendAhead; ++i) request(j0 + i * warps, i);
+    int slot = 0;
+    while (live > 0) {
         if (lane < live && prow < 0) report(a.status, DSA_ERR_DEVICE_FAULT);
-        uint2 u[R][4];
+#pragma unroll 1
+        for (int i = 0; i < live; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAppendAhead - 1) : "memory");
+            __syncwarp();
+            uint2 u[4];
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (i < live && DSA_IDX_OK(j0 + i, a.n, a.status)) {
-                const uint16_t* src = a.x + (j0 + i) * a.x_ld + 4 * lane;
+            for (int c = 0; c < 4; ++c) u[c] = reinterpret_cast<const uint2*>(mine[slot])[32 * c + lane];
+            __syncwarp();
+            request(j0 + (i + kAppendAhead) * warps, slot);
+            if (++slot == kAppendAhead) slot = 0;
+            const long long to = __shfl_sync(0xffffffffu, prow, i);
+            const uint32_t at = __shfl_sync(0xffffffffu, pos, i);
+            if (to < 0) continue;
+            uint64_t v[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) u[i][c] = *reinterpret_cast<const uint2*>(src + 128 * c);
-            }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const long long to = __shfl_sync(0xffffffffu, prow, i), at = __shfl_sync(0xffffffffu, pos, i);
-            if (i >= live || to < 0) continue;
-            float v[16];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                v[4 * c] = __uint_as_float(u[i][c].x << 16), v[4 * c + 1] = __uint_as_float(u[i][c].x & 0xffff0000u);
-                v[4 * c + 2] = __uint_as_float(u[i][c].y << 16), v[4 * c + 3] = __uint_as_float(u[i][c].y & 0xffff0000u);
-            }
+            for (int c = 0; c < 4; ++c) v[2 * c] = pair_of_bf16(u[c].x), v[2 * c + 1] = pair_of_bf16(u[c].y);
+            float rs = 1.f;  // the norm's factor: taken into the end, as it is one for the row
             if constexpr (NORM) {
-                float ss = 0.f;
+                uint64_t s2 = mul2(v[0], v[0]);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) ss = fmaf(v[k], v[k], ss);
-                const float rs = rsqrtf(warp_sum(ss) / 512.f + a.eps);
+                for (int k = 1; k < 8; ++k) s2 = fma2(v[k], v[k], s2);
+                rs = rsqrtf(warp_sum(lo_of(s2) + hi_of(s2)) / 512.f + a.eps);
+                if (FP8 && !(rs > 0x1p-60f && rs < 0x1p60f)) {  // a row of huge or tiny values, an infinity or a NaN
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] *= rs * g[k];
+                    for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], pair2(rs, rs));
+                    rs = 1.f;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], FP8 ? g[k] : mul2(g[k], pair2(rs, rs)));
             }
             if (pairs > 0) {
                 float c = 1.f, s = 0.f;
-                if (lane < pairs) rope_cos_sin(at, a.rope, lane, &c, &s);
+                if (lane < pairs) rope_cos_sin((long long)at, own, 0, &c, &s);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float ck = __shfl_sync(0xffffffffu, c, (p0 + k) & 31), sk = __shfl_sync(0xffffffffu, s, (p0 + k) & 31);
-                    if (p0 + k >= 0) {
-                        const float x0 = v[12 + 2 * k], x1 = v[13 + 2 * k];
-                        v[12 + 2 * k] = x0 * ck - x1 * sk;
-                        v[13 + 2 * k] = x0 * sk + x1 * ck;
-                    }
+                    const float x0 = lo_of(v[6 + k]), x1 = hi_of(v[6 + k]);
+                    if (p0 + k >= 0) v[6 + k] = pair2(x0 * ck - x1 * sk, x0 * sk + x1 * ck);
                 }
             }
             if constexpr (!FP8) {
                 uint16_t* dst = static_cast<uint16_t*>(a.pool.data) + to * 512 + 4 * lane;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint2*>(dst + 128 * c) = make_uint2(bf16x2(v[4 * c], v[4 * c + 1]), bf16x2(v[4 * c + 2], v[4 * c + 3]));
+                    *reinterpret_cast<uint2*>(dst + 128 * c) =
+                        make_uint2(bf16x2(lo_of(v[2 * c]), hi_of(v[2 * c])), bf16x2(lo_of(v[2 * c + 1]), hi_of(v[2 * c + 1])));
             } else {
                 float m = 0.f;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(v[k]));
+                for (int k = 0; k < 8; ++k) m = fmaxf(m, fmaxf(fabsf(lo_of(v[k])), fabsf(hi_of(v[k]))));
                 const float amax = __uint_as_float(warp_abs_max_bits(__float_as_uint(m)));  // (fmaxf passes over NaN)
-                const float scale = amax > 0.f ? amax / 448.f : 1.f;
-                if (scale < 0x1p-100f) {  // its reciprocal could leave fp32's range
+                float scale;
+                if (amax > 0x1p-60f && amax < 0x1p60f) {
+                    const float q = amax * (1.f / 448.f);  // amax / 448 by a reciprocal and a correction
+                    scale = fmaf(fmaf(-q, 448.f, amax), 1.f / 448.f, q);
+                    if constexpr (NORM) {  // the values are rounded already: a product with the reciprocal is near enough
+                        const float r = near_reciprocal(scale);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] /= scale;
-                } else {
-                    const BlockQuotient q(scale);
+                        for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], pair2(r, r));
+                    } else {
+                        const BlockQuotient2 quotient(scale);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = q(v[k]);
+                        for (int k = 0; k < 8; ++k) v[k] = quotient(v[k]);
+                    }
+                } else {  // parts of which could leave fp32's normal range
+                    scale = amax > 0.f ? amax / 448.f : 1.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = pair2(lo_of(v[k]) / scale, hi_of(v[k]) / scale);
                 }
                 uint8_t* dst = static_cast<uint8_t*>(a.pool.data) + to * 512 + 4 * lane;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint32_t*>(dst + 128 * c) = e4m3x4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-                if (lane == 0) a.pool.scale[to] = scale;
+                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint32_t*>(dst + 128 * c) = e4m3x4(v[2 * c], v[2 * c + 1]);
+                if (lane == 0) a.pool.scale[to] = amax > 0.f ? scale * rs : 1.f;
             }
         }
+        j0 += live * warps;
+        live = rows_from(j0);
+        append_places(a, j0, warps, live, lane, &prow, &pos);
     }
 }
 
@@ -403,8 +440,9 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
     const long long j0 = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * R;
     const int total = min(a.n, __ldg(a.cu_new + a.batch));
     const int live = (int)min((long long)R, total - j0);
-    long long prow, pos;
-    append_places<R>(a, j0, live, lane, &prow, &pos);
+    long long prow;
+    uint32_t pos;
+    append_places(a, j0, 1, live, lane, &prow, &pos);
     float g[E];
     if constexpr (NORM) {
 #pragma unroll
@@ -414,13 +452,16 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
     pdl_launch_dependents();
     if (live <= 0) return;
     if (lane < live && prow < 0) report(a.status, DSA_ERR_DEVICE_FAULT);
+    RopeTable own;
+    own_frequency(a.rope, lane, own);
     uint32_t u[R][E / 2];
 #pragma unroll
     for (int i = 0; i < R; ++i)
         if (i < live && DSA_IDX_OK(j0 + i, a.n, a.status)) load_bf16_words<E>(a.x + (j0 + i) * a.x_ld, lane, u[i], a.wide);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const long long to = __shfl_sync(0xffffffffu, prow, i), at = __shfl_sync(0xffffffffu, pos, i);
+        const long long to = __shfl_sync(0xffffffffu, prow, i);
+        const uint32_t at = __shfl_sync(0xffffffffu, pos, i);
         if (i >= live || to < 0) continue;
         float v[E];
         bf16_words<E>(u[i], v);
@@ -432,23 +473,22 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
 #pragma unroll
             for (int k = 0; k < E; ++k) v[k] *= rs * g[k];
         }
-        rotate_row<E>(v, lane, a.rope, at);
+        rotate_row<E>(v, lane, own, a.rope.rope_dim, (long long)at);
         store_row<E>(a.pool, to, lane, v);
     }
 }
 
 template <int DIM, bool NORM>
 static cudaError_t launch_append(const CacheAppendArgs& a, cudaStream_t st) {
-    const bool four = rows_per_warp(a.n) == 4;
-    const long long ctas = (a.n + (four ? 31ll : 7ll)) / (four ? 32 : 8);
     const dim3 block(kRowThreads);
     if (DIM == 512 && (a.pool.dtype == DSA_BF16 || a.pool.dtype == DSA_FP8_E4M3)) {
-        const bool fp8 = a.pool.dtype == DSA_FP8_E4M3;
-        const dim3 grid((unsigned)std::min<long long>(ctas, 8ll * sm_count()));
-        return fp8 ? launch_pdl(four ? cache_append_wide_kernel<4, NORM, true> : cache_append_wide_kernel<1, NORM, true>, grid, block, 0, st, a)
-                   : launch_pdl(four ? cache_append_wide_kernel<4, NORM, false> : cache_append_wide_kernel<1, NORM, false>, grid, block, 0, st, a);
+        const dim3 grid((unsigned)std::min<long long>((a.n + 7ll) / 8, 3ll * sm_count()));
+        return a.pool.dtype == DSA_FP8_E4M3 ? launch_pdl(cache_append_wide_kernel<NORM, true>, grid, block, 0, st, a)
+                                            : launch_pdl(cache_append_wide_kernel<NORM, false>, grid, block, 0, st, a);
     }
-    return launch_pdl(four ? cache_append_kernel<DIM, 4, NORM> : cache_append_kernel<DIM, 1, NORM>, dim3((unsigned)ctas), block, 0, st, a);
+    const bool four = rows_per_warp(a.n) == 4;
+    const dim3 grid((unsigned)((a.n + (four ? 31ll : 7ll)) / (four ? 32 : 8)));
+    return launch_pdl(four ? cache_append_kernel<DIM, 4, NORM> : cache_append_kernel<DIM, 1, NORM>, grid, block, 0, st, a);
 }
 
 static dsa_status_t check_rows(const dsa_pool_t* pool, const dsa_block_table_t* bt) {

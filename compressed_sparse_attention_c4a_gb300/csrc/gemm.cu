@@ -441,8 +441,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int 
                  "r"(z), "r"(src)
                  : "memory");
 }
-__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // A warp's 32 rows of 128 outputs, a thread a row's.  Through shared memory, 128 bytes of each row at a time in the tensor
 // map's swizzle (eight lanes' 16 bytes lie in different banks), and from there by one bulk copy: stored by the threads
