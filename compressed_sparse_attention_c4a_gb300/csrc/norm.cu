@@ -7,7 +7,10 @@
 // for the residual stream.
 //
 // A row is read once and held in registers: eight consecutive values a thread and step, so that sixteen lanes hold a block
-// and find its largest value by shuffles.  A warp takes a row of up to 1024 values, a CTA longer ones.
+// and find its largest value by shuffles.  A warp takes a row of up to 1024 values, a CTA longer ones.  CTAs go from row to row,
+// the next rows on their way into shared memory, each thread waiting for the pieces that it copied itself.
+#include <algorithm>
+
 #include "common.cuh"
 #include "rows8.cuh"
 
@@ -39,130 +42,164 @@ __device__ __forceinline__ float row_sum(float v, float* red, int warp, int lane
     return t;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(w[k] << 16);
-        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-}
+constexpr int kNormAhead = 2;  // rows on their way
 
-// W warps to a row, V steps of 8 values a thread.  W == 1: eight rows to a CTA of eight warps.
-template <int W, int V, bool RES>
-__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) norm_q8_kernel(NormArgs a) {
+// W warps to a row, V steps of 8 values a thread, C CTAs to an SM.  W == 1: eight rows to a CTA of eight warps.
+template <int W, int V, int C, bool RES>
+__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, C) norm_q8_kernel(NormArgs a) {
+    extern __shared__ uint4 ring[];  // [warps or 1][kNormAhead][x, residual][vecs]
     __shared__ float red[3][W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = W == 1 ? lane : (int)threadIdx.x;
-    const int vecs = a.dim / 8, blocks = row_blocks(a.dim);
+    const int vecs = a.dim / 8, blocks = row_blocks(a.dim), slot_vecs = vecs * (RES ? 2 : 1);
     const long long step = (long long)gridDim.x * (W == 1 ? 8 : 1);
-    float g[V][8];
+    uint4* const mine = ring + (W == 1 ? warp * kNormAhead * slot_vecs : 0);
+    uint64_t g[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = t + i * 32 * W;
         if (c < vecs && a.gamma) {
             const float4 p = __ldg(reinterpret_cast<const float4*>(a.gamma) + 2 * c);
             const float4 q = __ldg(reinterpret_cast<const float4*>(a.gamma) + 2 * c + 1);
-            g[i][0] = p.x, g[i][1] = p.y, g[i][2] = p.z, g[i][3] = p.w;
-            g[i][4] = q.x, g[i][5] = q.y, g[i][6] = q.z, g[i][7] = q.w;
+            g[i][0] = pair2(p.x, p.y), g[i][1] = pair2(p.z, p.w), g[i][2] = pair2(q.x, q.y), g[i][3] = pair2(q.z, q.w);
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[i][k] = 1.f;
+            for (int k = 0; k < 4; ++k) g[i][k] = pair2(1.f, 1.f);
         }
     }
+    const auto request = [&](long long row, int slot) {  // a group of copies, empty behind the last row
+        if (row < a.n) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = t + i * 32 * W;
+                if (c < vecs) {
+                    cp_async16_nc(smem_u32(mine + slot * slot_vecs + c), reinterpret_cast<const uint4*>(a.x + row * a.x_ld) + c, 16);
+                    if constexpr (RES)
+                        cp_async16_nc(smem_u32(mine + slot * slot_vecs + vecs + c),
+                                      reinterpret_cast<const uint4*>(a.residual + row * a.residual_ld) + c, 16);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     pdl_wait();
     pdl_launch_dependents();
-    int turn = 0;
-    for (long long row = W == 1 ? (long long)blockIdx.x * 8 + warp : (long long)blockIdx.x; row < a.n; row += step) {
-        const uint4* xr = reinterpret_cast<const uint4*>(a.x + row * a.x_ld);
-        uint4 ux[V], ur[V];
+    long long row = W == 1 ? (long long)blockIdx.x * 8 + warp : (long long)blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < kNormAhead; ++i) request(row + i * step, i);
+    int turn = 0, slot = 0;
+    for (; row < a.n; row += step) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kNormAhead - 1) : "memory");
+        uint64_t h[V][4], s2 = 0ull;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = t + i * 32 * W;
-            ux[i] = c < vecs ? xr[c] : make_uint4(0, 0, 0, 0);
-            if constexpr (RES)
-                ur[i] = c < vecs ? reinterpret_cast<const uint4*>(a.residual + row * a.residual_ld)[c] : make_uint4(0, 0, 0, 0);
-        }
-        float h[V][8], ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            unpack8(ux[i], h[i]);
+            const uint4 u = c < vecs ? mine[slot * slot_vecs + c] : make_uint4(0, 0, 0, 0);
+            h[i][0] = pair_of_bf16(u.x), h[i][1] = pair_of_bf16(u.y), h[i][2] = pair_of_bf16(u.z), h[i][3] = pair_of_bf16(u.w);
             if constexpr (RES) {
-                float r[8];
-                unpack8(ur[i], r);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) h[i][k] += r[k];
+                const uint4 r = c < vecs ? mine[slot * slot_vecs + vecs + c] : make_uint4(0, 0, 0, 0);
+                h[i][0] = add2(h[i][0], pair_of_bf16(r.x)), h[i][1] = add2(h[i][1], pair_of_bf16(r.y));
+                h[i][2] = add2(h[i][2], pair_of_bf16(r.z)), h[i][3] = add2(h[i][3], pair_of_bf16(r.w));
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(h[i][k], h[i][k], ss);
+            for (int k = 0; k < 4; ++k) s2 = fma2(h[i][k], h[i][k], s2);
         }
+        request(row + kNormAhead * step, slot);
+        if (++slot == kNormAhead) slot = 0;
         if (a.sum) {
             uint4* to = reinterpret_cast<uint4*>(a.sum + row * a.sum_ld);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = t + i * 32 * W;
                 if (c < vecs)
-                    to[c] = make_uint4(bf16x2(h[i][0], h[i][1]), bf16x2(h[i][2], h[i][3]), bf16x2(h[i][4], h[i][5]),
-                                       bf16x2(h[i][6], h[i][7]));
+                    to[c] = make_uint4(bf16x2(lo_of(h[i][0]), hi_of(h[i][0])), bf16x2(lo_of(h[i][1]), hi_of(h[i][1])),
+                                       bf16x2(lo_of(h[i][2]), hi_of(h[i][2])), bf16x2(lo_of(h[i][3]), hi_of(h[i][3])));
             }
         }
-        ss = row_sum<W>(ss, red[turn], warp, lane);
+        const float ss = row_sum<W>(lo_of(s2) + hi_of(s2), red[turn], warp, lane);
         turn ^= 1;
         float rs;
         if (ss < INFINITY) {
             rs = 1.f / sqrtf(ss / (float)a.dim + a.eps);
         } else {  // squares beyond fp32 (or an infinity, a NaN): the same of h 2^-80, beside which eps is nothing
-            float s2 = 0.f;
+            s2 = 0ull;
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    h[i][k] *= 0x1p-80f;
-                    s2 = fmaf(h[i][k], h[i][k], s2);
+                for (int k = 0; k < 4; ++k) {
+                    h[i][k] = mul2(h[i][k], pair2(0x1p-80f, 0x1p-80f));
+                    s2 = fma2(h[i][k], h[i][k], s2);
                 }
-            s2 = row_sum<W>(s2, red[2], warp, lane);
+            const float again = row_sum<W>(lo_of(s2) + hi_of(s2), red[2], warp, lane);
             if constexpr (W > 1) __syncthreads();  // red[2] is free again
-            rs = 1.f / sqrtf(s2 / (float)a.dim);
+            rs = 1.f / sqrtf(again / (float)a.dim);
         }
+        // The norm's factor is one for the row: a block's codes are those of gamma h whatever it is, its scale has it.
+        const bool plain = rs > 0x1p-60f && rs < 0x1p60f;
         uint8_t* codes = a.out + row * a.dim;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = t + i * 32 * W;
             float amax = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                h[i][k] = h[i][k] * rs * g[i][k];
-                amax = fmaxf(amax, fabsf(h[i][k]));
+            for (int k = 0; k < 4; ++k) {
+                h[i][k] = mul2(h[i][k], g[i][k]);
+                amax = fmaxf(amax, fmaxf(fabsf(lo_of(h[i][k])), fabsf(hi_of(h[i][k]))));
             }
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float scale = block_scale8(amax);
-            const BlockQuotient q(scale);
+            float scale;
+            if (plain && amax > 0x1p-60f && amax < 0x1p60f) {
+                const float r = 448.f * near_reciprocal(amax);
+                scale = amax * rs * (1.f / 448.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[i][k] = mul2(h[i][k], pair2(r, r));
+            } else {  // parts of which could leave fp32's normal range; NaN and infinities
+                amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h[i][k] = mul2(h[i][k], pair2(rs, rs));
+                    amax = fmaxf(amax, fmaxf(fabsf(lo_of(h[i][k])), fabsf(hi_of(h[i][k]))));
+                }
+                const unsigned half = lane < 16 ? 0xffffu : 0xffff0000u;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, o));
+                scale = block_scale8(amax);
+                const BlockQuotient2 q(scale);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[i][k] = q(h[i][k]);
+            }
             if (c < vecs) {
-                reinterpret_cast<uint2*>(codes)[c] = make_uint2(e4m3x4(q(h[i][0]), q(h[i][1]), q(h[i][2]), q(h[i][3])),
-                                                                e4m3x4(q(h[i][4]), q(h[i][5]), q(h[i][6]), q(h[i][7])));
+                reinterpret_cast<uint2*>(codes)[c] = make_uint2(e4m3x4(h[i][0], h[i][1]), e4m3x4(h[i][2], h[i][3]));
                 if ((lane & 15) == 0) a.out_scale[row * blocks + c / 16] = scale;
             }
         }
     }
 }
 
+template <int W, int V, int C, bool RES>
+static cudaError_t launch_rows(const NormArgs& a, cudaStream_t st) {
+    const int rows = W == 1 ? 8 : 1, smem = rows * kNormAhead * a.dim * 2 * (RES ? 2 : 1);
+    if (cudaFuncSetAttribute(norm_q8_kernel<W, V, C, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return cudaErrorInvalidValue;
+    const long long grid = std::min<long long>((a.n + rows - 1ll) / rows, (long long)sm_count() * C);
+    return launch_pdl(norm_q8_kernel<W, V, C, RES>, dim3((unsigned)grid), dim3(W == 1 ? 256 : 32 * W), smem, st, a);
+}
+
+// What bounds it: HBM with a residual (7 bytes a value: 8,192 rows of 8,192 in 72.2 us, 6.5 TB/s, 0.97 of the copy rate; of
+// 4,096 37.9, 16,384 of 2,048 38.9, 32,768 of 512 21.2), without one (3 bytes a value: 41.3, 23.1, 24.1) the arithmetic and a
+// row's two steps, sum and codes, one after the other.  Warps to a row, steps and CTAs an SM were chosen at these sizes: rows
+// of 8,192 with a residual by eight warps in two CTAs take 83.7 us, by sixteen in one 72.2; without one 41.3 and 51.4.  Loaded
+// into registers instead of copied ahead, the first took 106.
 template <bool RES>
 static cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
-    const long long sms = sm_count();
-    const auto grid = [&](long long rows, long long per_sm) {
-        return dim3((unsigned)(rows < sms * per_sm ? rows : sms * per_sm));
-    };
-    if (a.dim <= 1024) {
-        const dim3 g = grid((a.n + 7ll) / 8, 8), b(256);
-        return a.dim <= 256   ? launch_pdl(norm_q8_kernel<1, 1, RES>, g, b, 0, st, a)
-               : a.dim <= 512 ? launch_pdl(norm_q8_kernel<1, 2, RES>, g, b, 0, st, a)
-                              : launch_pdl(norm_q8_kernel<1, 4, RES>, g, b, 0, st, a);
-    }
-    if (a.dim <= 2048) return launch_pdl(norm_q8_kernel<8, 1, RES>, grid(a.n, 8), dim3(256), 0, st, a);
-    if (a.dim <= 4096) return launch_pdl(norm_q8_kernel<8, 2, RES>, grid(a.n, 4), dim3(256), 0, st, a);
-    if (a.dim <= 8192) return launch_pdl(norm_q8_kernel<8, 4, RES>, grid(a.n, 2), dim3(256), 0, st, a);
-    return launch_pdl(norm_q8_kernel<16, 4, RES>, grid(a.n, 1), dim3(512), 0, st, a);
+    if (a.dim <= 256) return launch_rows<1, 1, 4, RES>(a, st);
+    if (a.dim <= 512) return launch_rows<1, 2, 3, RES>(a, st);
+    if (a.dim <= 1024) return launch_rows<1, 4, 2, RES>(a, st);
+    if (a.dim <= 2048) return launch_rows<RES ? 8 : 4, RES ? 1 : 2, RES ? 4 : 6, RES>(a, st);
+    if (a.dim <= 4096) return launch_rows<8, 2, RES ? 2 : 3, RES>(a, st);
+    if (a.dim <= 8192) return launch_rows<RES ? 16 : 8, RES ? 2 : 4, RES ? 1 : 2, RES>(a, st);
+    return launch_rows<16, 4, 1, RES>(a, st);
 }
 
 }  // namespace dsa
