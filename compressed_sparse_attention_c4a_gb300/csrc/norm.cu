@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, C) norm_q8_kernel(NormA
 template <int W, int V, int C, bool RES>
 static cudaError_t launch_rows(const NormArgs& a, cudaStream_t st) {
     const int rows = W == 1 ? 8 : 1, smem = rows * kNormAhead * a.dim * 2 * (RES ? 2 : 1);
-    if (cudaFuncSetAttribute(norm_q8_kernel<W, V, C, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (smem > 48 * 1024 &&  // what a kernel may have unasked
+        cudaFuncSetAttribute(norm_q8_kernel<W, V, C, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return cudaErrorInvalidValue;
     const long long grid = std::min<long long>((a.n + rows - 1ll) / rows, (long long)sm_count() * C);
     return launch_pdl(norm_q8_kernel<W, V, C, RES>, dim3((unsigned)grid), dim3(W == 1 ? 256 : 32 * W), smem, st, a);

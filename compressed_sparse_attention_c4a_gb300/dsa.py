@@ -132,20 +132,25 @@ def _check(fn, code):
         raise DsaError(fn, code)
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_OUT_FORMAT = {torch.float32: DSA_FP32, torch.bfloat16: DSA_BF16, torch.uint8: DSA_FP8_E4M3,
+               torch.float8_e4m3fn: DSA_FP8_E4M3}
+
+
 def _want(fn, ok):
     """What the C call cannot see (types, strides, devices of the tensors) is refused as it refuses an argument."""
     if not ok:
         raise DsaError(fn, DSA_ERR_INVALID_ARG)
 
 
-def _dense(t, *shape):
-    return tuple(t.shape) == shape and t.is_contiguous()
-
-
-def _here(*tensors):
-    """Every tensor (or None) on the current CUDA device, whose stream the call takes."""
-    dev = torch.cuda.current_device()
-    return all(t is None or t.get_device() == dev for t in tensors)
+def _stream_here(fn, stream, *tensors):
+    """The stream's handle, the current one if None; every tensor (or None) has to be on the current CUDA device, whose stream
+    the call takes.  (Plain lookups: these calls take as long as the smallest kernels.)"""
+    dev = torch._C._cuda_getDevice() if tensors[0].is_cuda else None
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise DsaError(fn, DSA_ERR_INVALID_ARG)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def dsa_status_string(code):
@@ -386,20 +391,17 @@ def dsa_cache_append(cu_new, start_pos, x, rope_cfg, pool_, bt, norm=False, rms_
     says so, rotated by their positions start_pos[r] + 0, 1, .. and stored at those logical rows, in the pool's format
     (see include/dsa.h)."""
     fn = "dsa_cache_append"
-    _want(fn, x.dim() == 2 and x.dtype == torch.bfloat16 and x.shape[1] == pool_.dim and (x.numel() == 0 or x.stride(1) == 1))
-    _want(fn, cu_new.dtype == torch.int32 and start_pos.dtype == torch.int32 and _dense(start_pos, start_pos.numel())
-          and _dense(cu_new, start_pos.numel() + 1))
-    _want(fn, rms_gamma is None or (rms_gamma.dtype == torch.float32 and _dense(rms_gamma, pool_.dim)))
-    _want(fn, _here(cu_new, start_pos, x, rms_gamma, dev_status))
-    ld = x.stride(0) if x.shape[0] > 1 else pool_.dim
-    code = _lib.dsa_cache_append(start_pos.numel(), _ptr(cu_new), _ptr(start_pos), x.shape[0], _ptr(x), ld,
-                                 1 if norm else 0, _ptr(rms_gamma), float(rms_eps), ctypes.byref(rope_cfg),
-                                 ctypes.byref(pool_), ctypes.byref(bt), _ptr(dev_status), _stream(stream))
-    _check(fn, code)
-
-
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    shape, stride, batch, dim = x.shape, x.stride(), start_pos.numel(), pool_.dim
+    _want(fn, len(shape) == 2 and x.dtype is _BF16 and shape[1] == dim and (stride[1] == 1 or shape[0] == 0)
+          and cu_new.dtype is _I32 and start_pos.dtype is _I32 and start_pos.shape == (batch,)
+          and start_pos.is_contiguous() and cu_new.shape == (batch + 1,) and cu_new.is_contiguous()
+          and (rms_gamma is None or (rms_gamma.dtype is _F32 and rms_gamma.shape == (dim,) and rms_gamma.is_contiguous())))
+    handle = _stream_here(fn, stream, x, cu_new, start_pos, rms_gamma, dev_status)
+    code = _lib.dsa_cache_append(batch, cu_new.data_ptr(), start_pos.data_ptr(), shape[0], x.data_ptr(),
+                                 stride[0] if shape[0] > 1 else dim, 1 if norm else 0, _ptr(rms_gamma), rms_eps,
+                                 ctypes.byref(rope_cfg), ctypes.byref(pool_), ctypes.byref(bt), _ptr(dev_status), handle)
+    if code:
+        raise DsaError(fn, code)
 
 
 def dsa_norm_q8(x, gamma, eps, out, out_scale, residual=None, sum_out=None, stream=None):
@@ -407,52 +409,55 @@ def dsa_norm_q8(x, gamma, eps, out, out_scale, residual=None, sum_out=None, stre
     h = x + residual; sum_out = h in bf16 (it may be x or residual).  x, residual, sum_out: bf16 [n][dim], rows any stride
     apart; gamma None: ones (see include/dsa.h)."""
     fn = "dsa_norm_q8"
-    _want(fn, x.dim() == 2)
-    n, dim = x.shape
-    for t in (x, residual, sum_out):
-        _want(fn, t is None or (tuple(t.shape) == (n, dim) and t.dtype == torch.bfloat16
-                                and (t.numel() == 0 or t.stride(1) == 1)))
-    _want(fn, gamma is None or (gamma.dtype == torch.float32 and _dense(gamma, dim)))
-    _want(fn, out.element_size() == 1 and _dense(out, n, dim))
-    _want(fn, out_scale.dtype == torch.float32 and _dense(out_scale, n, -(-dim // 128)))
-    _want(fn, _here(x, residual, sum_out, gamma, out, out_scale))
-    code = _lib.dsa_norm_q8(n, dim, _ptr(x), _row_stride(x), _ptr(residual), 0 if residual is None else _row_stride(residual),
-                            _ptr(gamma), float(eps), _ptr(sum_out), 0 if sum_out is None else _row_stride(sum_out), _ptr(out),
-                            _ptr(out_scale), _stream(stream))
-    _check(fn, code)
+    shape = x.shape
+    _want(fn, len(shape) == 2)
+    n, dim = shape
+    ld = [0, 0, 0]
+    for i, t in enumerate((x, residual, sum_out)):
+        if t is not None:
+            stride = t.stride()
+            _want(fn, t.dtype is _BF16 and t.shape == shape and (stride[1] == 1 or n == 0))
+            ld[i] = stride[0] if n > 1 else dim
+    _want(fn, (gamma is None or (gamma.dtype is _F32 and gamma.shape == (dim,) and gamma.is_contiguous()))
+          and out.element_size() == 1 and out.shape == shape and out.is_contiguous()
+          and out_scale.dtype is _F32 and out_scale.shape == (n, (dim + 127) // 128) and out_scale.is_contiguous())
+    handle = _stream_here(fn, stream, x, residual, sum_out, gamma, out, out_scale)
+    code = _lib.dsa_norm_q8(n, dim, x.data_ptr(), ld[0], _ptr(residual), ld[1], _ptr(gamma), eps, _ptr(sum_out), ld[2],
+                            out.data_ptr(), out_scale.data_ptr(), handle)
+    if code:
+        raise DsaError(fn, code)
 
 
-def _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale, dev_status):
+def _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale):
     """The C arguments of a product: a [m][k] or [m][groups][k] (rows any stride apart), w [n][k] or [groups][n][k]."""
-    if a.dim() == 2:
-        a, out = a.unsqueeze(1), out.unsqueeze(1)
-        a_scale = a_scale.unsqueeze(1)
-        out_scale = None if out_scale is None else out_scale.unsqueeze(1)
-    if w.dim() == 2:
-        w, w_scale = w.unsqueeze(0), w_scale.unsqueeze(0)
-    _want(fn, a.dim() == 3 and w.dim() == 3 and out.dim() == 3 and a_scale.dim() == 3)
-    m, groups, k = a.shape
-    n = w.shape[1]
-    nkb, nnb = -(-k // 128), -(-n // 128)
+    shape = a.shape
+    grouped = len(shape) == 3
+    _want(fn, grouped or len(shape) == 2)
+    m, k = shape[0], shape[-1]
+    groups = shape[1] if grouped else 1
+    shape = w.shape
+    n = shape[-2] if len(shape) > 1 else 0
+    nkb, nnb = (k + 127) // 128, (n + 127) // 128
 
-    def rows(t, cols):  # [m][groups][cols], the last two dense
-        return (tuple(t.shape) == (m, groups, cols)
-                and (t.numel() == 0 or ((cols == 1 or t.stride(2) == 1) and (groups == 1 or t.stride(1) == cols))))
+    def rows(t, cols):  # elements between the rows of t [m][groups][cols], the last two dense
+        stride = t.stride()
+        _want(fn, t.shape == ((m, groups, cols) if grouped else (m, cols))
+              and (m == 0 or ((cols == 1 or stride[-1] == 1) and (groups == 1 or stride[1] == cols))))
+        return stride[0] if m > 1 else groups * cols
 
-    def ld(t, cols):
-        return t.stride(0) if m > 1 else groups * cols
-
-    _want(fn, a.element_size() == 1 and w.element_size() == 1 and rows(a, k) and _dense(w, groups, n, k))
-    _want(fn, a_scale.dtype == torch.float32 and rows(a_scale, nkb))
-    _want(fn, w_scale.dtype == torch.float32 and _dense(w_scale, groups, nnb, nkb))
-    fmt = {torch.float32: DSA_FP32, torch.bfloat16: DSA_BF16, torch.uint8: DSA_FP8_E4M3,
-           torch.float8_e4m3fn: DSA_FP8_E4M3}.get(out.dtype)
-    _want(fn, fmt is not None and rows(out, n))
-    _want(fn, fmt != DSA_FP8_E4M3 or (out_scale is not None and out_scale.dtype == torch.float32
-                                      and _dense(out_scale, m, groups, nnb)))
-    _want(fn, _here(a, a_scale, w, w_scale, out, out_scale, dev_status))
-    return [m, n, k, groups, _ptr(a), ld(a, k), _ptr(a_scale), ld(a_scale, nkb), _ptr(w), _ptr(w_scale), fmt, _ptr(out),
-            ld(out, n), _ptr(out_scale) if fmt == DSA_FP8_E4M3 else None]
+    lead = (groups,) if len(shape) == 3 else ()
+    fmt = _OUT_FORMAT.get(out.dtype)
+    _want(fn, fmt is not None and a.element_size() == 1 and w.element_size() == 1 and (groups == 1 or lead)
+          and shape == (*lead, n, k) and w.is_contiguous() and a_scale.dtype is _F32 and w_scale.dtype is _F32
+          and w_scale.shape == (*lead, nnb, nkb) and w_scale.is_contiguous())
+    if fmt == DSA_FP8_E4M3:
+        _want(fn, out_scale is not None and out_scale.dtype is _F32 and out_scale.is_contiguous()
+              and out_scale.shape == ((m, groups, nnb) if grouped else (m, nnb)))
+        out_scale = out_scale.data_ptr()
+    else:
+        out_scale = None
+    return (m, n, k, groups, a.data_ptr(), rows(a, k), a_scale.data_ptr(), rows(a_scale, nkb), w.data_ptr(),
+            w_scale.data_ptr(), fmt, out.data_ptr(), rows(out, n), out_scale)
 
 
 def dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale=None, dev_status=None, stream=None):
@@ -460,16 +465,20 @@ def dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale=None, dev_status=None, st
     w (uint8 [groups][n][k], w_scale fp32 [groups][ceil(n / 128)][ceil(k / 128)]), into out [m][groups][n] in fp32, bf16 or
     (uint8, with out_scale [m][groups][ceil(n / 128)]) 8-bit rows.  One group: the dimension may be left out everywhere.
     (See include/dsa.h.)"""
-    args = _gemm_q8_args("dsa_gemm_q8", a, a_scale, w, w_scale, out, out_scale, dev_status)
-    _check("dsa_gemm_q8", _lib.dsa_gemm_q8(*args, _ptr(dev_status), _stream(stream)))
+    args = _gemm_q8_args("dsa_gemm_q8", a, a_scale, w, w_scale, out, out_scale)
+    handle = _stream_here("dsa_gemm_q8", stream, a, a_scale, w, w_scale, out, out_scale, dev_status)
+    code = _lib.dsa_gemm_q8(*args, _ptr(dev_status), handle)
+    if code:
+        raise DsaError("dsa_gemm_q8", code)
 
 
 def dsa_debug_gemm_q8_stalled(a, a_scale, w, w_scale, out, wait_limit_ns, out_scale=None, dev_status=None, stream=None):
     """Test hook: the product's launch with every copy withheld, so that its bounded waits run out after ``wait_limit_ns``
     (see include/dsa.h)."""
-    args = _gemm_q8_args("dsa_debug_gemm_q8_stalled", a, a_scale, w, w_scale, out, out_scale, dev_status)
-    _check("dsa_debug_gemm_q8_stalled", _lib.dsa_debug_gemm_q8_stalled(*args, int(wait_limit_ns), _ptr(dev_status),
-                                                                       _stream(stream)))
+    fn = "dsa_debug_gemm_q8_stalled"
+    args = _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale)
+    handle = _stream_here(fn, stream, a, a_scale, w, w_scale, out, out_scale, dev_status)
+    _check(fn, _lib.dsa_debug_gemm_q8_stalled(*args, int(wait_limit_ns), _ptr(dev_status), handle))
 
 
 def dsa_gemm_q8_plan(m, n, k, groups=1):

@@ -218,3 +218,112 @@ class LayerStep:
         cur.wait_stream(self.side)
         self.attend()
         return self.out
+
+
+class LayerProjections:
+    """Weights of the projections around a layer's attention, as dsa_gemm_q8 takes them: e4m3 codes (uint8) and fp32 scales
+    per 128 x 128.
+
+    norm   fp32 [hidden]: the norm in front of the projections
+    q      ([heads * 512][hidden], scales): the queries;  q_norm fp32 [512] or None
+    kv     ([512][hidden], scales): the window rows;      kv_norm fp32 [512] or None
+    o      ([groups][rank][heads / groups * 512], scales): a matrix for each group of heads, rank a multiple of 128
+    out    ([hidden][groups * rank], scales)
+    """
+
+    def __init__(self, norm, q, kv, o, out, q_norm=None, kv_norm=None, eps=1e-6):
+        self.norm, self.q, self.kv, self.o, self.out = norm, q, kv, o, out
+        self.q_norm, self.kv_norm, self.eps = q_norm, kv_norm, eps
+
+
+class ProjectedStep(LayerStep):
+    """The layer step between its projections ([P2] 全景图: projection -> Q-norm, RoPE and insert beside the compressors ->
+    attention -> inverse RoPE and fp8 -> output projection): the hidden rows of the new tokens in, the layer's addition to
+    the residual stream out.
+
+        run(x): residual += x;  8-bit rows of the norm of it;  queries and window rows projected from them;  compressors and
+        query norm;  window rows normed, rotated and appended;  indexer and top-k;  attention into 8-bit rows;  the groups'
+        products, again in 8 bits;  the output projection -> self.delta (the next layer's x)
+
+    A query for each new token (decode, or a prefill chunk).  The compressors' and the indexer's raw inputs come with the
+    case, as LayerStep's.  q is written by the compressors' launch and read by the attention before it waits for the
+    kernel ahead of it, so the window rows are appended between the two.
+    """
+
+    def __init__(self, case, proj, residual):
+        super().__init__(case)
+        spec, dev, nq = self.spec, case["q"].device, case["nq"]
+        if nq != int(sum(spec.new)):
+            raise ValueError("a query for each new token")
+        if self.two_streams or self.fused_select:
+            raise ValueError("one stream, top-k and attention apart")
+        self.proj, self.residual = proj, residual
+        hidden = residual.shape[1]
+        groups, rank, _ = proj.o[0].shape
+
+        def rows8(*shape):
+            blocks = -(-shape[-1] // 128)
+            return (torch.empty(shape, dtype=torch.uint8, device=dev),
+                    torch.empty((*shape[:-1], blocks), dtype=torch.float32, device=dev))
+
+        self.hidden8, self.hidden8_scale = rows8(nq, hidden)
+        self.q_raw = torch.empty((nq, spec.heads * spec.dim), dtype=torch.bfloat16, device=dev)
+        self.kv = torch.empty((nq, spec.dim), dtype=torch.bfloat16, device=dev)
+        self.out8, self.out8_scale = rows8(nq, groups, spec.heads // groups * spec.dim)
+        self.low8, self.low8_scale = rows8(nq, groups, rank)
+        self.delta = torch.empty((nq, hidden), dtype=torch.bfloat16, device=dev)
+        self.query = dsa.query_job(self.q_raw.view(nq, spec.heads, spec.dim), case["q"], case["q_pos"], self.rope_main,
+                                   rms_gamma=proj.q_norm, rms_eps=proj.eps)
+
+    def _jobs(self):
+        """The compressors without the window insert, which the appended rows take the place of."""
+        if self.jobs is None:
+            c, pc = self.case, self.spec.gate == "channel"
+            self.jobs = [dsa.compress_job(c["x_new"], c["z_new"], c["state_x"], c["state_z"], self.rope_main,
+                                          self.main, self.main_bt, per_channel=pc)]
+            if self.has_index and self.spec.index_compress:
+                self.jobs.append(dsa.compress_job(c["xi_new"], c["zi_new"], c["state_xi"], c["state_zi"],
+                                                  self.rope_idx, self.idx, self.idx_bt, per_channel=pc))
+        return self.jobs
+
+    def project_in(self, x):
+        p = self.proj
+        dsa.dsa_norm_q8(x, p.norm, p.eps, self.hidden8, self.hidden8_scale, residual=self.residual, sum_out=self.residual)
+        dsa.dsa_gemm_q8(self.hidden8, self.hidden8_scale, *p.q, self.q_raw, dev_status=self.status)
+        dsa.dsa_gemm_q8(self.hidden8, self.hidden8_scale, *p.kv, self.kv, dev_status=self.status)
+
+    def compress(self):
+        """Both compressors and the queries' norm and rotation in one launch, then the window rows."""
+        c = self.case
+        dsa.dsa_compress_jobs(self.kind, c["cu_new"], c["start_pos"], self.max_new, c["state_slot"], c["state_x"].shape[0],
+                              self._jobs(), dev_status=self.status, query=self.query)
+        dsa.dsa_cache_append(c["cu_new"], c["start_pos"], self.kv, self.rope_main, self.swa, self.swa_bt, norm=True,
+                             rms_gamma=self.proj.kv_norm, rms_eps=self.proj.eps, dev_status=self.status)
+
+    def attend(self, topk=None):
+        c, s = self.case, self.spec
+        tk = (self.topk if topk is None else topk) if self.has_index else None
+        dsa.dsa_sparse_attn_q8(c["q"], c["q_pos"], c["q_req"] if s.queries == "all" else None, self.kind, tk,
+                               s.topk if self.has_index else 0, self.main, self.main_bt, self.swa, self.swa_bt, s.window,
+                               SM_SCALE, self.rope_main, self.out8, self.out8_scale, self.lse, self.workspace,
+                               dev_status=self.status)
+
+    def project_out(self):
+        p, nq = self.proj, self.case["nq"]
+        dsa.dsa_gemm_q8(self.out8, self.out8_scale, *p.o, self.low8, out_scale=self.low8_scale, dev_status=self.status)
+        dsa.dsa_gemm_q8(self.low8.view(nq, -1), self.low8_scale.view(nq, -1), *p.out, self.delta, dev_status=self.status)
+
+    def launches_per_step(self):
+        """Those of the layer step, and the norm, the four products and the appended rows."""
+        n = 1 + (1 if self.max_new > 1 else 0) + (2 if self.has_index else 0) + self.attn_plan[3]
+        return n + 6
+
+    def run(self, x):
+        self.project_in(x)
+        self.compress()
+        if self.has_index:
+            self.index()
+            self.select()
+        self.attend()
+        self.project_out()
+        return self.delta

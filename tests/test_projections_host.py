@@ -81,3 +81,46 @@ def test_stalled_hook_limits_host_only():
     assert f(*args, 0, None, None) == INVALID and f(*args, 2000000001, None, None) == INVALID
     args[0] = 0
     assert f(*args, 5, None, None) == OK
+
+
+def _cpu_norm(**over):
+    n, d = 4, 256
+    args = dict(x=torch.zeros((n, d), dtype=torch.bfloat16), gamma=torch.ones(d), eps=1e-6, out=torch.zeros((n, d), dtype=torch.uint8),
+                out_scale=torch.zeros((n, 2)))
+    args.update(over)
+    return lambda: dsa.dsa_norm_q8(**args)
+
+
+def _cpu_gemm(**over):
+    args = dict(a=torch.zeros((4, 2, 256), dtype=torch.uint8), a_scale=torch.ones((4, 2, 2)), w=torch.zeros((2, 130, 256), dtype=torch.uint8),
+                w_scale=torch.ones((2, 2, 2)), out=torch.zeros((4, 2, 130)))
+    args.update(over)
+    return lambda: dsa.dsa_gemm_q8(**args)
+
+
+def _cpu_append(**over):
+    args = dict(cu_new=torch.zeros(3, dtype=torch.int32), start_pos=torch.zeros(2, dtype=torch.int32),
+                x=torch.zeros((4, 64), dtype=torch.bfloat16), rope_cfg=dsa.rope(64), pool_=dsa.DsaPool(4096, None, 4, 256, 64, 0),
+                bt=dsa.DsaBlockTable(4096, 2, 4))
+    args.update(over)
+    return lambda: dsa.dsa_cache_append(**args)
+
+
+@pytest.mark.parametrize("call", [
+    _cpu_norm(),                                                       # not on the current device
+    _cpu_norm(x=torch.zeros((4, 256))), _cpu_norm(x=torch.zeros((256, 4), dtype=torch.bfloat16).t()),
+    _cpu_norm(x=torch.zeros(256, dtype=torch.bfloat16)), _cpu_norm(gamma=torch.ones(128)), _cpu_norm(gamma=torch.ones(256).double()),
+    _cpu_norm(out=torch.zeros((4, 512), dtype=torch.uint8)[:, ::2]), _cpu_norm(out_scale=torch.zeros((4, 3))),
+    _cpu_norm(residual=torch.zeros((3, 256), dtype=torch.bfloat16)), _cpu_norm(sum_out=torch.zeros((4, 256))),
+    _cpu_gemm(), _cpu_gemm(a=torch.zeros((4, 512), dtype=torch.uint8)), _cpu_gemm(a=torch.zeros((4, 256, 2), dtype=torch.uint8).transpose(1, 2)),
+    _cpu_gemm(a=torch.zeros((4, 2, 256), dtype=torch.int32)), _cpu_gemm(a_scale=torch.ones((4, 2, 1))), _cpu_gemm(w=torch.zeros((130, 256), dtype=torch.uint8)),
+    _cpu_gemm(w=torch.zeros((2, 256, 130), dtype=torch.uint8).transpose(1, 2)), _cpu_gemm(w_scale=torch.ones((2, 2, 2)).double()),
+    _cpu_gemm(w_scale=torch.ones((2, 1, 2))), _cpu_gemm(out=torch.zeros((4, 2, 130), dtype=torch.float16)),
+    _cpu_gemm(out=torch.zeros((4, 2, 130), dtype=torch.uint8)), _cpu_gemm(out=torch.zeros((4, 130, 2)).transpose(1, 2)),
+    _cpu_append(), _cpu_append(x=torch.zeros((4, 64))), _cpu_append(x=torch.zeros((4, 128), dtype=torch.bfloat16)),
+    _cpu_append(cu_new=torch.zeros(2, dtype=torch.int32)), _cpu_append(cu_new=torch.zeros(3, dtype=torch.int64)),
+    _cpu_append(start_pos=torch.zeros(4, dtype=torch.int32)[::2]), _cpu_append(rms_gamma=torch.ones(32))])
+def test_tensors_that_the_call_cannot_see_are_refused(call):
+    with pytest.raises(dsa.DsaError) as e:
+        call()
+    assert e.value.code == INVALID
