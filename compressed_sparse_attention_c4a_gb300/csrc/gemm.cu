@@ -32,6 +32,7 @@ struct GemmArgs {
     float* out_scale;
     int format;
     int vec;           // 1: four consecutive outputs may be stored at once, 2: 16 bytes
+    int whole;         // a row's outputs end on 16 bytes
     int splits;        // CTAs of a cluster that share a tile's blocks
     int tiles_n, tiles_m;
     int stages;
@@ -112,6 +113,7 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t p0, uint32_t p1, ui
 __device__ __forceinline__ void store_block(const GemmArgs& a, int i, int g, int nb, int lane, float4 v) {
     const int j = nb * kFeat + 4 * lane, left = a.n - j;
     const long long at = (long long)i * a.out_ld + (long long)g * a.n + j;
+    if (!DSA_IDX_OK(i, a.m, a.status) || !DSA_IDX_OK(nb, a.nnb, a.status) || !DSA_IDX_OK(g, a.groups, a.status)) return;
     if (a.format == kOutQ8) {
         float x[4] = {v.x, v.y, v.z, v.w}, amax = 0.f;
 #pragma unroll
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) gemm_q8_few_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int e = t + 128 * i, row = row0 + e / kChunk, j = i0 + e % kChunk, kb = rank + j * a.splits;
-                next[i] = row < a.m && j < count ? sa[(long long)row * a.a_scale_ld + kb] * __ldg(sw + kb) : 0.f;
+                next[i] = row < a.m && j < count && DSA_IDX_OK(kb, a.nkb, a.status) ? sa[(long long)row * a.a_scale_ld + kb] * __ldg(sw + kb) : 0.f;
             }
         };
         fetch(0);
@@ -445,10 +447,12 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int 
 // A warp's 32 rows of 128 outputs, a thread a row's.  Through shared memory, 128 bytes of each row at a time in the tensor
 // map's swizzle (eight lanes' 16 bytes lie in different banks), and from there by one bulk copy: stored by the threads
 // themselves, 32 lines an instruction, the outputs took a fifth of the kernel's time.  The copy leaves out what lies beyond
-// the matrix.  Where the output's alignment admits no tensor map, the threads store value by value.
+// the matrix, but by 16 bytes: the last outputs of rows that end within 16 bytes, and outputs whose alignment admits no tensor
+// map, are stored by the threads, value by value.
 __device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap& omap, uint8_t* stage, long long row, int g,
                                            int j0, int lane, const uint64_t (&acc)[64]) {
     const int left = min(128, a.n - j0), row0 = (int)row - lane;
+    if (!DSA_IDX_OK(j0 / 128, a.nnb, a.status) || !DSA_IDX_OK(g, a.groups, a.status)) return;
     float r = 1.f, s = 0.f;  // an 8-bit row's quotients: see BlockQuotient
     if (a.format == kOutQ8) {
         float amax = 0.f;
@@ -495,7 +499,7 @@ __device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap&
             }
         }
     };
-    if (a.vec == 2) {
+    if (a.vec == 2 && (left == 128 || a.whole)) {
         if (a.format == kOutF32) pieces(std::integral_constant<int, 4>());
         else if (a.format == kOutBf16) pieces(std::integral_constant<int, 2>());
         else pieces(std::integral_constant<int, 1>());
@@ -864,7 +868,7 @@ static dsa_status_t gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, con
     if (a_ld % 16 || a_ld < (long long)groups * k || a_scale_ld < (long long)groups * nkb ||
         out_ld < (long long)groups * n)
         return DSA_ERR_INVALID_ARG;
-    if (a_ld >= (1ll << 40) || a_scale_ld >= (1ll << 40) || out_ld >= (1ll << 40)) return DSA_ERR_UNSUPPORTED;
+    if (a_ld >= (1ll << 40) || a_scale_ld >= (1ll << 40) || out_ld >= (1ll << 38)) return DSA_ERR_UNSUPPORTED;  // the tensor maps' strides
     const GemmPlan p = plan_gemm(m, n, k, groups);
     GemmArgs args{};
     args.m = m, args.n = n, args.k = k, args.groups = groups, args.nkb = nkb, args.nnb = nnb;
@@ -874,6 +878,7 @@ static dsa_status_t gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, con
     args.out = out, args.out_ld = out_ld, args.out_scale = out_scale, args.format = out_format;
     args.vec = aligned(out, 4 * size) && out_ld % 4 == 0 && (groups == 1 || n % 4 == 0) ? 1 : 0;
     if (args.vec && aligned(out, 16) && out_ld * size % 16 == 0 && (groups == 1 || (long long)n * size % 16 == 0)) args.vec = 2;
+    args.whole = (long long)n * size % 16 == 0;
     args.splits = p.splits, args.tiles_n = (n + p.feat - 1) / p.feat, args.tiles_m = (m + p.rows - 1) / p.rows;
     args.status = dev_status, args.wait_ns = wait_ns, args.withhold = withhold;
     CUtensorMap wmap, amap;

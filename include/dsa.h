@@ -559,12 +559,14 @@ dsa_status_t dsa_cache_append(int32_t batch, const int32_t* cu_new, const int32_
  *
  * n          rows (host int, >= 0; 0 is a no-op);  dim a multiple of 16, <= 16,384
  * x, residual, sum   bf16, 16-byte aligned, rows *_ld elements apart (>= dim, a multiple of 8); residual and sum may be NULL
- *            (their ld is ignored).  sum may be x or residual itself (with the same ld), and must not overlap them otherwise
+ *            (their ld is ignored).  sum may be x or residual itself (with the same ld); outputs must not overlap inputs
+ *            otherwise, nor rows of one output each other
  * gamma      [dim] fp32, 16-byte aligned, or NULL (ones);  eps > 0
  * out        [n][dim] e4m3 bytes, 16-byte aligned;  out_scale [n][ceil(dim / 128)] fp32
  * A row that holds a NaN is NaN codes throughout; one that holds an infinity has NaN there and zeros elsewhere.
- * Launched with programmatic dependent launch: gamma is read before waiting for the preceding kernel in the stream, x and
- * residual only after it.
+ * Launched with programmatic dependent launch: gamma is read before waiting for the preceding kernel in the stream, so it must
+ * not be an output of the library's call right before this one (nor of another kernel that releases its dependents early and
+ * writes it afterwards); x and residual are read only after the wait.
  */
 dsa_status_t dsa_norm_q8(int32_t n, int32_t dim, const void* x, int64_t x_ld, const void* residual, int64_t residual_ld,
                          const float* gamma, float eps, void* sum, int64_t sum_ld, uint8_t* out, float* out_scale,
@@ -588,11 +590,12 @@ dsa_status_t dsa_norm_q8(int32_t n, int32_t dim, const void* x, int64_t x_ld, co
  * out_format DSA_FP32, DSA_BF16 or DSA_FP8_E4M3 (8-bit rows of n values for each row and group)
  * out        row i, group g at element i * out_ld + g * n, out_ld >= groups * n, aligned to an element
  * out_scale  [m][groups][ceil(n / 128)] fp32 (DSA_FP8_E4M3; else ignored)
- * The result does not depend on timing: it is the same, bit for bit, whenever the same call is made again on a GPU of the same
- * size.  An output that an expired bounded wait kept from being finished is 0 (DSA_ERR_TIMEOUT).
- * Launched with programmatic dependent launch: w and w_scale are read before waiting for the preceding kernel in the stream,
- * so a preceding kernel that releases its dependents early must not write them after releasing (no kernel of this library
- * does); a and a_scale are read, and outputs written, only after the wait.  out and out_scale must not overlap an input.
+ * The result does not depend on timing: it is the same, bit for bit, whenever the same call is made again on a GPU with as many
+ * SMs (which decide how a sum is split).  An output that an expired bounded wait kept from being finished is 0 (DSA_ERR_TIMEOUT).
+ * Launched with programmatic dependent launch: w and w_scale are read before waiting for the preceding kernel in the stream, so
+ * they must not be outputs of the library's call right before this one (nor of another kernel that releases its dependents
+ * early and writes them afterwards); a and a_scale are read, and outputs written, only after the wait.  out and out_scale must
+ * not overlap an input.
  */
 dsa_status_t dsa_gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, const uint8_t* a, int64_t a_ld,
                          const float* a_scale, int64_t a_scale_ld, const uint8_t* w, const float* w_scale,
