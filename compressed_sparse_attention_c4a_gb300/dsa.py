@@ -143,13 +143,11 @@ def _want(fn, ok):
         raise DsaError(fn, DSA_ERR_INVALID_ARG)
 
 
-def _stream_here(fn, stream, *tensors):
-    """The stream's handle, the current one if None; every tensor (or None) has to be on the current CUDA device, whose stream
-    the call takes.  (Plain lookups: these calls take as long as the smallest kernels.)"""
-    dev = torch._C._cuda_getDevice() if tensors[0].is_cuda else None
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise DsaError(fn, DSA_ERR_INVALID_ARG)
+def _handle(fn, dev, stream):
+    """The stream's handle, the current one's if None, for tensors on device `dev`: the current device, whose stream the call
+    takes.  (-1: tensors on the host.  Plain lookups: these calls take as long as the smallest kernels.)"""
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise DsaError(fn, DSA_ERR_INVALID_ARG)
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
@@ -392,14 +390,20 @@ def dsa_cache_append(cu_new, start_pos, x, rope_cfg, pool_, bt, norm=False, rms_
     (see include/dsa.h)."""
     fn = "dsa_cache_append"
     shape, stride, batch, dim = x.shape, x.stride(), start_pos.numel(), pool_.dim
+    dev = x.get_device()
     _want(fn, len(shape) == 2 and x.dtype is _BF16 and shape[1] == dim and (stride[1] == 1 or shape[0] == 0)
-          and cu_new.dtype is _I32 and start_pos.dtype is _I32 and start_pos.shape == (batch,)
-          and start_pos.is_contiguous() and cu_new.shape == (batch + 1,) and cu_new.is_contiguous()
-          and (rms_gamma is None or (rms_gamma.dtype is _F32 and rms_gamma.shape == (dim,) and rms_gamma.is_contiguous())))
-    handle = _stream_here(fn, stream, x, cu_new, start_pos, rms_gamma, dev_status)
+          and cu_new.dtype is _I32 and start_pos.dtype is _I32 and start_pos.dim() == 1 and start_pos.is_contiguous()
+          and cu_new.shape == (batch + 1,) and cu_new.is_contiguous()
+          and cu_new.get_device() == dev and start_pos.get_device() == dev
+          and (rms_gamma is None or (rms_gamma.dtype is _F32 and rms_gamma.shape == (dim,) and rms_gamma.is_contiguous()
+                                     and rms_gamma.get_device() == dev))
+          and (dev_status is None or dev_status.get_device() == dev))
+    handle = _handle(fn, dev, stream)
     code = _lib.dsa_cache_append(batch, cu_new.data_ptr(), start_pos.data_ptr(), shape[0], x.data_ptr(),
-                                 stride[0] if shape[0] > 1 else dim, 1 if norm else 0, _ptr(rms_gamma), rms_eps,
-                                 ctypes.byref(rope_cfg), ctypes.byref(pool_), ctypes.byref(bt), _ptr(dev_status), handle)
+                                 stride[0] if shape[0] > 1 else dim, 1 if norm else 0,
+                                 None if rms_gamma is None else rms_gamma.data_ptr(), rms_eps, ctypes.byref(rope_cfg),
+                                 ctypes.byref(pool_), ctypes.byref(bt), None if dev_status is None else dev_status.data_ptr(),
+                                 handle)
     if code:
         raise DsaError(fn, code)
 
@@ -409,55 +413,82 @@ def dsa_norm_q8(x, gamma, eps, out, out_scale, residual=None, sum_out=None, stre
     h = x + residual; sum_out = h in bf16 (it may be x or residual).  x, residual, sum_out: bf16 [n][dim], rows any stride
     apart; gamma None: ones (see include/dsa.h)."""
     fn = "dsa_norm_q8"
-    shape = x.shape
+    shape, stride = x.shape, x.stride()
     _want(fn, len(shape) == 2)
     n, dim = shape
-    ld = [0, 0, 0]
-    for i, t in enumerate((x, residual, sum_out)):
-        if t is not None:
-            stride = t.stride()
-            _want(fn, t.dtype is _BF16 and t.shape == shape and (stride[1] == 1 or n == 0))
-            ld[i] = stride[0] if n > 1 else dim
-    _want(fn, (gamma is None or (gamma.dtype is _F32 and gamma.shape == (dim,) and gamma.is_contiguous()))
-          and out.element_size() == 1 and out.shape == shape and out.is_contiguous()
-          and out_scale.dtype is _F32 and out_scale.shape == (n, (dim + 127) // 128) and out_scale.is_contiguous())
-    handle = _stream_here(fn, stream, x, residual, sum_out, gamma, out, out_scale)
-    code = _lib.dsa_norm_q8(n, dim, x.data_ptr(), ld[0], _ptr(residual), ld[1], _ptr(gamma), eps, _ptr(sum_out), ld[2],
-                            out.data_ptr(), out_scale.data_ptr(), handle)
+    dev = x.get_device()
+    x_ld = stride[0] if n > 1 else dim
+    residual_at = sum_at = gamma_at = None
+    ok = (x.dtype is _BF16 and (stride[1] == 1 or n == 0) and out.element_size() == 1 and out.shape == shape
+          and out.is_contiguous() and out_scale.dtype is _F32 and out_scale.shape == (n, (dim + 127) // 128)
+          and out_scale.is_contiguous() and out.get_device() == dev and out_scale.get_device() == dev)
+    residual_ld = sum_ld = 0
+    if residual is not None:
+        stride = residual.stride()
+        ok = ok and (residual.dtype is _BF16 and residual.shape == shape and (stride[1] == 1 or n == 0)
+                     and residual.get_device() == dev)
+        residual_ld, residual_at = stride[0] if n > 1 else dim, residual.data_ptr()
+    if sum_out is not None:
+        stride = sum_out.stride()
+        ok = ok and (sum_out.dtype is _BF16 and sum_out.shape == shape and (stride[1] == 1 or n == 0)
+                     and sum_out.get_device() == dev)
+        sum_ld, sum_at = stride[0] if n > 1 else dim, sum_out.data_ptr()
+    if gamma is not None:
+        ok = ok and gamma.dtype is _F32 and gamma.shape == (dim,) and gamma.is_contiguous() and gamma.get_device() == dev
+        gamma_at = gamma.data_ptr()
+    _want(fn, ok)
+    code = _lib.dsa_norm_q8(n, dim, x.data_ptr(), x_ld, residual_at, residual_ld, gamma_at, eps, sum_at, sum_ld,
+                            out.data_ptr(), out_scale.data_ptr(), _handle(fn, dev, stream))
     if code:
         raise DsaError(fn, code)
 
 
-def _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale):
-    """The C arguments of a product: a [m][k] or [m][groups][k] (rows any stride apart), w [n][k] or [groups][n][k]."""
-    shape = a.shape
-    grouped = len(shape) == 3
-    _want(fn, grouped or len(shape) == 2)
-    m, k = shape[0], shape[-1]
-    groups = shape[1] if grouped else 1
-    shape = w.shape
-    n = shape[-2] if len(shape) > 1 else 0
-    nkb, nnb = (k + 127) // 128, (n + 127) // 128
-
-    def rows(t, cols):  # elements between the rows of t [m][groups][cols], the last two dense
-        stride = t.stride()
-        _want(fn, t.shape == ((m, groups, cols) if grouped else (m, cols))
-              and (m == 0 or ((cols == 1 or stride[-1] == 1) and (groups == 1 or stride[1] == cols))))
-        return stride[0] if m > 1 else groups * cols
-
-    lead = (groups,) if len(shape) == 3 else ()
-    fmt = _OUT_FORMAT.get(out.dtype)
-    _want(fn, fmt is not None and a.element_size() == 1 and w.element_size() == 1 and (groups == 1 or lead)
-          and shape == (*lead, n, k) and w.is_contiguous() and a_scale.dtype is _F32 and w_scale.dtype is _F32
-          and w_scale.shape == (*lead, nnb, nkb) and w_scale.is_contiguous())
-    if fmt == DSA_FP8_E4M3:
-        _want(fn, out_scale is not None and out_scale.dtype is _F32 and out_scale.is_contiguous()
-              and out_scale.shape == ((m, groups, nnb) if grouped else (m, nnb)))
-        out_scale = out_scale.data_ptr()
+def _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale, dev_status, stream):
+    """The C arguments of a product: a [m][k] or [m][groups][k] (rows any stride apart), w [n][k] or [groups][n][k]; those up to
+    out_scale, then dev_status and the stream."""
+    shape, lead = a.shape, w.shape
+    if len(shape) == 3:
+        m, groups, k = shape
+        nkb = (k + 127) // 128
+        want_scale, middle = (m, groups, nkb), True
     else:
-        out_scale = None
-    return (m, n, k, groups, a.data_ptr(), rows(a, k), a_scale.data_ptr(), rows(a_scale, nkb), w.data_ptr(),
-            w_scale.data_ptr(), fmt, out.data_ptr(), rows(out, n), out_scale)
+        _want(fn, len(shape) == 2)
+        (m, k), groups = shape, 1
+        nkb = (k + 127) // 128
+        want_scale, middle = (m, nkb), False
+    if len(lead) == 3:
+        n = lead[1]
+        nnb = (n + 127) // 128
+        ok = lead[0] == groups and lead[2] == k and w_scale.shape == (groups, nnb, nkb)
+    else:
+        _want(fn, len(lead) == 2 and groups == 1)
+        n = lead[0]
+        nnb = (n + 127) // 128
+        ok = lead[1] == k and w_scale.shape == (nnb, nkb)
+    dev, fmt = a.get_device(), _OUT_FORMAT.get(out.dtype)
+    ok = (ok and fmt is not None and a.element_size() == 1 and w.element_size() == 1 and w.is_contiguous()
+          and a_scale.dtype is _F32 and a_scale.shape == want_scale and w_scale.dtype is _F32 and w_scale.is_contiguous()
+          and out.shape == ((m, groups, n) if middle else (m, n)) and a_scale.get_device() == dev and w.get_device() == dev
+          and w_scale.get_device() == dev and out.get_device() == dev)
+    sa, ss, so = a.stride(), a_scale.stride(), out.stride()
+    if m and ok:   # the last dimension dense, the groups next to one another
+        ok = ((k == 1 or sa[-1] == 1) and (nkb == 1 or ss[-1] == 1) and (n == 1 or so[-1] == 1)
+              and (groups == 1 or (sa[1] == k and ss[1] == nkb and so[1] == n)))
+    scale_at = None
+    if fmt == DSA_FP8_E4M3:
+        ok = (ok and out_scale is not None and out_scale.dtype is _F32 and out_scale.is_contiguous()
+              and out_scale.shape == ((m, groups, nnb) if middle else (m, nnb)) and out_scale.get_device() == dev)
+        if ok:
+            scale_at = out_scale.data_ptr()
+    status_at = None
+    if dev_status is not None:
+        ok = ok and dev_status.get_device() == dev
+        status_at = dev_status.data_ptr()
+    _want(fn, ok)
+    many = m > 1
+    return (m, n, k, groups, a.data_ptr(), sa[0] if many else groups * k, a_scale.data_ptr(), ss[0] if many else groups * nkb,
+            w.data_ptr(), w_scale.data_ptr(), fmt, out.data_ptr(), so[0] if many else groups * n,
+            scale_at), status_at, _handle(fn, dev, stream)
 
 
 def dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale=None, dev_status=None, stream=None):
@@ -465,9 +496,8 @@ def dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale=None, dev_status=None, st
     w (uint8 [groups][n][k], w_scale fp32 [groups][ceil(n / 128)][ceil(k / 128)]), into out [m][groups][n] in fp32, bf16 or
     (uint8, with out_scale [m][groups][ceil(n / 128)]) 8-bit rows.  One group: the dimension may be left out everywhere.
     (See include/dsa.h.)"""
-    args = _gemm_q8_args("dsa_gemm_q8", a, a_scale, w, w_scale, out, out_scale)
-    handle = _stream_here("dsa_gemm_q8", stream, a, a_scale, w, w_scale, out, out_scale, dev_status)
-    code = _lib.dsa_gemm_q8(*args, _ptr(dev_status), handle)
+    args, status, handle = _gemm_q8_args("dsa_gemm_q8", a, a_scale, w, w_scale, out, out_scale, dev_status, stream)
+    code = _lib.dsa_gemm_q8(*args, status, handle)
     if code:
         raise DsaError("dsa_gemm_q8", code)
 
@@ -476,9 +506,8 @@ def dsa_debug_gemm_q8_stalled(a, a_scale, w, w_scale, out, wait_limit_ns, out_sc
     """Test hook: the product's launch with every copy withheld, so that its bounded waits run out after ``wait_limit_ns``
     (see include/dsa.h)."""
     fn = "dsa_debug_gemm_q8_stalled"
-    args = _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale)
-    handle = _stream_here(fn, stream, a, a_scale, w, w_scale, out, out_scale, dev_status)
-    _check(fn, _lib.dsa_debug_gemm_q8_stalled(*args, int(wait_limit_ns), _ptr(dev_status), handle))
+    args, status, handle = _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale, dev_status, stream)
+    _check(fn, _lib.dsa_debug_gemm_q8_stalled(*args, int(wait_limit_ns), status, handle))
 
 
 def dsa_gemm_q8_plan(m, n, k, groups=1):
