@@ -40,7 +40,8 @@ UNIT = "query-tokens/s"
 COPIES = 4
 KERNEL_SOURCES = {"index_kernel": "index_scores.cu", "attn_kernel": "attention.cu", "topk_kernel": "topk.cu",
                   "compress_kernel": "compress.cu", "attn_fp4_kernel": "attention_fp4.cu", "cache_write_kernel": "cache.cu",
-                  "cache_read_kernel": "cache.cu"}
+                  "cache_read_kernel": "cache.cu", "cache_append_wide_kernel": "cache.cu", "norm_q8_kernel": "norm.cu",
+                  "gemm_q8_few_kernel": "gemm.cu", "gemm_q8_wide_kernel": "gemm.cu"}
 
 
 def parse():

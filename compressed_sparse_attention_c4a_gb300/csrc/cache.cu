@@ -304,14 +304,16 @@ __device__ __forceinline__ void append_places(const CacheAppendArgs& a, long lon
     if (*prow >= 0 && !DSA_IDX_OK(*prow, pool_rows(a.pool), a.status)) *prow = -1;
 }
 
-constexpr int kAppendAhead = 2;  // rows of a warp on their way
-
 // Rows of 512 into bf16 or e4m3 pools.  Lane l holds dims 128 i + 4 l .. + 3, so that the 32 pairs of the rotation lie two to
-// a lane in sixteen lanes.  The warps take the rows in turn, two of a warp's on their way into shared memory while it works on
-// one; the places of a warp's next eight rows are found by eight lanes side by side.  131,072 rows normed into e4m3 (1,540 bytes
-// each) take 40.4 us, 5.0 TB/s: bound by the issue slots (70 % busy), of about 250 instructions a row.
+// a lane in sixteen lanes.  The warps take the rows in turn, the next one or two of a warp's on their way into shared memory
+// while it works on one; the places of a warp's next eight rows are found by eight lanes side by side.  131,072 rows normed into
+// e4m3 (1,540 bytes each) take 39.6 us, 5.1 TB/s: bound by the issue slots (70 % busy), of about 250 instructions a row; into
+// bf16 (2,048 bytes) 45.7, 5.9 TB/s; without the norm into e4m3 36.4.  One row on its way against two: with the norm 39.6
+// against 40.3 us and, into bf16, 45.7 against 50.1, without it 42.2 against 36.4.  Two rows to a warp, sixteen lanes each, took
+// 36.6 us for the first but longer for few rows (6,000 rows 5.2 us against 4.2, 32 rows 3.0 against 2.3).
 template <bool NORM, bool FP8>
 __global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __grid_constant__ CacheAppendArgs a) {
+    constexpr int kAppendAhead = NORM ? 1 : 2;  // rows of a warp on their way
     const int lane = threadIdx.x & 31;
     const int total = min(a.n, __ldg(a.cu_new + a.batch));
     uint64_t g[8];

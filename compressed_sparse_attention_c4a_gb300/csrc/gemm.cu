@@ -5,8 +5,9 @@
 // [P2] "DeepSeek V4 稀疏注意力完全解剖" 全景图 (the projections around the attention) and 融合点 2 (the attention's output goes
 // in fp8 into a batched product, one matrix per group of heads).
 //
-// The inner sums run in kind::f8f6f4 (fp32 accumulation in TMEM), one accumulator per block of 128; the epilogue warps
-// read each, multiply by the two scales' product and add it to sums in fp32 registers.
+// The inner sums run in kind::f8f6f4 (fp32 accumulation in TMEM), one accumulator per block of 128; warps of sums read each,
+// multiply by the two scales' product and add it to sums in fp32 registers.  (The tensor cores can scale by themselves only by
+// powers of two per 32 values; these scales are any fp32 number.)
 #include <algorithm>
 #include <type_traits>
 
@@ -187,8 +188,14 @@ __device__ __forceinline__ void join_rows(const GemmArgs& a, const float* part, 
 }
 
 // Tile: 128 weight rows x BN rows of a.  The MMA's M is the weights' side, so that few rows of a cost few columns.  A tile's
-// blocks of 128 along k are shared by the CTAs of a cluster, whose sums are added in rank order.
+// blocks of 128 along k are shared by the CTAs of a cluster, whose sums are added in rank order (no workspace, and the same
+// bits every time).
 // Warp 0: copies, warp 1: products, warps 2-5: sums, a thread a weight row's.
+// What bounds it: the weights' bytes where there are many (32 rows x 32,768 x 4,096: 23.2 us for 134 MB, 5.9 TB/s; they stream
+// at 6.5, the rest is the launch, the first copies and the end), else the chain of steps: set-up 1,100 cycles (under the first
+// copies), first copy 1,400 to 1,700, 150 to 600 a block, barrier and loads of the join 2,500 (1 x 520 x 4,096: 3.8 us; 32
+// rows in eight groups of 1,024 x 4,096, 34 MB: 9.6).
+// Two CTAs an SM: a sub-partition then holds four of their warps, of at most 128 registers.
 template <int BN>
 __global__ void __launch_bounds__(kFewThreads, 2) gemm_q8_few_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                         const __grid_constant__ CUtensorMap amap,
@@ -387,6 +394,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) gemm_q8_few_kernel(const __gri
 //
 // Warp 0: copies; warp 1: products (even CTA); warps 2, 3: the scales' products, kChunk blocks at a time; warps 4-11: sums, four
 // for each half of the outputs, a thread holding a row's 128 sums.
+//
+// What bounds it: the sums.  8,192 rows x 32,768 x 4,096 take 862 us (2.55 PFLOP/s, 1.35 times the measured bf16 rate; 784 in
+// short runs, before the clocks fall under the power limit), 2,048 rows in eight groups of 1,024 x 4,096 67 (2.05: 256 tiles
+// are 3.4 rounds of 76 pairs).  A block takes ~720 cycles, of which the products take 512 and the sums' packed FMAs 384 (three
+// register operands make one 3 cycles); timed without the sums the kernel ran at the tensor cores' rate (562 us), timed without
+// the products no faster than with them.  Tried, against 812 in the same runs: sixteen warps of 64 sums 920; products and barriers
+// for each half of the outputs 919; TMEM loads of 16 columns 863; two loads in flight 835; the next block's first load ahead of
+// this block's last sums 1,073; six stages as four; bands of 4, 8 or 16 row tiles alike.  A spilled register costs more than any
+// of these (1,114 with 124 bytes of them).
 constexpr int kWideThreads = 384;
 constexpr int kWideStages = 4;
 static_assert(kWideStages % 2 == 0, "a stage meets the same accumulator every round");
@@ -787,7 +803,7 @@ static GemmPlan plan_gemm(int m, int n, int k, int groups) {
     return best;
 }
 
-// Codes [z][y][x] (x contiguous) in boxes of 128 x values and `rows` of the dimension `box_dim`, one of the other.
+// Codes [z][y][x] (x contiguous) in boxes of 128 x box_y x box_z.
 static bool make_codes_map(CUtensorMap* map, const void* base, long long x, long long y, long long z, long long y_stride,
                            long long z_stride, int box_y, int box_z) {
     auto fn = tensor_map_encoder();
