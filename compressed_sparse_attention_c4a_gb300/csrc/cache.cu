@@ -373,14 +373,24 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __
                 uint64_t s2 = mul2(v[0], v[0]);
 #pragma unroll
                 for (int k = 1; k < 8; ++k) s2 = fma2(v[k], v[k], s2);
-                rs = rsqrtf(warp_sum(lo_of(s2) + hi_of(s2)) / 512.f + a.eps);
+                const float ss = warp_sum(lo_of(s2) + hi_of(s2));
+                rs = rsqrtf(ss / 512.f + a.eps);
+                if (!(ss < INFINITY)) {  // squares beyond fp32: the same of the values times 2^-80, beside which eps is nothing
+                    s2 = 0ull;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        v[k] = mul2(v[k], pair2(0x1p-80f, 0x1p-80f));
+                        s2 = fma2(v[k], v[k], s2);
+                    }
+                    rs = rsqrtf(warp_sum(lo_of(s2) + hi_of(s2)) / 512.f);
+                }
                 if (FP8 && !(rs > 0x1p-60f && rs < 0x1p60f)) {  // a row of huge or tiny values, an infinity or a NaN
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], pair2(rs, rs));
                     rs = 1.f;
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], FP8 ? g[k] : mul2(g[k], pair2(rs, rs)));
+                for (int k = 0; k < 8; ++k) v[k] = mul2(FP8 ? v[k] : mul2(v[k], pair2(rs, rs)), g[k]);
             }
             if (pairs > 0) {
                 float c = 1.f, s = 0.f;
@@ -471,9 +481,16 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
             float ss = 0.f;
 #pragma unroll
             for (int k = 0; k < E; ++k) ss = fmaf(v[k], v[k], ss);
-            const float rs = rsqrtf(warp_sum(ss) / (float)DIM + a.eps);
+            ss = warp_sum(ss);
+            float rs = rsqrtf(ss / (float)DIM + a.eps);
+            if (!(ss < INFINITY)) {  // as above
+                ss = 0.f;
 #pragma unroll
-            for (int k = 0; k < E; ++k) v[k] *= rs * g[k];
+                for (int k = 0; k < E; ++k) v[k] *= 0x1p-80f, ss = fmaf(v[k], v[k], ss);
+                rs = rsqrtf(warp_sum(ss) / (float)DIM);
+            }
+#pragma unroll
+            for (int k = 0; k < E; ++k) v[k] = v[k] * rs * g[k];
         }
         rotate_row<E>(v, lane, own, a.rope.rope_dim, (long long)at);
         store_row<E>(a.pool, to, lane, v);

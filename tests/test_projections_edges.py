@@ -6,7 +6,9 @@ import torch
 
 from compressed_sparse_attention_c4a_gb300 import dsa
 from oracle import projection as OP
+from oracle.codecs import e4m3_decode
 from _parity import np64
+from _rows8 import half_step
 from test_projections import (BF16, EPS, NORM_OFF, check_gemm, check_norm, gen, ints, make_pool, new_out, physical, randn, rows8,
                               run_norm, schedule, tables, weights8)
 
@@ -174,3 +176,46 @@ def test_norm_of_one_row_is_the_row_of_many():
             assert torch.equal(a[777:778], b)
         check_norm(x[777:778], r[777:778], None, *one)
     assert NORM_OFF < 1e-5
+
+
+@pytest.mark.parametrize("fmt,dim", [("bf16", 512), ("fp8", 512), ("bf16", 128), ("fp8", 64)])
+def test_append_norms_rows_of_huge_and_tiny_values(fmt, dim):
+    """Rows whose squares leave fp32 at either end, of zeros, and with one value that outweighs the others."""
+    g = gen(dim)
+    x = randn(g, 9, dim).to(torch.bfloat16)
+    x[0] = 0
+    x[1] *= 2.0 ** 70
+    x[2] *= 2.0 ** 122
+    x[3] *= 2.0 ** -100
+    x[4, 5] = 3e38
+    x[5, :] = -3.3e38
+    x[6] *= 2.0 ** 60
+    x[7] *= 2.0 ** -40
+    gamma = 1 + 0.2 * randn(g, dim)
+    cu, req, pos = schedule([250], [9])
+    bt, blocks = tables([250], [9], g)
+    pool, data, scale = make_pool(blocks, dim, fmt)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dsa.dsa_cache_append(ints(cu), ints([250]), x, dsa.rope(64), pool, dsa.block_table(bt), norm=True, rms_gamma=gamma,
+                         rms_eps=EPS, dev_status=status)
+    assert int(status) == 0
+    want = OP.append_rows(np64(x), pos, np64(gamma), EPS, True, 64)
+    off = NORM_OFF * np.abs(want)
+    tail = want[:, dim - 64:]
+    off[:, dim - 64:] = (1e-6 + NORM_OFF) * np.repeat(np.hypot(tail[:, 0::2], tail[:, 1::2]), 2, axis=1)
+    rows = physical(bt, req, pos)
+    if fmt == "bf16":
+        # Below 2^-126 the steps no longer shrink with the value: half of bf16's is 2^-134 there (row 4, whose large value makes
+        # the others 2^-123 of theirs), of fp32's 2^-150, a few times
+        tiny = np.where(np.abs(want) < 2.0 ** -125, 2.0 ** -134 + 2.0 ** -146, 0)
+        err = np.abs(np64(data[rows]) - want) - (BF16 * np.abs(want) + off * (1 + BF16) + tiny)
+        worst = np.unravel_index(np.argmax(err), err.shape)
+        assert err[worst] <= 0, (worst, err[worst], want[worst])
+    else:
+        s = np64(scale[rows])[:, None]
+        amax = np.max(np.abs(want), axis=1, keepdims=True)
+        ideal = np.where(amax > 0, amax / 448, 1.0)
+        assert (np.abs(s - ideal) <= np.max(off, axis=1, keepdims=True) / 448 + 2.0 ** -23 * ideal).all()
+        q = np.clip(want / s, -448, 448)
+        got = e4m3_decode(data[rows].cpu().numpy())
+        assert (np.abs(got - q) <= half_step(q) + off / s + 2.0 ** -22 * np.abs(q)).all()
