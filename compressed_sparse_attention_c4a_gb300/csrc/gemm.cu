@@ -395,14 +395,16 @@ __global__ void __launch_bounds__(kFewThreads, 2) gemm_q8_few_kernel(const __gri
 // Warp 0: copies; warp 1: products (even CTA); warps 2, 3: the scales' products, kChunk blocks at a time; warps 4-11: sums, four
 // for each half of the outputs, a thread holding a row's 128 sums.
 //
-// What bounds it: the sums.  8,192 rows x 32,768 x 4,096 take 862 us (2.55 PFLOP/s, 1.35 times the measured bf16 rate; 784 in
-// short runs, before the clocks fall under the power limit), 2,048 rows in eight groups of 1,024 x 4,096 67 (2.05: 256 tiles
-// are 3.4 rounds of 76 pairs).  A block takes ~720 cycles, of which the products take 512 and the sums' packed FMAs 384 (three
-// register operands make one 3 cycles); timed without the sums the kernel ran at the tensor cores' rate (562 us), timed without
-// the products no faster than with them.  Tried, against 812 in the same runs: sixteen warps of 64 sums 920; products and barriers
-// for each half of the outputs 919; TMEM loads of 16 columns 863; two loads in flight 835; the next block's first load ahead of
-// this block's last sums 1,073; six stages as four; bands of 4, 8 or 16 row tiles alike.  A spilled register costs more than any
-// of these (1,114 with 124 bytes of them).
+// What bounds it: the sums.  8,192 rows x 32,768 x 4,096 take 853 us (2.58 PFLOP/s, 1.37 times the measured bf16 rate; 735 to
+// 780 in short runs, before the clocks fall under the power limit), 2,048 rows in eight groups of 1,024 x 4,096 59 to 63 (256
+// tiles are 3.4 rounds of 76 pairs).  A block takes ~700 cycles, of which the products take 512 and the packed FMAs of both warps
+// of sums on a scheduler 384 (three register operands make one 3 cycles); the rest of a warp's turn is its wait, its factor and
+// its first load, one after the other.  Timed without the sums the kernel ran at the tensor cores' rate (562 us), timed without the
+// products no faster than with them.  Tried, in the same runs: sixteen warps of 64 sums 920 against 812; products and barriers for
+// each half of the outputs 919; TMEM loads of 16 columns 863; two loads in flight instead of one 850 against 790; scalar FMAs 850
+// against 780; last tiles cut into halves of 128 outputs: a block of a half takes 0.9 of a whole one's time; six stages as four;
+// bands of 4, 8 or 16 row tiles alike.  Registers: 136 a thread for the first four warps and 184 for the sums spill nothing; with
+// 64 and 216 it was the first four that spilled whenever a line changed (2,048 rows x 8,192 x 4,096: 57.4 us against 62 to 86).
 constexpr int kWideThreads = 384;
 constexpr int kWideStages = 4;
 static_assert(kWideStages % 2 == 0, "a stage meets the same accumulator every round");
@@ -438,8 +440,14 @@ __device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t ma
         : "memory");
 }
 // Only TMEM has been read before it, which has ended: no release at cluster scope, whose fence took most of the kernel's time.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mbar_arrive_cluster_elect(uint32_t bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 struct WideTile {
     int g, n0, m0;  // group, first output, first row
@@ -464,7 +472,7 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int 
 // map's swizzle (eight lanes' 16 bytes lie in different banks), and from there by one bulk copy: stored by the threads
 // themselves, 32 lines an instruction, the outputs took a fifth of the kernel's time.  The copy leaves out what lies beyond
 // the matrix, but by 16 bytes: the last outputs of rows that end within 16 bytes, and outputs whose alignment admits no tensor
-// map, are stored by the threads, value by value.
+// map, are stored by the threads, a lane an output.
 __device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap& omap, uint8_t* stage, long long row, int g,
                                            int j0, int lane, const uint64_t (&acc)[64]) {
     const int left = min(128, a.n - j0), row0 = (int)row - lane;
@@ -494,12 +502,16 @@ __device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap&
         else return e4m3x4(quotient(lo_of(acc[2 * w])), quotient(hi_of(acc[2 * w])), quotient(lo_of(acc[2 * w + 1])),
                            quotient(hi_of(acc[2 * w + 1])));
     };
+    const bool bulk = a.vec == 2 && (left == 128 || a.whole);
     const auto pieces = [&](auto bytes) {  // bytes an output
         constexpr int B = decltype(bytes)::value, PER = 128 / B;  // outputs in 128 bytes
 #pragma unroll
         for (int piece = 0; piece < B; ++piece) {
             uint8_t* to = stage + (piece & 1) * 4096;
-            if (lane == 0) bulk_wait_read<1>();  // the copy before the last has left this half of the stage
+            if (lane == 0) {
+                if (bulk) bulk_wait_read<1>();  // the copy before the last has left this half of the stage
+                else bulk_wait_read<0>();
+            }
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -507,30 +519,29 @@ __device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap&
                 *reinterpret_cast<uint4*>(to + lane * 128 + ((c ^ (lane & 7)) * 16)) =
                     make_uint4(word(bytes, w), word(bytes, w + 1), word(bytes, w + 2), word(bytes, w + 3));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (piece * PER < left) tma_store_3d(&omap, j0 + piece * PER, g, row0, smem_u32(to));
-                bulk_commit();
+            if (bulk) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (piece * PER < left) tma_store_3d(&omap, j0 + piece * PER, g, row0, smem_u32(to));
+                    bulk_commit();
+                }
+            } else {  // row by row, a lane an output
+                using T = std::conditional_t<B == 4, uint32_t, std::conditional_t<B == 2, uint16_t, uint8_t>>;
+                __syncwarp();
+                T* out = static_cast<T*>(a.out) + row0 * a.out_ld + (long long)g * a.n + j0 + piece * PER;
+#pragma unroll 1
+                for (int r = 0; r < min(32, a.m - row0); ++r, out += a.out_ld)
+#pragma unroll 1
+                    for (int e = lane; e < min(PER, left - piece * PER); e += 32)
+                        out[e] = *reinterpret_cast<const T*>(to + r * 128 + ((e * B / 16) ^ (r & 7)) * 16 + e * B % 16);
+                __syncwarp();
             }
         }
     };
-    if (a.vec == 2 && (left == 128 || a.whole)) {
-        if (a.format == kOutF32) pieces(std::integral_constant<int, 4>());
-        else if (a.format == kOutBf16) pieces(std::integral_constant<int, 2>());
-        else pieces(std::integral_constant<int, 1>());
-        return;
-    }
-    if (row >= a.m) return;
-    const long long at = row * a.out_ld + (long long)g * a.n + j0;
-#pragma unroll
-    for (int j = 0; j < 128; ++j) {
-        const float v = j % 2 ? hi_of(acc[j / 2]) : lo_of(acc[j / 2]);
-        if (j >= left) continue;
-        if (a.format == kOutF32) static_cast<float*>(a.out)[at + j] = v;
-        else if (a.format == kOutBf16) static_cast<uint16_t*>(a.out)[at + j] = float_to_bf16(v);
-        else static_cast<uint8_t*>(a.out)[at + j] = float_to_e4m3(quotient(v));
-    }
+    if (a.format == kOutF32) pieces(std::integral_constant<int, 4>());
+    else if (a.format == kOutBf16) pieces(std::integral_constant<int, 2>());
+    else pieces(std::integral_constant<int, 1>());
 }
 
 __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __grid_constant__ CUtensorMap wmap,
@@ -584,7 +595,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
     pdl_launch_dependents();
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
         if (warp == 0 && lane == 0 && !a.withhold) {
             int s = 0;
             uint32_t ph = 1;
@@ -691,55 +702,57 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int half = (warp - 4) >> 2;
         const int mine = 128 * (int)rank + 32 * (warp & 3) + lane;  // the thread's row of the tile
         const uint32_t column = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
-        const uint32_t drained_to[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
-        int b = 0, c = 0;
-        uint32_t aph = 0, cph = 0;
+        const uint32_t drained_to = mapa_shared(smem_u32(acc_empty), 0);
+        const uint32_t factor = smem_u32(scales) + (half * 128 + 32 * (warp & 3) + lane) * 4;
+        uint32_t b = 0, c = 0, aph = 0, cph = 0;  // the accumulator, the scales' buffer, and their parities
         bool live = true;
         for (int t = pair; t < tiles; t += pairs) {
-            const WideTile x = wide_tile(a, t);
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-            for (int kb = 0; kb < a.nkb && live; ++kb) {
-                if (kb % kChunk == 0) {
-                    live = __all_sync(0xffffffffu, wait_or_stop(&sc_full[c], cph, stop, a));
-                    if (!live) break;
-                }
-                const float f = scales[(c * kChunk + kb % kChunk) * 256 + half * 128 + 32 * (warp & 3) + lane];
-                if (kb % kChunk == kChunk - 1 || kb == a.nkb - 1) {  // the chunk's last
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_empty[c]);
-                    c ^= 1;
-                    cph ^= c == 0 ? 1u : 0u;
-                }
-                live = __all_sync(0xffffffffu, wait_or_stop(&acc_full[b], aph, stop, a));
-                if (!live) break;
-                tc_fence_after();
-                const uint32_t from = column + b * 256;
-                uint64_t f2;
-                asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
-                uint32_t p[2][32];
-                tmem_ld32_nowait(from, p[0]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tmem_wait_ld();
-                    regs_after_wait(p[q & 1]);
-                    if (q < 3) {
-                        tmem_ld32_nowait(from + 32 * (q + 1), p[(q + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive_cluster(drained_to[b]);
+            int left = a.nkb;
+#pragma unroll 1
+            while (left > 0 && live) {
+                live = __all_sync(0xffffffffu, wait_or_stop(&sc_full[c], cph, stop, a));
+                uint32_t at = factor + c * kChunk * 1024;
+                const int until = max(left - kChunk, 0);
+#pragma unroll 1
+                for (; left > until && live; --left) {
+                    const float f = ld_shared_f32(at);
+                    at += 1024;
+                    if (!__all_sync(0xffffffffu, mbar_try_wait(&acc_full[b], aph))) {
+                        live = __all_sync(0xffffffffu, wait_or_stop(&acc_full[b], aph, stop, a));
+                        if (!live) break;
                     }
+                    tc_fence_after();
+                    uint64_t f2;
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
+                    uint32_t p[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * q + j], p[q & 1][2 * j], p[q & 1][2 * j + 1], f2);
+                    for (int q = 0; q < 4; ++q) {
+                        tmem_ld32_nowait(column + b * 256 + 32 * q, p);
+                        tmem_wait_ld();
+                        regs_after_wait(p);
+                        if (q == 3) {
+                            tc_fence_before();
+                            mbar_arrive_cluster_elect(drained_to + 8 * b);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) fma2(acc[16 * q + j], p[2 * j], p[2 * j + 1], f2);
+                    }
+                    b ^= 1;
+                    aph ^= b ^ 1;
                 }
-                b ^= 1;
-                aph ^= b == 0 ? 1u : 0u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_empty[c]);
+                c ^= 1;
+                cph ^= c ^ 1;
             }
+            const WideTile x = wide_tile(a, t);
             if (!live) {  // a wait expired: this tile and the ones after it are zeros
 #pragma unroll
                 for (int j = 0; j < 64; ++j) acc[j] = 0ull;
@@ -773,9 +786,9 @@ constexpr int kFewCtasPerSm = 2;
 // The form with the least estimated time.  A round of CTAs takes a fixed time and one for each block of k; both were fitted to
 // in-graph times over cold weights on 152 SMs (us).  Outputs x k, rows: the best forms (rows of a tile x CTAs that share it),
 // and what they were taken for:
-//   4,096 x 4,096       1: 16x8 6.0, 16x4 6.1, 16x1 9.7;  64: 32x4 7.3, 32x2 8.5, pairs 16.7;  256: 32x1 13.5, pairs 17.7;
-//                       400: pairs 17.8, 32x1 25.6
-//   4,096 x 16,384      32: 32x8 14.2, 32x4 16.0;  64: 32x4 15.7, 32x2 21.1, pairs 53.6;  400: pairs 54.8, 32x1 83.0
+//   4,096 x 4,096       1: 16x8 6.0, 16x4 6.1, 16x1 9.7;  64: 32x4 7.3, 32x2 8.5, pairs 16.6;  256: 32x1 13.6, pairs 17.4;
+//                       400: pairs 17.5, 32x1 25.4
+//   4,096 x 16,384      32: 32x8 14.2, 32x4 16.0;  64: 32x4 15.7, 32x2 21.1, pairs 52.0;  400: pairs 52.4, 32x2 70.5
 //   8 x 1,024 x 4,096   32: 32x4 9.1, 32x2 10.7;  100: 32x1 13.7, pairs 17.9;  160: pairs 18.3, 32x1 24.5
 //   32,768 x 4,096      32: 32x1 23.8, 32x2 27.5, 16x1 28.0;  64: 32x1 30.3, pairs 33.8;  100: pairs 35.0
 // The bytes of the weights bound every form; among those that they bound alike the one with the least work of its own is taken.
@@ -789,7 +802,7 @@ static GemmPlan plan_gemm(int m, int n, int k, int groups) {
     const auto rounds = [](long long items, long long at_once) { return (double)((items + at_once - 1) / at_once); };
     const auto cost = [&](double work) { return std::max(work, bytes_us) + 0.02 * work; };
     GemmPlan best{256, 256, 2};
-    double least = cost(3.2 + rounds(wide_tiles, sms / 2) * (2.0 + 0.388 * nkb));
+    double least = cost(3.2 + rounds(wide_tiles, sms / 2) * (2.0 + 0.365 * nkb));
     for (int rows = 16; rows <= 32; rows *= 2) {
         const long long tiles = (long long)groups * row_blocks(n) * ((m + rows - 1ll) / rows);
         for (int splits = 1; splits <= 8 && (splits == 1 || nkb >= 2 * splits); splits *= 2) {

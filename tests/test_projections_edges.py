@@ -219,3 +219,19 @@ def test_append_norms_rows_of_huge_and_tiny_values(fmt, dim):
         q = np.clip(want / s, -448, 448)
         got = e4m3_decode(data[rows].cpu().numpy())
         assert (np.abs(got - q) <= half_step(q) + off / s + 2.0 ** -22 * np.abs(q)).all()
+
+
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("m,n,k,groups", [(2050, 2100, 400, 1), (2050, 2177, 256, 1), (2304, 2304, 1040, 1), (520, 2432, 400, 3),
+                                          (300, 900, 2576, 4)])
+def test_gemm_last_tiles(m, n, k, groups, fmt):
+    """Many rows: last tiles that have no second block of 128 outputs, or a part of either; more tiles than pairs of CTAs and
+    fewer; chunks of scales that end early."""
+    g = gen(m + n)
+    a, a_scale = rows8(g, m, groups, k)
+    w, w_scale = weights8(g, groups, n, k)
+    out, out_scale = new_out(m, groups, n, fmt)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dsa.dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale, dev_status=status)
+    assert int(status) == 0
+    check_gemm(a, a_scale, w, w_scale, out, out_scale)
