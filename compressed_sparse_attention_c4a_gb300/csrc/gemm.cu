@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) gemm_q8_few_kernel(const __gri
 // Tile: 256 rows of a x 256 outputs, by a pair of CTAs whose tensor cores work as one (cta_group::2): each CTA copies its 128
 // rows of a and its 128 weight rows, the even one issues the products, and each has its rows' sums over all 256 outputs in its
 // TMEM, two accumulators of 256 columns in turn.  Pairs go from tile to tile; the products of the next tile's first two blocks
-// run while a tile is stored.
+// run while a tile is stored.  Where the tiles leave pairs idle and the blocks are many, two pairs share a tile (SPLIT, below).
 //
 // Warp 0: copies; warp 1: products (even CTA); warps 2, 3: the scales' products, kChunk blocks at a time; warps 4-11: sums, four
 // for each half of the outputs, a thread holding a row's 128 sums.
@@ -429,8 +429,8 @@ __device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t ades
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrives at the barrier in the pair's CTAs of `mask` once the products issued so far are complete.
-__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t mask = 3) {
+// Arrives at the barrier in the cluster's CTAs of `mask` once the products issued so far are complete.
+__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t mask) {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
@@ -544,6 +544,10 @@ __device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap&
     else pieces(std::integral_constant<int, 1>());
 }
 
+// SPLIT: a cluster of two pairs shares a tile, each with half of its blocks; the first pair ends up with the first 128 outputs and
+// the second with the others, whose sums they get from one another through distributed shared memory (500 rows x 4,096 x 8,192:
+// 22.0 us against 28.9; the exchange and the two barriers around it take ~2.5).
+template <bool SPLIT>
 __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                        const __grid_constant__ CUtensorMap amap,
                                                                        const __grid_constant__ CUtensorMap omap,
@@ -563,8 +567,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int pairs = (int)(gridDim.x / 2), pair = (int)(blockIdx.x / 2);
+    const uint32_t rank = cluster_ctarank() & 1, even = cluster_ctarank() & ~1u;  // in the pair; the pair's even CTA
+    const int part = SPLIT ? (int)even / 2 : 0, share = SPLIT ? 4 : 2;            // the pair's part of the blocks; CTAs of a tile
+    const int pairs = (int)(gridDim.x / share), pair = (int)(blockIdx.x / share);
+    const int middle = (a.nkb + 7) / 8 * 4;  // a multiple of 4: scales are read four at a time
+    const int kb0 = part == 0 ? 0 : middle, kb1 = SPLIT && part == 0 ? middle : a.nkb;
     const int tiles = a.groups * a.tiles_m * a.tiles_n;
 
     if (threadIdx.x == 0) {
@@ -603,12 +610,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
             for (int t = pair; t < tiles && live; t += pairs) {
                 const WideTile x = wide_tile(a, t);
                 const int row = x.m0 + 128 * (int)rank, feat = x.n0 + 128 * (int)rank;
-                for (int kb = 0; kb < a.nkb; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_or_stop(&empty[s], ph, stop, a)) {
                         live = false;
                         break;
                     }
-                    const uint32_t st = smem_u32(base) + s * kWideStage, bar = mapa_shared(smem_u32(&full[s]), 0);
+                    const uint32_t st = smem_u32(base) + s * kWideStage, bar = mapa_shared(smem_u32(&full[s]), even);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kWideStage);
                     tma_load_3d_pair(st, &amap, kb * 128, x.g, row, bar);
                     tma_load_3d_pair(st + 128 * 128, &wmap, kb * 128, feat, x.g, bar);
@@ -626,7 +633,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
             constexpr uint32_t idesc = idesc_e4m3(256, 256);
             const uint64_t desc = rows128_desc(smem_u32(base));
             const uint32_t first = __shfl_sync(0xffffffffu, (uint32_t)desc, 0), d = __shfl_sync(0xffffffffu, tmem, 0);
-            long long left = (long long)((tiles - pair + pairs - 1) / pairs) * a.nkb;
+            long long left = (long long)((tiles - pair + pairs - 1) / pairs) * (kb1 - kb0);
             for (uint32_t ph = 0; left > 0; ph ^= 1) {
 #pragma unroll
                 for (int s = 0; s < kWideStages; ++s) {
@@ -644,12 +651,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
                     for (int ks = 0; ks < 4; ++ks)
                         mma_f8_pair_elect(d + (s & 1) * 256, desc_lo(desc, lo + 2 * ks), desc_lo(desc, lo + (128 * 128 >> 4) + 2 * ks),
                                           idesc, ks > 0 ? 1u : 0u);
-                    mma_commit_pair_elect(&acc_full[s & 1]);
-                    mma_commit_pair_elect(&empty[s]);
+                    mma_commit_pair_elect(&acc_full[s & 1], (uint16_t)(3u << even));
+                    mma_commit_pair_elect(&empty[s], (uint16_t)(3u << even));
                     --left;
                 }
             }
-            mma_commit_pair_elect(drained, 1);
+            mma_commit_pair_elect(drained, (uint16_t)(1u << even));
             mbar_wait_bounded(drained, 0, kWaitLimitNs);
         } else if (warp >= 2) {
             // Each lane two rows: their scales of kChunk blocks (32 bytes of each row), times those of the two halves' weights.
@@ -662,7 +669,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
                 const WideTile x = wide_tile(a, t);
                 const float* sw = a.w_scale + ((long long)x.g * a.nnb + x.n0 / 128) * a.nkb;
                 const bool second = x.n0 / 128 + 1 < a.nnb;
-                for (int kb = 0; kb < a.nkb; kb += kChunk) {
+                for (int kb = kb0; kb < kb1; kb += kChunk) {
                     float s[2][kChunk];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -701,12 +708,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
             }
         }
         __syncwarp();
+        if constexpr (SPLIT) {  // as the warps of sums
+            cluster_arrive_relaxed();
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int half = (warp - 4) >> 2;
         const int mine = 128 * (int)rank + 32 * (warp & 3) + lane;  // the thread's row of the tile
         const uint32_t column = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * 128;
-        const uint32_t drained_to = mapa_shared(smem_u32(acc_empty), 0);
+        const uint32_t drained_to = mapa_shared(smem_u32(acc_empty), even);
         const uint32_t factor = smem_u32(scales) + (half * 128 + 32 * (warp & 3) + lane) * 4;
         uint32_t b = 0, c = 0, aph = 0, cph = 0;  // the accumulator, the scales' buffer, and their parities
         bool live = true;
@@ -714,7 +727,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-            int left = a.nkb;
+            int left = kb1 - kb0;
 #pragma unroll 1
             while (left > 0 && live) {
                 live = __all_sync(0xffffffffu, wait_or_stop(&sc_full[c], cph, stop, a));
@@ -752,6 +765,27 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
                 c ^= 1;
                 cph ^= c ^ 1;
             }
+            if constexpr (SPLIT) {  // one tile a cluster
+                cluster_arrive_relaxed();
+                cluster_wait();  // every product of the four CTAs has ended: the stages are free
+                const int at = (32 * (warp & 3) + lane) * 16;
+                if (half != part) {
+                    const uint32_t to = mapa_shared(smem_u32(base), cluster_ctarank() ^ 2) + at;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        st_cluster_v4(to + j * 2048, lo_of(acc[2 * j]), hi_of(acc[2 * j]), lo_of(acc[2 * j + 1]), hi_of(acc[2 * j + 1]));
+                }
+                cluster_arrive();
+                cluster_wait();
+                if (half != part) continue;
+                for (int r = 0; r < 4; ++r) live = live && ld_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(stop)), r)) == 0u;
+                live = __all_sync(0xffffffffu, live);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float4 v = *reinterpret_cast<const float4*>(base + at + j * 2048);
+                    acc[2 * j] = add2(acc[2 * j], pair2(v.x, v.y)), acc[2 * j + 1] = add2(acc[2 * j + 1], pair2(v.z, v.w));
+                }
+            }
             const WideTile x = wide_tile(a, t);
             if (!live) {  // a wait expired: this tile and the ones after it are zeros
 #pragma unroll
@@ -761,14 +795,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
             if (j0 < a.n && x.m0 + 128 * (int)rank + 32 * (warp & 3) < a.m)
                 store_wide(a, omap, stage_out + (warp - 4) * kOutBytes, x.m0 + mine, x.g, j0, lane, acc);
         }
-        if (lane == 0) bulk_wait_all();
+        if (lane == 0) bulk_wait_read<0>();  // shared memory is left; the kernel's end waits for the rest
     }
     if (*stop) {  // copies that the other CTA asked for may still be on their way: they take microseconds
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < 2000000ull) {}
     }
     tc_fence_before();
-    cluster_arrive();
+    cluster_arrive_relaxed();  // no data: each thread's loads have ended, and a release would wait for the outputs
     cluster_wait();
     tc_fence_after();
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -778,7 +812,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
 struct GemmPlan {
     int feat;    // outputs of a tile: 128, or 256 by a pair of CTAs
     int rows;    // rows of a in a tile
-    int splits;  // CTAs that share a tile: its blocks of k, or (a pair) its rows
+    int splits;  // CTAs that share a tile: its blocks of k, or its rows by a pair (2), both by two pairs (4)
 };
 
 constexpr int kFewCtasPerSm = 2;
@@ -786,11 +820,13 @@ constexpr int kFewCtasPerSm = 2;
 // The form with the least estimated time.  A round of CTAs takes a fixed time and one for each block of k; both were fitted to
 // in-graph times over cold weights on 152 SMs (us).  Outputs x k, rows: the best forms (rows of a tile x CTAs that share it),
 // and what they were taken for:
-//   4,096 x 4,096       1: 16x8 6.0, 16x4 6.1, 16x1 9.7;  64: 32x4 7.3, 32x2 8.5, pairs 16.6;  256: 32x1 13.6, pairs 17.4;
-//                       400: pairs 17.5, 32x1 25.4
-//   4,096 x 16,384      32: 32x8 14.2, 32x4 16.0;  64: 32x4 15.7, 32x2 21.1, pairs 52.0;  400: pairs 52.4, 32x2 70.5
-//   8 x 1,024 x 4,096   32: 32x4 9.1, 32x2 10.7;  100: 32x1 13.7, pairs 17.9;  160: pairs 18.3, 32x1 24.5
+//   4,096 x 4,096       1: 16x8 6.0, 16x4 6.1, 16x1 9.7;  64: 32x4 7.3, 32x2 8.5, pairs 16.6;  256: 32x1 13.5, two pairs 14.3,
+//                       pairs 17.1;  500: two pairs 15.5, pairs 17.2, 32x1 26.4
+//   4,096 x 8,192       160: two pairs 20.7, 32x1 22.9, pairs 28.7;  500: two pairs 22.0, pairs 28.9, 32x1 45.6
+//   4,096 x 16,384      32: 32x8 14.2, 32x4 16.0;  64: 32x4 15.7, 32x2 21.1, pairs 52.0
+//   8 x 1,024 x 4,096   32: 32x4 9.1, 32x2 10.7;  100: 32x1 13.7, pairs 17.6;  160: two pairs 16.2, pairs 17.9, 32x1 24.5
 //   32,768 x 4,096      32: 32x1 23.8, 32x2 27.5, 16x1 28.0;  64: 32x1 30.3, pairs 33.8;  100: pairs 35.0
+//   1,000 x 1,040       500: 32x1 5.7, pairs 8.2, two pairs 10.1;  2,048: pairs 8.6, two pairs 11.2, 32x1 14.0
 // The bytes of the weights bound every form; among those that they bound alike the one with the least work of its own is taken.
 // Tiles of 64 and 128 rows (one CTA an SM, a block 0.3 and 0.53 us) were best nowhere but at 160 to 256 rows of 4,096 x 16,384
 // (128x2 39.8 us, 32x1 42.6), and are not built.
@@ -803,6 +839,10 @@ static GemmPlan plan_gemm(int m, int n, int k, int groups) {
     const auto cost = [&](double work) { return std::max(work, bytes_us) + 0.02 * work; };
     GemmPlan best{256, 256, 2};
     double least = cost(3.2 + rounds(wide_tiles, sms / 2) * (2.0 + 0.365 * nkb));
+    if (4 * wide_tiles <= sms * 27 / 32 && nkb >= 16) {  // all clusters at once
+        const double us = cost(7.8 + 0.40 * ((nkb + 7) / 8 * 4));
+        if (us < least) best = GemmPlan{256, 256, 4}, least = us;
+    }
     for (int rows = 16; rows <= 32; rows *= 2) {
         const long long tiles = (long long)groups * row_blocks(n) * ((m + rows - 1ll) / rows);
         for (int splits = 1; splits <= 8 && (splits == 1 || nkb >= 2 * splits); splits *= 2) {
@@ -865,11 +905,12 @@ static dsa_status_t launch_wide(const CUtensorMap& wmap, const CUtensorMap& amap
     }
     const long long tiles = (long long)a.groups * a.tiles_n * a.tiles_m;
     if (tiles > 0x3fffffff) return DSA_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(gemm_q8_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess)
-        return DSA_ERR_CUDA;
-    const long long pairs = std::min<long long>(tiles, sm_count() / 2);
-    if (launch_pdl_cluster(gemm_q8_wide_kernel, dim3((unsigned)(2 * pairs)), dim3(kWideThreads), kWideSmem, st, 2, wmap, amap,
-                           omap, a) != cudaSuccess)
+    const bool split = a.splits == 4;
+    const auto kernel = split ? gemm_q8_wide_kernel<true> : gemm_q8_wide_kernel<false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess) return DSA_ERR_CUDA;
+    const long long grid = split ? 4 * tiles : 2 * std::min<long long>(tiles, sm_count() / 2);
+    if (launch_pdl_cluster(kernel, dim3((unsigned)grid), dim3(kWideThreads), kWideSmem, st, a.splits, wmap, amap, omap, a) !=
+        cudaSuccess)
         return DSA_ERR_CUDA;
     return launch_status();
 }

@@ -603,8 +603,8 @@ dsa_status_t dsa_gemm_q8(int32_t m, int32_t n, int32_t k, int32_t groups, const 
 
 /*
  * dsa_gemm_q8_plan - how dsa_gemm_q8 splits the work for these sizes on the current device; host only, launches nothing.
- * plan[0] = outputs of a tile, plan[1] = rows of a tile, plan[2] = CTAs of a cluster that share a tile (its blocks along k, or
- * two halves of its outputs).  Returns DSA_ERR_INVALID_ARG / DSA_ERR_UNSUPPORTED as dsa_gemm_q8 would for these sizes (and
+ * plan[0] = outputs of a tile, plan[1] = rows of a tile, plan[2] = CTAs of a cluster that share a tile (its blocks along k; with
+ * 256 outputs two share its rows and four its rows and blocks).  Returns DSA_ERR_INVALID_ARG / DSA_ERR_UNSUPPORTED as dsa_gemm_q8 would for these sizes (and
  * DSA_ERR_INVALID_ARG for m = 0).
  */
 dsa_status_t dsa_gemm_q8_plan(int32_t m, int32_t n, int32_t k, int32_t groups, int32_t* plan);

@@ -235,3 +235,40 @@ def test_gemm_last_tiles(m, n, k, groups, fmt):
     dsa.dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale, dev_status=status)
     assert int(status) == 0
     check_gemm(a, a_scale, w, w_scale, out, out_scale)
+
+
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "fp8"])
+@pytest.mark.parametrize("m,n,k,groups", [(500, 2900, 8192, 1), (600, 2100, 4112, 1), (500, 1537, 4096, 2), (1000, 1153, 6160, 1),
+                                          (2000, 700, 5120, 1)])
+def test_gemm_blocks_shared_by_two_pairs(m, n, k, groups, fmt):
+    """Few tiles of many blocks: two pairs of CTAs share a tile's blocks and exchange their sums; ragged rows, outputs and blocks;
+    the same bits again."""
+    g = gen(m + n)
+    a, a_scale = rows8(g, m, groups, k)
+    w, w_scale = weights8(g, groups, n, k)
+    assert dsa.dsa_gemm_q8_plan(m, n, k, groups) == (256, 256, 4)
+    outs = []
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        out, out_scale = new_out(m, groups, n, fmt)
+        dsa.dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale, dev_status=status)
+        outs.append(out)
+    assert int(status) == 0
+    check_gemm(a, a_scale, w, w_scale, out, out_scale)
+    assert all(torch.equal(o.view(torch.uint8), out.view(torch.uint8)) for o in outs)
+
+
+def test_gemm_two_pairs_bounded_waits():
+    g = gen(13)
+    a, a_scale = rows8(g, 500, 1, 8192)
+    w, w_scale = weights8(g, 1, 2900, 8192)
+    assert dsa.dsa_gemm_q8_plan(500, 2900, 8192) == (256, 256, 4)
+    out, _ = new_out(500, 1, 2900, "bf16")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dsa.dsa_debug_gemm_q8_stalled(a, a_scale, w, w_scale, out, 20_000_000, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == dsa.DSA_ERR_TIMEOUT and not out.any()
+    status.zero_()
+    dsa.dsa_gemm_q8(a, a_scale, w, w_scale, out, dev_status=status)
+    check_gemm(a, a_scale, w, w_scale, out, None)
+    assert int(status) == 0
