@@ -272,3 +272,34 @@ def test_gemm_two_pairs_bounded_waits():
     dsa.dsa_gemm_q8(a, a_scale, w, w_scale, out, dev_status=status)
     check_gemm(a, a_scale, w, w_scale, out, None)
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("m,n,k,n2", [(2048, 4096, 2048, 512), (500, 4096, 8192, 1024), (33, 2048, 1024, 4096)])
+def test_products_of_products_from_a_graph(m, n, k, n2):
+    """8-bit outputs read by the next product, launched before the first has ended: the bits of calls with a wait in between."""
+    g = gen(m)
+    w, w_scale = weights8(g, 1, n, k)
+    w2, w2_scale = weights8(g, 1, n2, n)
+    inputs = [rows8(g, m, 1, k) for _ in range(3)]
+    mid, mid_scale = new_out(m, 1, n, "fp8")
+    outs = [new_out(m, 1, n2, "bf16")[0] for _ in inputs]
+
+    def chain(i, wait=lambda: None):
+        dsa.dsa_gemm_q8(*inputs[i], w, w_scale, mid, mid_scale)
+        wait()
+        dsa.dsa_gemm_q8(mid, mid_scale, w2, w2_scale, outs[i])
+        wait()
+
+    for i in range(3):
+        chain(i, torch.cuda.synchronize)
+    want = [o.clone() for o in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in list(range(3)) * 3:
+            chain(i)
+    for _ in range(10):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, x) for o, x in zip(outs, want))
