@@ -473,10 +473,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int 
 // themselves, 32 lines an instruction, the outputs took a fifth of the kernel's time.  The copy leaves out what lies beyond
 // the matrix, but by 16 bytes: the last outputs of rows that end within 16 bytes, and outputs whose alignment admits no tensor
 // map, are stored by the threads, a lane an output.
-// The stage has two halves, and a piece goes into the half that the piece before the last had: with one piece a tile (8-bit
-// outputs) the halves have to alternate from tile to tile.  turn: the half of the next piece, kept between tiles.
-__device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap& omap, uint8_t* stage, uint32_t& turn,
-                                           long long row, int g, int j0, int lane, const uint64_t (&acc)[64]) {
+__device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap& omap, uint8_t* stage, long long row, int g,
+                                           int j0, int lane, const uint64_t (&acc)[64]) {
     const int left = min(128, a.n - j0), row0 = (int)row - lane;
     if (!DSA_IDX_OK(j0 / 128, a.nnb, a.status) || !DSA_IDX_OK(g, a.groups, a.status)) return;
     float r = 1.f, s = 0.f;  // an 8-bit row's quotients: see BlockQuotient
@@ -509,10 +507,12 @@ __device__ __forceinline__ void store_wide(const GemmArgs& a, const CUtensorMap&
         constexpr int B = decltype(bytes)::value, PER = 128 / B;  // outputs in 128 bytes
 #pragma unroll
         for (int piece = 0; piece < B; ++piece) {
-            uint8_t* to = stage + turn * 4096;
-            turn ^= 1;
+            uint8_t* to = stage + (piece & 1) * 4096;
             if (lane == 0) {
-                if (bulk) bulk_wait_read<1>();  // the copy before the last has left this half of the stage
+                // The copy that went through this half of the stage has left it: the one before the last, or (8-bit outputs, one
+                // piece a tile) the last tile's.  Halves that alternate from tile to tile instead cost every format a twentieth
+                // (8,192 rows x 32,768 x 4,096 862 us against 816, eight groups of 1,024 x 4,096 64.8 against 62.2).
+                if (bulk && B > 1) bulk_wait_read<1>();
                 else bulk_wait_read<0>();
             }
             __syncwarp();
@@ -725,7 +725,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
         const uint32_t drained_to = mapa_shared(smem_u32(acc_empty), even);
         const uint32_t factor = smem_u32(scales) + (half * 128 + 32 * (warp & 3) + lane) * 4;
         uint32_t b = 0, c = 0, aph = 0, cph = 0;  // the accumulator, the scales' buffer, and their parities
-        uint32_t turn = 0;                        // the half of the stage that the next outputs go through
         bool live = true;
         for (int t = pair; t < tiles; t += pairs) {
             uint64_t acc[64];
@@ -797,7 +796,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) gemm_q8_wide_kernel(const __g
             }
             const int j0 = x.n0 + 128 * half;
             if (j0 < a.n && x.m0 + 128 * (int)rank + 32 * (warp & 3) < a.m)
-                store_wide(a, omap, stage_out + (warp - 4) * kOutBytes, turn, x.m0 + mine, x.g, j0, lane, acc);
+                store_wide(a, omap, stage_out + (warp - 4) * kOutBytes, x.m0 + mine, x.g, j0, lane, acc);
         }
         if (lane == 0) bulk_wait_read<0>();  // shared memory is left; the kernel's end waits for the rest
     }
