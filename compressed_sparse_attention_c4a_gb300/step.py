@@ -227,7 +227,8 @@ class LayerProjections:
     norm   fp32 [hidden]: the norm in front of the projections
     q      ([heads * 512][hidden], scales): the queries;  q_norm fp32 [512] or None
     kv     ([512][hidden], scales): the window rows;      kv_norm fp32 [512] or None
-    o      ([groups][rank][heads / groups * 512], scales): a matrix for each group of heads, rank a multiple of 128
+    o      ([groups][rank][heads / groups * 512], scales): a matrix for each group of heads, the heads a multiple of the groups
+           (rank a multiple of 128)
     out    ([hidden][groups * rank], scales)
     """
 
@@ -259,7 +260,10 @@ class ProjectedStep(LayerStep):
             raise ValueError("one stream, top-k and attention apart")
         self.proj, self.residual = proj, residual
         hidden = residual.shape[1]
-        groups, rank, _ = proj.o[0].shape
+        groups, rank, inner = proj.o[0].shape
+        # the attention and the query job write and read through bare pointers: sizes that do not fit are refused here
+        if spec.heads % groups or inner != spec.heads // groups * spec.dim:
+            raise ValueError("the output projection's groups share the heads evenly: [groups][rank][heads / groups * dim]")
 
         def rows8(*shape):
             blocks = -(-shape[-1] // 128)
