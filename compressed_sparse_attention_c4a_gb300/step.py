@@ -227,8 +227,8 @@ class LayerProjections:
     norm   fp32 [hidden]: the norm in front of the projections
     q      ([heads * 512][hidden], scales): the queries;  q_norm fp32 [512] or None
     kv     ([512][hidden], scales): the window rows;      kv_norm fp32 [512] or None
-    o      ([groups][rank][heads / groups * 512], scales): a matrix for each group of heads, the heads a multiple of the groups
-           (rank a multiple of 128)
+    o      ([groups][rank][heads / groups * 512], scales): a matrix for each group of heads, the heads a multiple of the groups;
+           rank a multiple of 128 where there are several (a group's part of the 8-bit rows between the products ends on a scale)
     out    ([hidden][groups * rank], scales)
     """
 
@@ -264,6 +264,8 @@ class ProjectedStep(LayerStep):
         # the attention and the query job write and read through bare pointers: sizes that do not fit are refused here
         if spec.heads % groups or inner != spec.heads // groups * spec.dim:
             raise ValueError("the output projection's groups share the heads evenly: [groups][rank][heads / groups * dim]")
+        if groups > 1 and rank % 128:
+            raise ValueError("the rank of several groups is a multiple of 128")
 
         def rows8(*shape):
             blocks = -(-shape[-1] // 128)
