@@ -266,6 +266,9 @@ class ProjectedStep(LayerStep):
             raise ValueError("the output projection's groups share the heads evenly: [groups][rank][heads / groups * dim]")
         if groups > 1 and rank % 128:
             raise ValueError("the rank of several groups is a multiple of 128")
+        if proj.q_norm is not None and (proj.q_norm.dtype != torch.float32 or proj.q_norm.shape != (spec.dim,)
+                                        or not proj.q_norm.is_contiguous() or proj.q_norm.device != dev):
+            raise ValueError("q_norm: fp32 [dim], dense, on the case's device")
 
         def rows8(*shape):
             blocks = -(-shape[-1] // 128)

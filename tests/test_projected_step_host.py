@@ -33,7 +33,8 @@ def test_buffers_fit_the_attention():
     dict(heads=64, groups=3),                              # 63 heads of 64 would fit
     dict(heads=16, groups=32, inner=512), dict(inner=4096 - 512), dict(inner=8192),
     dict(rank=200),                                        # 2 ceil(200 / 128) is ceil(400 / 128): no shape gives it away
-    dict(rank=64),
+    dict(rank=64), dict(q_norm=torch.ones(256)), dict(q_norm=torch.ones(512, dtype=torch.bfloat16)),
+    dict(q_norm=torch.ones(1024)[::2]),
     ])
 def test_refusals(args):
     with pytest.raises(ValueError):
