@@ -254,7 +254,7 @@ class ProjectedStep(LayerStep):
     def __init__(self, case, proj, residual):
         super().__init__(case)
         spec, dev, nq = self.spec, case["q"].device, case["nq"]
-        if nq != int(sum(spec.new)):
+        if nq != int(sum(spec.new)) or (spec.queries != "all" and any(n != 1 for n in spec.new)):
             raise ValueError("a query for each new token")
         if self.two_streams or self.fused_select:
             raise ValueError("one stream, top-k and attention apart")

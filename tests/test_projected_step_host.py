@@ -35,7 +35,7 @@ def test_buffers_fit_the_attention():
     dict(rank=200),                                        # 2 ceil(200 / 128) is ceil(400 / 128): no shape gives it away
     dict(rank=64), dict(q_norm=torch.ones(256)), dict(q_norm=torch.ones(512, dtype=torch.bfloat16)),
     dict(q_norm=torch.ones(1024)[::2]),
-    ])
+    dict(new=[2, 0]), dict(new=[0, 2]), dict(new=[3, 1])])  # the last token's query of each request only
 def test_refusals(args):
     with pytest.raises(ValueError):
         make(**args)
