@@ -135,6 +135,7 @@ def _check(fn, code):
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _OUT_FORMAT = {torch.float32: DSA_FP32, torch.bfloat16: DSA_BF16, torch.uint8: DSA_FP8_E4M3,
                torch.float8_e4m3fn: DSA_FP8_E4M3}
+_CODES = frozenset((torch.uint8, torch.float8_e4m3fn))   # what holds e4m3 codes
 
 
 def _want(fn, ok):
@@ -409,9 +410,9 @@ def dsa_cache_append(cu_new, start_pos, x, rope_cfg, pool_, bt, norm=False, rms_
 
 
 def dsa_norm_q8(x, gamma, eps, out, out_scale, residual=None, sum_out=None, stream=None):
-    """out, out_scale (uint8 [n][dim], fp32 [n][ceil(dim / 128)]) = the 8-bit rows of gamma * h / sqrt(mean(h^2) + eps),
-    h = x + residual; sum_out = h in bf16 (it may be x or residual).  x, residual, sum_out: bf16 [n][dim], rows any stride
-    apart; gamma None: ones (see include/dsa.h)."""
+    """out, out_scale (uint8 or float8_e4m3fn [n][dim], fp32 [n][ceil(dim / 128)]) = the 8-bit rows of
+    gamma * h / sqrt(mean(h^2) + eps), h = x + residual; sum_out = h in bf16 (it may be x or residual).  x, residual, sum_out:
+    bf16 [n][dim], rows any stride apart; gamma None: ones (see include/dsa.h)."""
     fn = "dsa_norm_q8"
     shape, stride = x.shape, x.stride()
     _want(fn, len(shape) == 2)
@@ -419,7 +420,7 @@ def dsa_norm_q8(x, gamma, eps, out, out_scale, residual=None, sum_out=None, stre
     dev = x.get_device()
     x_ld = stride[0] if n > 1 else dim
     residual_at = sum_at = gamma_at = None
-    ok = (x.dtype is _BF16 and (stride[1] == 1 or n == 0) and out.element_size() == 1 and out.shape == shape
+    ok = (x.dtype is _BF16 and (stride[1] == 1 or n == 0) and out.dtype in _CODES and out.shape == shape
           and out.is_contiguous() and out_scale.dtype is _F32 and out_scale.shape == (n, (dim + 127) // 128)
           and out_scale.is_contiguous() and out.get_device() == dev and out_scale.get_device() == dev)
     residual_ld = sum_ld = 0
@@ -466,7 +467,7 @@ def _gemm_q8_args(fn, a, a_scale, w, w_scale, out, out_scale, dev_status, stream
         nnb = (n + 127) // 128
         ok = lead[1] == k and w_scale.shape == (nnb, nkb)
     dev, fmt = a.get_device(), _OUT_FORMAT.get(out.dtype)
-    ok = (ok and fmt is not None and a.element_size() == 1 and w.element_size() == 1 and w.is_contiguous()
+    ok = (ok and fmt is not None and a.dtype in _CODES and w.dtype in _CODES and w.is_contiguous()
           and a_scale.dtype is _F32 and a_scale.shape == want_scale and w_scale.dtype is _F32 and w_scale.is_contiguous()
           and out.shape == ((m, groups, n) if middle else (m, n)) and a_scale.get_device() == dev and w.get_device() == dev
           and w_scale.get_device() == dev and out.get_device() == dev)
@@ -495,7 +496,7 @@ def dsa_gemm_q8(a, a_scale, w, w_scale, out, out_scale=None, dev_status=None, st
     """out[i][g] = w[g] a[i][g] for 8-bit rows a (uint8 [m][groups][k], a_scale fp32 [m][groups][ceil(k / 128)]) and weights
     w (uint8 [groups][n][k], w_scale fp32 [groups][ceil(n / 128)][ceil(k / 128)]), into out [m][groups][n] in fp32, bf16 or
     (uint8, with out_scale [m][groups][ceil(n / 128)]) 8-bit rows.  One group: the dimension may be left out everywhere.
-    (See include/dsa.h.)"""
+    Codes are uint8 or float8_e4m3fn.  (See include/dsa.h.)"""
     args, status, handle = _gemm_q8_args("dsa_gemm_q8", a, a_scale, w, w_scale, out, out_scale, dev_status, stream)
     code = _lib.dsa_gemm_q8(*args, status, handle)
     if code:
