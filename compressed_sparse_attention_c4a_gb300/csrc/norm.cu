@@ -118,24 +118,30 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, C) norm_q8_kernel(NormA
         }
         const float ss = row_sum<W>(lo_of(s2) + hi_of(s2), red[turn], warp, lane);
         turn ^= 1;
-        float rs;
-        if (ss < INFINITY) {
-            rs = 1.f / sqrtf(ss / (float)a.dim + a.eps);
-        } else {  // squares beyond fp32 (or an infinity, a NaN): the same of h 2^-80, beside which eps is nothing
-            s2 = 0ull;
+        // The norm's factor is one for the row: a block's codes are those of gamma h whatever it is, its scale has it.  Rows of
+        // huge or tiny values (an infinity, a NaN) take it first: gamma times them could leave fp32 where the norm does not.
+        float rs = 1.f / sqrtf(ss / (float)a.dim + a.eps);
+        if (!(rs > 0x1p-20f && rs < 0x1p20f)) {
+            if (!(ss < INFINITY)) {  // squares beyond fp32: those of h 2^-80, beside which eps is nothing
+                s2 = 0ull;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t u = mul2(h[i][k], pair2(0x1p-80f, 0x1p-80f));
+                        s2 = fma2(u, u, s2);
+                        h[i][k] = mul2(h[i][k], pair2(0x1p-40f, 0x1p-40f));  // the rest is rs's: small values keep their bits
+                    }
+                const float again = row_sum<W>(lo_of(s2) + hi_of(s2), red[2], warp, lane);
+                if constexpr (W > 1) __syncthreads();  // red[2] is free again
+                rs = 0x1p-40f / sqrtf(again / (float)a.dim);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    h[i][k] = mul2(h[i][k], pair2(0x1p-80f, 0x1p-80f));
-                    s2 = fma2(h[i][k], h[i][k], s2);
-                }
-            const float again = row_sum<W>(lo_of(s2) + hi_of(s2), red[2], warp, lane);
-            if constexpr (W > 1) __syncthreads();  // red[2] is free again
-            rs = 1.f / sqrtf(again / (float)a.dim);
+                for (int k = 0; k < 4; ++k) h[i][k] = mul2(h[i][k], pair2(rs, rs));
+            rs = 1.f;
         }
-        // The norm's factor is one for the row: a block's codes are those of gamma h whatever it is, its scale has it.
-        const bool plain = rs > 0x1p-60f && rs < 0x1p60f;
         uint8_t* codes = a.out + row * a.dim;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, C) norm_q8_kernel(NormA
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             float scale;
-            if (plain && amax > 0x1p-60f && amax < 0x1p60f) {
+            if (amax > 0x1p-60f && amax < 0x1p60f) {  // the scale is above 2^-89
                 const float r = 448.f * near_reciprocal(amax);
                 scale = amax * rs * (1.f / 448.f);
 #pragma unroll
