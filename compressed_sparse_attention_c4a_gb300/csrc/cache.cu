@@ -375,16 +375,18 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __
                 for (int k = 1; k < 8; ++k) s2 = fma2(v[k], v[k], s2);
                 const float ss = warp_sum(lo_of(s2) + hi_of(s2));
                 rs = rsqrtf(ss / 512.f + a.eps);
-                if (!(ss < INFINITY)) {  // squares beyond fp32: the same of the values times 2^-80, beside which eps is nothing
+                if (!(ss < INFINITY)) {  // squares beyond fp32: those of the values times 2^-80, beside which eps is nothing
                     s2 = 0ull;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        v[k] = mul2(v[k], pair2(0x1p-80f, 0x1p-80f));
-                        s2 = fma2(v[k], v[k], s2);
+                        const uint64_t w = mul2(v[k], pair2(0x1p-80f, 0x1p-80f));
+                        s2 = fma2(w, w, s2);
+                        v[k] = mul2(v[k], pair2(0x1p-40f, 0x1p-40f));  // the rest is rs's: small values keep their bits
                     }
-                    rs = rsqrtf(warp_sum(lo_of(s2) + hi_of(s2)) / 512.f);
+                    rs = 0x1p-40f * rsqrtf(warp_sum(lo_of(s2) + hi_of(s2)) / 512.f);
                 }
-                if (FP8 && !(rs > 0x1p-60f && rs < 0x1p60f)) {  // a row of huge or tiny values, an infinity or a NaN
+                // A row of huge or tiny values, an infinity or a NaN: gamma times them could leave fp32 where the norm does not
+                if (FP8 && !(rs > 0x1p-20f && rs < 0x1p20f)) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], pair2(rs, rs));
                     rs = 1.f;
@@ -426,8 +428,14 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __
 #pragma unroll
                         for (int k = 0; k < 8; ++k) v[k] = quotient(v[k]);
                     }
-                } else {  // parts of which could leave fp32's normal range
-                    scale = amax > 0.f ? amax / 448.f : 1.f;
+                } else {  // parts of which could leave fp32's normal range, the norm's factor not yet taken in
+                    if constexpr (NORM) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = mul2(v[k], pair2(rs, rs));
+                    }
+                    const float most = amax * rs;
+                    rs = 1.f;
+                    scale = most > 0.f ? most / 448.f : 1.f;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] = pair2(lo_of(v[k]) / scale, hi_of(v[k]) / scale);
                 }
@@ -486,8 +494,12 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
             if (!(ss < INFINITY)) {  // as above
                 ss = 0.f;
 #pragma unroll
-                for (int k = 0; k < E; ++k) v[k] *= 0x1p-80f, ss = fmaf(v[k], v[k], ss);
-                rs = rsqrtf(warp_sum(ss) / (float)DIM);
+                for (int k = 0; k < E; ++k) {
+                    const float w = v[k] * 0x1p-80f;
+                    ss = fmaf(w, w, ss);
+                    v[k] *= 0x1p-40f;
+                }
+                rs = 0x1p-40f * rsqrtf(warp_sum(ss) / (float)DIM);
             }
 #pragma unroll
             for (int k = 0; k < E; ++k) v[k] = v[k] * rs * g[k];
