@@ -9,6 +9,7 @@
 // A row is read once and held in registers: eight consecutive values a thread and step, so that sixteen lanes hold a block
 // and find its largest value by shuffles.  A warp takes a row of up to 1024 values, a CTA longer ones.  CTAs go from row to row,
 // the next rows on their way into shared memory, each thread waiting for the pieces that it copied itself.
+// The call has no status word: in the bounds-checked build a bad index leaves its access out, which the values show.
 #include <algorithm>
 
 #include "common.cuh"
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, C) norm_q8_kernel(NormA
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = t + i * 32 * W;
-                if (c < vecs) {
+                if (c < vecs && DSA_IDX_OK(slot * slot_vecs + (RES ? vecs : 0) + c, kNormAhead * slot_vecs, nullptr)) {
                     cp_async16_nc(smem_u32(mine + slot * slot_vecs + c), reinterpret_cast<const uint4*>(a.x + row * a.x_ld) + c, 16);
                     if constexpr (RES)
                         cp_async16_nc(smem_u32(mine + slot * slot_vecs + vecs + c),
@@ -175,9 +176,9 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, C) norm_q8_kernel(NormA
 #pragma unroll
                 for (int k = 0; k < 4; ++k) h[i][k] = q(h[i][k]);
             }
-            if (c < vecs) {
+            if (c < vecs && DSA_IDX_OK(row * vecs + c, (long long)a.n * vecs, nullptr)) {
                 reinterpret_cast<uint2*>(codes)[c] = make_uint2(e4m3x4(h[i][0], h[i][1]), e4m3x4(h[i][2], h[i][3]));
-                if ((lane & 15) == 0) a.out_scale[row * blocks + c / 16] = scale;
+                if ((lane & 15) == 0 && DSA_IDX_OK(c / 16, blocks, nullptr)) a.out_scale[row * blocks + c / 16] = scale;
             }
         }
     }
