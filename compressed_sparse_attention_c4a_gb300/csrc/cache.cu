@@ -307,10 +307,12 @@ __device__ __forceinline__ void append_places(const CacheAppendArgs& a, long lon
 // Rows of 512 into bf16 or e4m3 pools.  Lane l holds dims 128 i + 4 l .. + 3, so that the 32 pairs of the rotation lie two to
 // a lane in sixteen lanes.  The warps take the rows in turn, the next one or two of a warp's on their way into shared memory
 // while it works on one; the places of a warp's next eight rows are found by eight lanes side by side.  131,072 rows normed into
-// e4m3 (1,540 bytes each) take 39.6 us, 5.1 TB/s: bound by the issue slots (70 % busy), of about 250 instructions a row; into
-// bf16 (2,048 bytes) 45.7, 5.9 TB/s; without the norm into e4m3 36.4.  One row on its way against two: with the norm 39.6
-// against 40.3 us and, into bf16, 45.7 against 50.1, without it 42.2 against 36.4.  Two rows to a warp, sixteen lanes each, took
-// 36.6 us for the first but longer for few rows (6,000 rows 5.2 us against 4.2, 32 rows 3.0 against 2.3).
+// e4m3 (1,540 bytes each) take 40.1 us, 5.0 TB/s, into bf16 (2,048 bytes) 46.1, 5.8 TB/s, without the norm into e4m3 36.6.  What
+// bounds the first: a row is one chain (sum, factor, rotation, largest value, codes) of about 250 instructions, and 24 warps an
+// SM do not cover it: the issue slots are 70 % busy and DRAM 49 %, 45 instructions a row less (angles of consecutive rows turned
+// from the first one's) took longer, two rows to a warp, sixteen lanes each, 36.6 us against 39.6, but longer for few rows (6,000
+// rows 5.2 us against 4.2, 32 rows 3.0 against 2.3).  One row on its way against two: with the norm 39.6 against 40.3 us and,
+// into bf16, 45.7 against 50.1, without it 42.2 against 36.4.
 template <bool NORM, bool FP8>
 __global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __grid_constant__ CacheAppendArgs a) {
     constexpr int kAppendAhead = NORM ? 1 : 2;  // rows of a warp on their way
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_wide_kernel(const __
                 const float amax = __uint_as_float(warp_abs_max_bits(__float_as_uint(m)));  // (fmaxf passes over NaN)
                 float scale;
                 if (amax > 0x1p-60f && amax < 0x1p60f) {
-                    const float q = amax * (1.f / 448.f);  // amax / 448 by a reciprocal and a correction
+                    const float q = amax * (1.f / 448.f);  // amax / 448: a reciprocal, a correction by the remainder (Markstein's)
                     scale = fmaf(fmaf(-q, 448.f, amax), 1.f / 448.f, q);
                     if constexpr (NORM) {  // the values are rounded already: a product with the reciprocal is near enough
                         const float r = near_reciprocal(scale);

@@ -403,8 +403,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) gemm_q8_few_kernel(const __gri
 // products no faster than with them.  Tried, in the same runs: sixteen warps of 64 sums 920 against 812; products and barriers for
 // each half of the outputs 919; TMEM loads of 16 columns 863; two loads in flight instead of one 850 against 790; scalar FMAs 850
 // against 780; last tiles cut into halves of 128 outputs: a block of a half takes 0.9 of a whole one's time; six stages as four;
-// bands of 4, 8 or 16 row tiles alike.  Registers: 136 a thread for the first four warps and 184 for the sums spill nothing; with
-// 64 and 216 it was the first four that spilled whenever a line changed (2,048 rows x 8,192 x 4,096: 57.4 us against 62 to 86).
+// bands of 4, 8 or 16 row tiles alike.  Registers: 136 a thread for the first four warps and 184 for the sums spill nothing (SPLIT:
+// 44 bytes of stores, 84 of loads); with 64 and 216 it was the first four that spilled whenever a line changed (2,048 rows x 8,192 x
+// 4,096: 57.4 us against 62 to 86).
 constexpr int kWideThreads = 384;
 constexpr int kWideStages = 4;
 static_assert(kWideStages % 2 == 0, "a stage meets the same accumulator every round");

@@ -194,11 +194,12 @@ static cudaError_t launch_rows(const NormArgs& a, cudaStream_t st) {
     return launch_pdl(norm_q8_kernel<W, V, C, RES>, dim3((unsigned)grid), dim3(W == 1 ? 256 : 32 * W), smem, st, a);
 }
 
-// What bounds it: HBM with a residual (7 bytes a value: 8,192 rows of 8,192 in 72.2 us, 6.5 TB/s, 0.97 of the copy rate; of
-// 4,096 37.9, 16,384 of 2,048 38.9, 32,768 of 512 21.2), without one (3 bytes a value: 41.3, 23.1, 24.1) the arithmetic and a
-// row's two steps, sum and codes, one after the other.  Warps to a row, steps and CTAs an SM were chosen at these sizes: rows
-// of 8,192 with a residual by eight warps in two CTAs take 83.7 us, by sixteen in one 72.2; without one 41.3 and 51.4.  Loaded
-// into registers instead of copied ahead, the first took 106.
+// What bounds it: HBM with a residual (7 bytes a value: 8,192 rows of 8,192 in 73.1 us, 6.5 TB/s, 0.96 of the copy rate; of
+// 4,096 38.0, 16,384 of 2,048 39.3, 32,768 of 512 21.5).  Without one (3 bytes a value: 40.2, 22.9, 22.5, 12.2) neither HBM (51 %
+// at 8,192 values a row) nor the issue slots (56 %): sixteen warps an SM (their rows in 116 registers a thread) wait for shuffles
+// and shared memory (1.8 of 6.9 cycles a warp's instruction) and for results of fixed latency (1.6).  Warps to a row, steps and
+// CTAs an SM were chosen at these sizes: rows of 8,192 with a residual by eight warps in two CTAs took 83.7 us where sixteen in
+// one took 72.2; without one 41.3 and 51.4.  Loaded into registers instead of copied ahead, the first took 106.
 template <bool RES>
 static cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     if (a.dim <= 256) return launch_rows<1, 1, 4, RES>(a, st);

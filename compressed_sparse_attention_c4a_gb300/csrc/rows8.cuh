@@ -1,5 +1,4 @@
-// Rows in 8 bits: e4m3 codes with one fp32 scale per 128 consecutive values, as dsa_norm_q8, dsa_gemm_q8 and
-// dsa_sparse_attn_q8 write them.
+// Rows in 8 bits: e4m3 codes with one fp32 scale per 128 consecutive values, as dsa_norm_q8 and dsa_gemm_q8 write them.
 #pragma once
 
 #include "common.cuh"
@@ -14,7 +13,8 @@ __host__ __device__ constexpr int row_blocks(int n) { return (n + kRowBlock - 1)
 // for a block of zeros.
 __device__ __forceinline__ float block_scale8(float amax) { return amax > 0.f ? fmaxf(amax / 448.f, 0x1p-126f) : 1.f; }
 
-// v / scale as correctly rounded division gives it: a product with the reciprocal and one correction by the remainder.
+// v / scale as correctly rounded division gives it: a product with the reciprocal and one correction by the quotient's remainder
+// (Markstein's).
 // An infinite scale (a block that holds an infinity) makes 0 of finite values and NaN of infinities, as division does.
 struct BlockQuotient {
     float r, s;

@@ -246,8 +246,8 @@ class ProjectedStep(LayerStep):
         query norm;  window rows normed, rotated and appended;  indexer and top-k;  attention into 8-bit rows;  the groups'
         products, again in 8 bits;  the output projection -> self.delta (the next layer's x)
 
-    A query for each new token (decode, or a prefill chunk).  The compressors' and the indexer's raw inputs come with the
-    case, as LayerStep's.  q is written by the compressors' launch and read by the attention before it waits for the
+    A query for each new token (decode, or a prefill chunk).  The compressors' raw rows and logits and the indexer's queries, keys
+    and weights come with the case, as LayerStep's: no projection makes them here.  q is written by the compressors' launch and read by the attention before it waits for the
     kernel ahead of it, so the window rows are appended between the two.
     """
 

@@ -545,9 +545,10 @@ dsa_status_t dsa_cache_append(int32_t batch, const int32_t* cu_new, const int32_
  * 8-bit rows, as dsa_norm_q8 and dsa_gemm_q8 write them and dsa_gemm_q8 reads them: e4m3 codes and one fp32 scale for each
  * block of 128 consecutive values (the last block of a row may be shorter),
  *     scale_b = max(max |v| of the block / 448, 2^-126)  (1 for a block of zeros),    code_d = e4m3(v_d / scale_{d / 128}),
- * rounded to nearest even.  A NaN keeps a NaN code and does not count in the maximum; a block with an infinity has an infinite
- * scale, zero codes for its finite values and NaN codes for its infinities.  dsa_sparse_attn_q8's output is such rows of
- * heads * 512 values.
+ * rounded to nearest even (in fp32: a quotient within 2^-20 of the border between two codes may take either).  A NaN keeps a NaN
+ * code and does not count in the maximum; a block with an infinity has an infinite scale, zero codes for its finite values and
+ * NaN codes for its infinities.  dsa_sparse_attn_q8's output is such rows of heads * 512 values, but for the scale's lower limit,
+ * which it does not have.
  */
 
 /*
@@ -561,7 +562,8 @@ dsa_status_t dsa_cache_append(int32_t batch, const int32_t* cu_new, const int32_
  * x, residual, sum   bf16, 16-byte aligned, rows *_ld elements apart (>= dim, a multiple of 8); residual and sum may be NULL
  *            (their ld is ignored).  sum may be x or residual itself (with the same ld); outputs must not overlap inputs
  *            otherwise, nor rows of one output each other
- * gamma      [dim] fp32, 16-byte aligned, or NULL (ones);  eps > 0
+ * gamma      [dim] fp32, 16-byte aligned, or NULL (ones);  eps > 0, finite (below 2^-126 the squares of values as small as its
+ *            root lose bits)
  * out        [n][dim] e4m3 bytes, 16-byte aligned;  out_scale [n][ceil(dim / 128)] fp32
  * A row that holds a NaN is NaN codes throughout; one that holds an infinity has NaN there and zeros elsewhere.
  * Launched with programmatic dependent launch: gamma is read before waiting for the preceding kernel in the stream, so it must
